@@ -380,6 +380,44 @@ mx_status mx_grouped_mm_fwd_q_noalloc(const uint16_t* A, const uint8_t* qW, cons
                                       const int32_t* offs, int64_t M, int64_t N, int64_t K, int64_t E,
                                       uint16_t* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * MXFP4: the same 32-element blocks and E8M0 scale bytes with 4-bit E2M1
+ * elements.
+ *   scale    byte = clamp(floor(log2 amax) - 2, -127, 127) + 127 (2 is E2M1's
+ *            largest exponent); 0x00 for an all-zero block; 0xFF when the
+ *            block holds NaN or Inf;
+ *   element  E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign bit) of
+ *            value * 2^(127 - byte), rounded to nearest even, saturated to
+ *            +-6, sign kept on values that round to zero; every element of a
+ *            NaN/Inf block is code 0 (E2M1 has no NaN: the scale byte makes
+ *            the block's products NaN);
+ *   packing  two codes to a byte, the even element of the contraction axis in
+ *            bits 0..3, the odd one in bits 4..7.
+ * ------------------------------------------------------------------------ */
+
+/* 1x32 blocks along cols, as mx_quantize_rowwise.  x bf16 [batch, rows, cols]
+ * -> q [batch, rows, cols/2], s row-major [batch, rows, cols/32]
+ * (scale_layout MX_SCALES_ROWMAJOR; requires cols % 32 == 0) or in the GEMM
+ * layout [batch, cols/128, rows, 4] (MX_SCALES_GEMM; requires cols % 128 ==
+ * 0).  Fewer than 2^32 blocks. */
+mx_status mx_quantize_rowwise_fp4(const uint16_t* x, int64_t batch, int64_t rows, int64_t cols, uint8_t* q,
+                                  uint8_t* s, int scale_layout, void* stream);
+
+/* Values of MXFP4 codes: out bf16 [batch, rows, cols] of q [batch, rows,
+ * cols/2] and s in either layout.  Exact: every code * 2^(byte - 127) is a
+ * bf16 number, except the codes 4 and 6 of byte 254, which give Inf; byte 255
+ * gives NaN.  Sizes as mx_quantize_rowwise_fp4. */
+mx_status mx_dequantize_fp4(const uint8_t* q, const uint8_t* s, int64_t batch, int64_t rows, int64_t cols,
+                            int scale_layout, uint16_t* out, void* stream);
+
+/* Expert weights in both orientations from one read, as mx_quantize_weights:
+ * W [E, N, K] -> q [E, N, K/2] (blocks along K) with s in the GEMM layout
+ * [E, K/128, N, 4], and q_t [E, K, N/2] (blocks along N, stored transposed)
+ * with s_t in the GEMM layout [E, N/128, K, 4].  Requires N % 128 == 0 and
+ * K % 128 == 0.  w, q, q_t 16-byte aligned; s, s_t 4-byte aligned. */
+mx_status mx_quantize_weights_fp4(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* q, uint8_t* s,
+                                  uint8_t* q_t, uint8_t* s_t, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

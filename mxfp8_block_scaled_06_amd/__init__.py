@@ -25,6 +25,7 @@ __all__ = [
     "mx_check_offsets", "check_offsets", "mx_grouped_mm_fwd_q_noalloc", "NOALLOC_SCRATCH_BYTES",
     "mx_route", "route_capacity", "mx_quantize_dual_gather", "mx_grouped_gemm_mx_rows", "mx_routed_experts",
     "mx_topk_sum_rows", "mx_route_workspace_bytes",
+    "mx_quantize_rowwise_fp4", "mx_dequantize_fp4", "mx_quantize_weights_fp4",
 ]
 
 OP_FWD, OP_DGRAD, OP_WGRAD, OP_FWD_Q, OP_DGRAD_Q = 0, 1, 2, 3, 4
@@ -109,6 +110,12 @@ def load_library():
         f.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_sz, c_vp]
     lib.mx_grouped_mm_fwd_q_noalloc.restype = c_int
     lib.mx_grouped_mm_fwd_q_noalloc.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp]
+    lib.mx_quantize_rowwise_fp4.restype = c_int
+    lib.mx_quantize_rowwise_fp4.argtypes = [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_int, c_vp]
+    lib.mx_dequantize_fp4.restype = c_int
+    lib.mx_dequantize_fp4.argtypes = [c_vp, c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_vp]
+    lib.mx_quantize_weights_fp4.restype = c_int
+    lib.mx_quantize_weights_fp4.argtypes = lib.mx_quantize_weights.argtypes
     _lib = lib
     return lib
 
@@ -677,3 +684,87 @@ def mx_routed_experts(x, expert_idx, W, check: bool = True, weights=None, cache=
     epilogue) on the device."""
     from .autograd import mx_routed_experts as _f
     return _f(x, expert_idx, W, check, weights, cache)
+
+
+# ---------------------------------------------------------------------------
+# MXFP4 (4-bit E2M1 elements, two to a byte, E8M0 scales per 32)
+# ---------------------------------------------------------------------------
+def _scale_shape(scale_layout, lead, R, C):
+    """Shape of the scales of [*lead, R, C] values in a layout, and its code."""
+    if scale_layout == "rowmajor":
+        if C % 32:
+            raise ValueError(f"the last axis ({C}) must be a multiple of 32")
+        return (*lead, R, C // 32), SCALES_ROWMAJOR
+    if scale_layout == "gemm":
+        if C % 128:
+            raise ValueError(f"the last axis ({C}) must be a multiple of 128 for scales in the GEMM layout")
+        return (*lead, C // 128, R, 4), SCALES_GEMM
+    raise ValueError("scale_layout must be 'gemm' or 'rowmajor'")
+
+
+def _same_device(first, *rest):
+    """Every tensor on the device of the first one (the kernels run there)."""
+    for t in rest:
+        if t.device != first.device:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+
+
+def mx_quantize_rowwise_fp4(x, q=None, s=None, scale_layout: str = "rowmajor"):
+    """MXFP4 of x bf16 [B?, R, C] in 1x32 blocks along the last axis: q uint8
+    [B?, R, C/2] (two codes to a byte, the even column in the low four bits)
+    and s uint8 [B?, R, C/32], or [B?, C/128, R, 4] with scale_layout="gemm"
+    (an operand of mx_grouped_gemm_mxfp4 as it stands)."""
+    import torch
+    lib = load_library()
+    _require(x, torch.bfloat16, "x")
+    B, R, C = _as3d(x)
+    s_shape, layout = _scale_shape(scale_layout, x.shape[:-2], R, C)
+    q = _out(q, (*x.shape[:-1], C // 2), torch.uint8, x.device, "q")
+    s = _out(s, s_shape, torch.uint8, x.device, "s")
+    with torch.cuda.device(x.device):
+        _check("mx_quantize_rowwise_fp4",
+               lib.mx_quantize_rowwise_fp4(_ptr(x), B, R, C, _ptr(q), _ptr(s), layout, _stream(x.device)))
+    return q, s
+
+
+def mx_dequantize_fp4(q, s, scale_layout: str = "rowmajor", out=None):
+    """The values of MXFP4 codes, bf16 [B?, R, C], from q uint8 [B?, R, C/2]
+    and s in either layout.  Exact (a NaN/Inf block's scale byte 255 gives
+    NaN)."""
+    import torch
+    lib = load_library()
+    _require(q, torch.uint8, "q")
+    _require(s, torch.uint8, "s")
+    B, R, C = _as3d(q)
+    C *= 2
+    s_shape, layout = _scale_shape(scale_layout, q.shape[:-2], R, C)
+    if tuple(s.shape) != s_shape:
+        raise ValueError(f"s must have shape {s_shape} for codes {tuple(q.shape)}, got {tuple(s.shape)}")
+    _same_device(q, s)
+    out = _out(out, (*q.shape[:-1], C), torch.bfloat16, q.device, "out")
+    with torch.cuda.device(q.device):
+        _check("mx_dequantize_fp4",
+               lib.mx_dequantize_fp4(_ptr(q), _ptr(s), B, R, C, layout, _ptr(out), _stream(q.device)))
+    return out
+
+
+def mx_quantize_weights_fp4(W, q=None, s=None, q_t=None, s_t=None):
+    """MXFP4 of W bf16 [E, N, K] in both orientations from one read:
+    (q [E, N, K/2], s [E, K/128, N, 4], q_t [E, K, N/2], s_t [E, N/128, K, 4]),
+    blocks along K and along N, scales in the GEMM layout.  N and K must be
+    multiples of 128."""
+    import torch
+    lib = load_library()
+    _require(W, torch.bfloat16, "W")
+    if W.dim() != 3:
+        raise ValueError("W must be [E, N, K]")
+    E, N, K = W.shape
+    dev = W.device
+    q = _out(q, (E, N, K // 2), torch.uint8, dev, "q")
+    s = _out(s, (E, K // 128, N, 4), torch.uint8, dev, "s")
+    q_t = _out(q_t, (E, K, N // 2), torch.uint8, dev, "q_t")
+    s_t = _out(s_t, (E, N // 128, K, 4), torch.uint8, dev, "s_t")
+    with torch.cuda.device(dev):
+        _check("mx_quantize_weights_fp4", lib.mx_quantize_weights_fp4(_ptr(W), E, N, K, _ptr(q), _ptr(s), _ptr(q_t),
+                                                                      _ptr(s_t), _stream(dev)))
+    return q, s, q_t, s_t

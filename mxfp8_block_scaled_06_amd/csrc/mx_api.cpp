@@ -543,3 +543,62 @@ mx_status mx_quantize_rowwise_gather(const uint16_t* x, int64_t src_rows, const 
 }
 
 }  // extern "C"
+
+namespace {
+
+// Checks shared by the MXFP4 quantizer and dequantizer: x holds the bf16
+// values, q the codes.
+mx_status check_fp4(const char* fn, const void* x, int64_t batch, int64_t rows, int64_t cols, const void* q,
+                    const void* s, int scale_layout) {
+  if (scale_layout != MX_SCALES_ROWMAJOR && scale_layout != MX_SCALES_GEMM)
+    return fail(MX_ERR_LAYOUT, "%s: unknown scale layout %d (MX_SCALES_ROWMAJOR = %d, MX_SCALES_GEMM = %d)", fn,
+                scale_layout, (int)MX_SCALES_ROWMAJOR, (int)MX_SCALES_GEMM);
+  mx_status st = check_quant(fn, x, batch, rows, cols, q, s, 1, scale_layout == MX_SCALES_GEMM ? 128 : 32);
+  if (st != MX_OK || rows == 0 || cols == 0) return st;
+  // batch * rows * (cols/32) < 2^32, without overflow on the way
+  const int64_t most = ((int64_t)1 << 32) - 1;
+  if (batch > most || rows > most || cols / 32 > most || batch * rows > most || batch * rows > most / (cols / 32))
+    return fail(MX_ERR_SHAPE, "%s: batch*rows*cols/32 must be below 2^32 blocks", fn);
+  return MX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_quantize_rowwise_fp4(const uint16_t* x, int64_t batch, int64_t rows, int64_t cols, uint8_t* q,
+                                  uint8_t* s, int scale_layout, void* stream) {
+  const char* fn = "mx_quantize_rowwise_fp4";
+  const mx_status st = check_fp4(fn, x, batch, rows, cols, q, s, scale_layout);
+  if (st != MX_OK || rows == 0 || cols == 0) return st;
+  return hip_status(mxk::launch_quant_rowwise_fp4(x, batch * rows, cols, q, s,
+                                                  scale_layout == MX_SCALES_GEMM ? rows : 0, (hipStream_t)stream),
+                    fn);
+}
+
+mx_status mx_dequantize_fp4(const uint8_t* q, const uint8_t* s, int64_t batch, int64_t rows, int64_t cols,
+                            int scale_layout, uint16_t* out, void* stream) {
+  const char* fn = "mx_dequantize_fp4";
+  const mx_status st = check_fp4(fn, out, batch, rows, cols, q, s, scale_layout);
+  if (st != MX_OK || rows == 0 || cols == 0) return st;
+  return hip_status(mxk::launch_dequant_fp4(q, s, batch * rows, cols, out, scale_layout == MX_SCALES_GEMM ? rows : 0,
+                                            (hipStream_t)stream),
+                    fn);
+}
+
+mx_status mx_quantize_weights_fp4(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* q, uint8_t* s,
+                                  uint8_t* q_t, uint8_t* s_t, void* stream) {
+  const char* fn = "mx_quantize_weights_fp4";
+  if (E < 1 || N < 0 || K < 0)
+    return fail(MX_ERR_SHAPE, "%s: E=%lld N=%lld K=%lld", fn, (long long)E, (long long)N, (long long)K);
+  if (N % 128 != 0 || K % 128 != 0)
+    return fail(MX_ERR_SHAPE, "%s: N=%lld and K=%lld must be multiples of 128", fn, (long long)N, (long long)K);
+  if (N == 0 || K == 0) return MX_OK;
+  if (N / 256 >= 65535 || K / 256 >= 65535 || E > 65535) return fail(MX_ERR_SHAPE, "%s: too large for one launch", fn);
+  if (!w || !q || !s || !q_t || !s_t) return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(w, 16) || !aligned(q, 16) || !aligned(q_t, 16) || !aligned(s, 4) || !aligned(s_t, 4))
+    return fail(MX_ERR_ALIGN, "%s: w, q, q_t must be 16-byte and s, s_t 4-byte aligned", fn);
+  return hip_status(mxk::launch_quant_weights_fp4(w, E, N, K, q, s, q_t, s_t, (hipStream_t)stream), fn);
+}
+
+}  // extern "C"

@@ -68,6 +68,15 @@ hipError_t launch_check_offsets(const int32_t* offs, int64_t E, int64_t M, int a
                                 hipStream_t st);
 size_t gemm_lds_bytes();
 
+// MXFP4 (mx_fp4.hip).  Scales row-major when gemm_rows_per_batch == 0, else in
+// the GEMM layout with that many rows per batch entry.
+hipError_t launch_quant_rowwise_fp4(const uint16_t* x, int64_t rows_total, int64_t cols, uint8_t* q, uint8_t* s,
+                                    int64_t gemm_rows_per_batch, hipStream_t st);
+hipError_t launch_dequant_fp4(const uint8_t* q, const uint8_t* s, int64_t rows_total, int64_t cols, uint16_t* out,
+                              int64_t gemm_rows_per_batch, hipStream_t st);
+hipError_t launch_quant_weights_fp4(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* q, uint8_t* s,
+                                    uint8_t* q_t, uint8_t* s_t, hipStream_t st);
+
 constexpr int kMaxExperts = 1024;
 
 // Record `text` as the calling thread's mx_last_error() and return `st`.

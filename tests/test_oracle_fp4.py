@@ -1,0 +1,80 @@
+"""The MXFP4 oracle against hand-worked blocks, the refusals of the MXFP4
+entry points (host-side checks, no kernel is launched) and of their binding."""
+
+import numpy as np
+import pytest
+
+import mxfp8_block_scaled_06_amd as mx
+from mxfp8_block_scaled_06_amd import inputs as inp
+from oracle import mxfp4
+from test_abi import FAKE, _err, _lib
+
+
+def _bits(values):
+    return inp.f32_to_bf16_bits(np.asarray(values, dtype=np.float32))
+
+
+def test_element_codes_by_hand():
+    # every magnitude, every midpoint (ties to the even code) and saturation
+    y = [0, .25, .5, .75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 7.9, .26, .74, 2.51, 3.49, 4.99, 5.01]
+    want = [0, 0, 1, 2, 2, 2, 3, 4, 4, 4, 5, 6, 6, 6, 7, 7, 1, 1, 5, 5, 6, 7]
+    assert mxfp4.e2m1_encode(np.array(y)).tolist() == want
+    assert mxfp4.e2m1_encode(-np.array(y)).tolist() == [w + 8 for w in want]
+    assert mxfp4.e2m1_decode(np.arange(16)).tolist() == [0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6]
+
+
+def test_blocks_by_hand():
+    x = np.zeros((1, 4 * 32), dtype=np.float32)
+    x[0, 32:36] = [7.0, -1.0, 0.5, -0.125]        # amax 7: exponent 2, byte 127: 7 saturates to 6, -0.125 rounds to -0
+    x[0, 64] = 2.0 ** -120                        # exponent -122 would be -122: byte 5, code 4 = 6
+    x[0, 96] = np.inf
+    x[0, 97] = 1.0
+    q, s = mxfp4.quantize_rowwise_fp4(_bits(x))
+    assert s.tolist() == [[0, 127, 5, 255]]
+    assert q[0, 16:18].tolist() == [0x7 | 0xA << 4, 0x1 | 0x8 << 4]
+    assert q[0, 32] == 6 and not q[0, 48:].any() and not q[0, :16].any()
+    v = mxfp4.dequant_rowwise_fp4(q, s)
+    assert v[0, 32:36].tolist() == [6.0, -1.0, 0.5, -0.0] and v[0, 64] == 2.0 ** -120 and np.isnan(v[0, 96:]).all()
+
+
+def test_quantizer_refusals():
+    lib = _lib()
+    R, G = mx.SCALES_ROWMAJOR, mx.SCALES_GEMM
+    q = lib.mx_quantize_rowwise_fp4
+    d = lambda x, b, r, c, qq, s, lay, st: lib.mx_dequantize_fp4(qq, s, b, r, c, lay, x, st)  # noqa: E731
+    for f in (q, d):
+        assert f(FAKE, 1, 4, 48, FAKE, FAKE, R, None) == 2
+        assert "multiple of 32" in _err(lib)
+        assert f(FAKE, 1, 4, 96, FAKE, FAKE, G, None) == 2
+        assert "multiple of 128" in _err(lib)
+        assert f(FAKE, 1, 4, 96, FAKE, FAKE, 2, None) == 6
+        assert f(FAKE, 0, 4, 64, FAKE, FAKE, R, None) == 2
+        assert f(FAKE, 1, -4, 64, FAKE, FAKE, R, None) == 2
+        assert f(None, 1, 4, 64, FAKE, FAKE, R, None) == 1
+        assert f(FAKE, 1, 4, 64, FAKE, None, R, None) == 1
+        assert f(FAKE + 8, 1, 4, 64, FAKE, FAKE, R, None) == 3
+        assert f(FAKE, 1, 4, 64, FAKE + 4, FAKE, R, None) == 3
+        assert f(FAKE, 4, 1 << 25, 1024, FAKE, FAKE, R, None) == 2
+        assert "2^32" in _err(lib)
+        assert f(FAKE, 1 << 40, 1 << 40, 1024, FAKE, FAKE, R, None) == 2
+        assert f(None, 1, 0, 64, None, None, R, None) == 0
+    w = lib.mx_quantize_weights_fp4
+    assert w(FAKE, 2, 256, 200, FAKE, FAKE, FAKE, FAKE, None) == 2
+    assert w(FAKE, 2, 96, 256, FAKE, FAKE, FAKE, FAKE, None) == 2
+    assert w(FAKE, 0, 128, 128, FAKE, FAKE, FAKE, FAKE, None) == 2
+    assert w(FAKE, 1, 128, 128, FAKE, FAKE, None, FAKE, None) == 1
+    assert w(FAKE, 1, 128, 128, FAKE, FAKE + 2, FAKE, FAKE, None) == 3
+    assert w(None, 1, 0, 128, None, None, None, None, None) == 0
+
+
+def test_binding_refusals():
+    import torch
+    _lib()
+    with pytest.raises(ValueError, match="GPU tensor"):
+        mx.mx_quantize_rowwise_fp4(torch.zeros((4, 64), dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="multiple of 32"):
+        mx._scale_shape("rowmajor", (), 4, 48)
+    with pytest.raises(ValueError, match="multiple of 128"):
+        mx._scale_shape("gemm", (), 4, 96)
+    with pytest.raises(ValueError, match="scale_layout"):
+        mx._scale_shape("blocked", (), 4, 96)
