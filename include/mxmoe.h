@@ -418,6 +418,41 @@ mx_status mx_dequantize_fp4(const uint8_t* q, const uint8_t* s, int64_t batch, i
 mx_status mx_quantize_weights_fp4(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* q, uint8_t* s,
                                   uint8_t* q_t, uint8_t* s_t, void* stream);
 
+/* Element format of the activations in the products below (the weights are
+ * MXFP4): E4M3 codes, one per byte, or E2M1 codes, two per byte. */
+#define MX_FMT_FP8 0
+#define MX_FMT_FP4 1
+
+/* The rows-grouped GEMM with MXFP4 weights:
+ *   C[i, j] = sum_k X[i, k] * Y[e][j, k] * 2^(sX[i, k/32] + sY[e][j, k/32] - 254)
+ * for the rows i of expert e (offs: int32 [E] cumulative END offsets on the
+ * device, any group sizes), accumulated in fp32.  X [I, Kc] in x_format
+ * (Kc or Kc/2 bytes a row), sX [Kc/128, I, 4]; Y [E, J, Kc/2], sY [E, Kc/128,
+ * J, 4], scales in the GEMM layout.  row_map NULL: C [I, J] (c_rows is not
+ * read); else row i goes to C row row_map[i] when that lies in [0, c_rows) and
+ * is dropped otherwise, and C rows that no entry names are left as they were.
+ * C is bf16 (rounded to nearest even), or float with out_f32 != 0.  Rows past
+ * offs[E-1] are not written.  Requires Kc % 128 == 0, Kc >= 128 (or I or J
+ * zero), Kc <= 2^23, J % 8 == 0, 1 <= E <= 1024. */
+mx_status mx_grouped_gemm_mxfp4(const uint8_t* X, const uint8_t* sX, int x_format, const uint8_t* Y,
+                                const uint8_t* sY, int scale_layout, const int32_t* offs, int64_t I, int64_t J,
+                                int64_t Kc, int64_t E, const int32_t* row_map, int64_t c_rows, void* C, int out_f32,
+                                void* stream);
+
+/* mx_grouped_mm_fwd_q / _dgrad_q with MXFP4 weights, (q, s) respectively
+ * (q_t, s_t) of mx_quantize_weights_fp4; the activations are quantized to
+ * act_format in the workspace.  fwd requires K % 128 == 0 and N % 8 == 0,
+ * dgrad N % 128 == 0 and K % 8 == 0.  ws: mx_grouped_mm_fp4_workspace_bytes
+ * of M rows and C contraction elements (K for fwd, N for dgrad), 256-byte
+ * aligned; 0 for sizes or a format that the call refuses. */
+size_t mx_grouped_mm_fp4_workspace_bytes(int64_t M, int64_t C, int act_format);
+mx_status mx_grouped_mm_fwd_fp4(const uint16_t* A, const uint8_t* qW, const uint8_t* sW, const int32_t* offs,
+                                int64_t M, int64_t N, int64_t K, int64_t E, int act_format, uint16_t* out, void* ws,
+                                size_t ws_bytes, void* stream);
+mx_status mx_grouped_mm_dgrad_fp4(const uint16_t* dOut, const uint8_t* qWt, const uint8_t* sWt, const int32_t* offs,
+                                  int64_t M, int64_t N, int64_t K, int64_t E, int act_format, uint16_t* dA, void* ws,
+                                  size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

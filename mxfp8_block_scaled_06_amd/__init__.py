@@ -26,10 +26,12 @@ __all__ = [
     "mx_route", "route_capacity", "mx_quantize_dual_gather", "mx_grouped_gemm_mx_rows", "mx_routed_experts",
     "mx_topk_sum_rows", "mx_route_workspace_bytes",
     "mx_quantize_rowwise_fp4", "mx_dequantize_fp4", "mx_quantize_weights_fp4",
+    "mx_grouped_gemm_mxfp4", "mx_grouped_mm_fwd_fp4", "mx_grouped_mm_dgrad_fp4", "mx_grouped_mm_fp4_workspace_bytes",
 ]
 
 OP_FWD, OP_DGRAD, OP_WGRAD, OP_FWD_Q, OP_DGRAD_Q = 0, 1, 2, 3, 4
 SCALES_ROWMAJOR, SCALES_GEMM = 0, 1
+FORMATS = {"mxfp8": 0, "mxfp4": 1}    # MX_FMT_FP8, MX_FMT_FP4
 OFFS_DECREASING, OFFS_RANGE, OFFS_LAST, OFFS_ALIGN = 1, 2, 4, 8
 NOALLOC_SCRATCH_BYTES = 128 << 20     # MX_NOALLOC_SCRATCH_BYTES of include/mxmoe.h
 _STATUS = {0: "MX_OK", 1: "MX_ERR_NULL", 2: "MX_ERR_SHAPE", 3: "MX_ERR_ALIGN", 4: "MX_ERR_WORKSPACE",
@@ -116,6 +118,15 @@ def load_library():
     lib.mx_dequantize_fp4.argtypes = [c_vp, c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_vp]
     lib.mx_quantize_weights_fp4.restype = c_int
     lib.mx_quantize_weights_fp4.argtypes = lib.mx_quantize_weights.argtypes
+    lib.mx_grouped_gemm_mxfp4.restype = c_int
+    lib.mx_grouped_gemm_mxfp4.argtypes = [c_vp, c_vp, c_int, c_vp, c_vp, c_int, c_vp, c_i64, c_i64, c_i64, c_i64, c_vp,
+                                          c_i64, c_vp, c_int, c_vp]
+    lib.mx_grouped_mm_fp4_workspace_bytes.restype = c_sz
+    lib.mx_grouped_mm_fp4_workspace_bytes.argtypes = [c_i64, c_i64, c_int]
+    for name in ("mx_grouped_mm_fwd_fp4", "mx_grouped_mm_dgrad_fp4"):
+        f = getattr(lib, name)
+        f.restype = c_int
+        f.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_sz, c_vp]
     _lib = lib
     return lib
 
@@ -768,3 +779,110 @@ def mx_quantize_weights_fp4(W, q=None, s=None, q_t=None, s_t=None):
         _check("mx_quantize_weights_fp4", lib.mx_quantize_weights_fp4(_ptr(W), E, N, K, _ptr(q), _ptr(s), _ptr(q_t),
                                                                       _ptr(s_t), _stream(dev)))
     return q, s, q_t, s_t
+
+
+def _format(fmt, name):
+    if fmt not in FORMATS:
+        raise ValueError(f"{name} must be 'mxfp8' or 'mxfp4', got {fmt!r}")
+    return FORMATS[fmt]
+
+
+def mx_grouped_gemm_mxfp4(X, sX, Y, sY, offs, x_format: str = "mxfp8", row_map=None, c_rows: Optional[int] = None,
+                          out=None, out_dtype=None):
+    """C[i,j] = sum_k X[i,k] Y[e][j,k] 2^(sX+sY-254) over the rows i of expert
+    e, with MXFP4 weights Y uint8 [E, J, Kc/2] and X uint8 [I, Kc] (x_format
+    "mxfp8") or [I, Kc/2] ("mxfp4"); scales in the GEMM layout, sX [Kc/128, I,
+    4] and sY [E, Kc/128, J, 4]; offs int32 [E] END offsets of the groups (any
+    sizes; rows past the last group are not written).  out bf16, or fp32 with
+    out_dtype=torch.float32: [I, J], or with row_map (int32 [I]) [c_rows, J],
+    row i stored at row_map[i], as mx_grouped_gemm_mx_rows."""
+    import torch
+    lib = load_library()
+    fmt = _format(x_format, "x_format")
+    for t, n in ((X, "X"), (sX, "sX"), (Y, "Y"), (sY, "sY")):
+        _require(t, torch.uint8, n)
+    _require(offs, torch.int32, "offs")
+    if X.dim() != 2 or Y.dim() != 3:
+        raise ValueError("X must be [I, Kc] codes and Y [E, J, Kc/2]")
+    E, J, Kc = Y.shape[0], Y.shape[1], 2 * Y.shape[2]
+    I = X.shape[0]
+    if X.shape[1] != (Kc if fmt == 0 else Kc // 2):
+        raise ValueError(f"{x_format} rows of X must hold {Kc if fmt == 0 else Kc // 2} bytes for Kc={Kc}, got "
+                         f"{X.shape[1]}")
+    _offs(offs, E)
+    for t, want, n in ((sX, (Kc // 128, I, 4), "sX"), (sY, (E, Kc // 128, J, 4), "sY")):
+        if tuple(t.shape) != want:
+            raise ValueError(f"{n} must be in the GEMM scale layout {want}, got {tuple(t.shape)}")
+    _same_device(X, sX, Y, sY, offs)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    if row_map is None:
+        if c_rows is not None:
+            raise ValueError("c_rows goes with row_map")
+        c_rows = I
+    else:
+        _require(row_map, torch.int32, "row_map")
+        _same_device(X, row_map)
+        if tuple(row_map.shape) != (I,):
+            raise ValueError(f"row_map must be int32 [{I}] (one entry per row of X), got {tuple(row_map.shape)}")
+        if c_rows is None:
+            c_rows = out.shape[0] if out is not None else I
+    if out is None and row_map is not None:
+        out = torch.zeros((c_rows, J), dtype=out_dtype, device=X.device)
+    out = _out(out, (c_rows, J), out_dtype, X.device, "out")
+    with torch.cuda.device(X.device):
+        _check("mx_grouped_gemm_mxfp4",
+               lib.mx_grouped_gemm_mxfp4(_ptr(X), _ptr(sX), fmt, _ptr(Y), _ptr(sY), SCALES_GEMM, _ptr(offs), I, J, Kc,
+                                         E, _ptr(row_map), int(c_rows), _ptr(out), int(out_dtype == torch.float32),
+                                         _stream(X.device)))
+    return out
+
+
+def mx_grouped_mm_fp4_workspace_bytes(M: int, C: int, act_format: str = "mxfp8") -> int:
+    return int(load_library().mx_grouped_mm_fp4_workspace_bytes(int(M), int(C), _format(act_format, "act_format")))
+
+
+def _mm_fp4(name, a, q, s, offs, act_format, out, ws):
+    import torch
+    lib = load_library()
+    fmt = _format(act_format, "act_format")
+    _require(a, torch.bfloat16, "A" if name == "mx_grouped_mm_fwd_fp4" else "dOut")
+    _require(q, torch.uint8, "weight codes")
+    _require(s, torch.uint8, "weight scales")
+    if a.dim() != 2 or q.dim() != 3:
+        raise ValueError("activations must be [M, C] and weight codes [E, J, C/2]")
+    M, C = a.shape
+    E, J, C2 = q.shape
+    if 2 * C2 != C:
+        raise ValueError(f"the activations contract over {C} elements but the weight codes over {2 * C2}")
+    _offs(offs, E)
+    if C % 128 or tuple(s.shape) != (E, C // 128, J, 4):
+        raise ValueError(f"weight scales must be in the GEMM scale layout {(E, C // 128, J, 4)} (contraction a "
+                         f"multiple of 128), got {tuple(s.shape)}")
+    _same_device(a, q, s, offs)
+    out = _out(out, (M, J), torch.bfloat16, a.device, "out")
+    need = mx_grouped_mm_fp4_workspace_bytes(M, C, act_format)
+    if ws is None:
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=a.device)
+    _require(ws, torch.uint8, "ws")
+    _same_device(a, ws)
+    sizes = (M, J, C) if name == "mx_grouped_mm_fwd_fp4" else (M, C, J)
+    with torch.cuda.device(a.device):
+        _check(name, getattr(lib, name)(_ptr(a), _ptr(q), _ptr(s), _ptr(offs), *sizes, E, fmt, _ptr(out), _ptr(ws),
+                                        ws.numel(), _stream(a.device)))
+    return out
+
+
+def mx_grouped_mm_fwd_fp4(A, qW, sW, offs, act_format: str = "mxfp8", out=None, ws=None):
+    """out [M, N] = A [M, K] @ W[e]^T per expert group, W given as (q, s) of
+    mx_quantize_weights_fp4 (qW uint8 [E, N, K/2], sW [E, K/128, N, 4]); A bf16
+    is quantized to act_format ("mxfp8" or "mxfp4") on the way."""
+    return _mm_fp4("mx_grouped_mm_fwd_fp4", A, qW, sW, offs, act_format, out, ws)
+
+
+def mx_grouped_mm_dgrad_fp4(dOut, qWt, sWt, offs, act_format: str = "mxfp8", out=None, ws=None):
+    """dA [M, K] = dOut [M, N] @ W[e] per expert group, W given as (q_t, s_t)
+    of mx_quantize_weights_fp4 (qWt uint8 [E, K, N/2], sWt [E, N/128, K, 4])."""
+    return _mm_fp4("mx_grouped_mm_dgrad_fp4", dOut, qWt, sWt, offs, act_format, out, ws)

@@ -601,4 +601,109 @@ mx_status mx_quantize_weights_fp4(const uint16_t* w, int64_t E, int64_t N, int64
   return hip_status(mxk::launch_quant_weights_fp4(w, E, N, K, q, s, q_t, s_t, (hipStream_t)stream), fn);
 }
 
+mx_status mx_grouped_gemm_mxfp4(const uint8_t* X, const uint8_t* sX, int x_format, const uint8_t* Y,
+                                const uint8_t* sY, int scale_layout, const int32_t* offs, int64_t I, int64_t J,
+                                int64_t Kc, int64_t E, const int32_t* row_map, int64_t c_rows, void* C, int out_f32,
+                                void* stream) {
+  const char* fn = "mx_grouped_gemm_mxfp4";
+  if (scale_layout != MX_SCALES_GEMM)
+    return fail(MX_ERR_LAYOUT, "%s: scales must be in the GEMM layout [K/128][rows][4] (MX_SCALES_GEMM = %d, got %d)",
+                fn, (int)MX_SCALES_GEMM, scale_layout);
+  if (x_format != MX_FMT_FP8 && x_format != MX_FMT_FP4)
+    return fail(MX_ERR_SHAPE, "%s: x_format must be MX_FMT_FP8 = %d or MX_FMT_FP4 = %d (got %d)", fn, MX_FMT_FP8,
+                MX_FMT_FP4, x_format);
+  if (I < 0 || J < 0 || Kc < 0) return fail(MX_ERR_SHAPE, "%s: negative size", fn);
+  if (E < 1 || E > mxk::kMaxExperts)
+    return fail(MX_ERR_SHAPE, "%s: number of experts E=%lld outside [1, %d]", fn, (long long)E, mxk::kMaxExperts);
+  if (Kc % 128 != 0 || J % 8 != 0)
+    return fail(MX_ERR_SHAPE, "%s: Kc=%lld must be a multiple of 128 and J=%lld of 8", fn, (long long)Kc, (long long)J);
+  if (Kc > ((int64_t)1 << 23) || I >= ((int64_t)1 << 31) || J >= ((int64_t)1 << 31))
+    return fail(MX_ERR_SHAPE, "%s: too large (I=%lld J=%lld Kc=%lld; Kc <= 2^23)", fn, (long long)I, (long long)J,
+                (long long)Kc);
+  if (row_map && (c_rows < 0 || c_rows >= ((int64_t)1 << 31)))
+    return fail(MX_ERR_SHAPE, "%s: c_rows=%lld outside [0, 2^31)", fn, (long long)c_rows);
+  if (I == 0 || J == 0 || (row_map && c_rows == 0)) return MX_OK;
+  if (Kc == 0) return fail(MX_ERR_SHAPE, "%s: no contraction (Kc=0)", fn);
+  if (!X || !sX || !Y || !sY || !offs || !C) return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(C, 16) || !aligned(sX, 4) || !aligned(sY, 4) ||
+      !aligned(offs, 4) || !aligned(row_map, 4))
+    return fail(MX_ERR_ALIGN, "%s: X, Y, C must be 16-byte and scales, offsets and row_map 4-byte aligned", fn);
+  // one workgroup per tile: at most 2^31 - 1 of them
+  if ((I / 64 + E + 1) * (J / 32 + 1) >= ((int64_t)1 << 30))
+    return fail(MX_ERR_SHAPE, "%s: too many output tiles for one launch", fn);
+  mxk::Fp4GemmArgs a{};
+  a.X = X;
+  a.sX = sX;
+  a.Y = Y;
+  a.sY = sY;
+  a.offs = offs;
+  a.row_map = row_map;
+  a.C = C;
+  a.I = I;
+  a.J = J;
+  a.Kc = Kc;
+  a.c_rows = row_map ? c_rows : I;
+  a.E = (int)E;
+  a.x_fp4 = x_format == MX_FMT_FP4;
+  a.out_f32 = out_f32 != 0;
+  return hip_status(mxk::launch_fp4_gemm(a, (hipStream_t)stream), fn);
+}
+
+size_t mx_grouped_mm_fp4_workspace_bytes(int64_t M, int64_t C, int act_format) {
+  if (M < 0 || C < 0 || C % 128 != 0 || (act_format != MX_FMT_FP8 && act_format != MX_FMT_FP4)) return 0;
+  if (C > ((int64_t)1 << 23) || M >= ((int64_t)1 << 31)) return 0;
+  return align_up((size_t)M * (size_t)(act_format == MX_FMT_FP4 ? C / 2 : C), 256) +
+         align_up((size_t)M * (size_t)(C / 32), 256);
+}
+
+}  // extern "C"
+
+namespace {
+
+// out [M, J] = quantized a [M, C] times the MXFP4 weights [E, J, C/2].
+mx_status mm_fp4(const char* fn, const char* c_name, const char* j_name, const uint16_t* a, const uint8_t* q,
+                 const uint8_t* s, const int32_t* offs, int64_t M, int64_t J, int64_t C, int64_t E, int act_format,
+                 uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+  mx_status st = check_mm(fn, a, q, offs, out, M, J, C, E);
+  if (st != MX_OK) return st;
+  if (!s) return fail(MX_ERR_NULL, "%s: null weight scales", fn);
+  if (act_format != MX_FMT_FP8 && act_format != MX_FMT_FP4)
+    return fail(MX_ERR_SHAPE, "%s: act_format must be MX_FMT_FP8 = %d or MX_FMT_FP4 = %d (got %d)", fn, MX_FMT_FP8,
+                MX_FMT_FP4, act_format);
+  if (C % 128 != 0) return fail(MX_ERR_SHAPE, "%s: %s=%lld is not a multiple of 128", fn, c_name, (long long)C);
+  if (J % 8 != 0) return fail(MX_ERR_SHAPE, "%s: %s=%lld is not a multiple of 8", fn, j_name, (long long)J);
+  if (C > ((int64_t)1 << 23) || M >= ((int64_t)1 << 31) || !rowwise_blocks_fit(M, C))
+    return fail(MX_ERR_SHAPE, "%s: too large (M=%lld %s=%lld)", fn, (long long)M, c_name, (long long)C);
+  const size_t need = mx_grouped_mm_fp4_workspace_bytes(M, C, act_format);
+  if (!ws || ws_bytes < need)
+    return fail(MX_ERR_WORKSPACE, "%s: workspace of %zu bytes at %p, need %zu", fn, ws_bytes, ws, need);
+  if (!aligned(ws, 256)) return fail(MX_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
+  if (M == 0 || J == 0) return MX_OK;
+  if (C == 0) return fail(MX_ERR_SHAPE, "%s: no contraction (%s=0)", fn, c_name);
+  uint8_t* qa = (uint8_t*)ws;
+  uint8_t* sa = qa + align_up((size_t)M * (size_t)(act_format == MX_FMT_FP4 ? C / 2 : C), 256);
+  const hipStream_t hs = (hipStream_t)stream;
+  st = hip_status(act_format == MX_FMT_FP4 ? mxk::launch_quant_rowwise_fp4(a, M, C, qa, sa, M, hs)
+                                           : mxk::launch_quant_rowwise(a, M, C, qa, sa, M, hs), fn);
+  if (st != MX_OK) return st;
+  return mx_grouped_gemm_mxfp4(qa, sa, act_format, q, s, MX_SCALES_GEMM, offs, M, J, C, E, nullptr, 0, out, 0, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_grouped_mm_fwd_fp4(const uint16_t* A, const uint8_t* qW, const uint8_t* sW, const int32_t* offs,
+                                int64_t M, int64_t N, int64_t K, int64_t E, int act_format, uint16_t* out, void* ws,
+                                size_t ws_bytes, void* stream) {
+  return mm_fp4("mx_grouped_mm_fwd_fp4", "K", "N", A, qW, sW, offs, M, N, K, E, act_format, out, ws, ws_bytes, stream);
+}
+
+mx_status mx_grouped_mm_dgrad_fp4(const uint16_t* dOut, const uint8_t* qWt, const uint8_t* sWt, const int32_t* offs,
+                                  int64_t M, int64_t N, int64_t K, int64_t E, int act_format, uint16_t* dA, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  return mm_fp4("mx_grouped_mm_dgrad_fp4", "N", "K", dOut, qWt, sWt, offs, M, K, N, E, act_format, dA, ws, ws_bytes,
+                stream);
+}
+
 }  // extern "C"

@@ -74,6 +74,19 @@ hipError_t launch_quant_rowwise_fp4(const uint16_t* x, int64_t rows_total, int64
                                     int64_t gemm_rows_per_batch, hipStream_t st);
 hipError_t launch_dequant_fp4(const uint8_t* q, const uint8_t* s, int64_t rows_total, int64_t cols, uint16_t* out,
                               int64_t gemm_rows_per_batch, hipStream_t st);
+// Rows-grouped product with MXFP4 weights (see mx_fp4_gemm.hip).
+struct Fp4GemmArgs {
+  const uint8_t* X;           // [I, Kc] E4M3, or [I, Kc/2] E2M1 with x_fp4
+  const uint8_t* sX;          // [Kc/128, I, 4]
+  const uint8_t* Y;           // [E, J, Kc/2] E2M1
+  const uint8_t* sY;          // [E, Kc/128, J, 4]
+  const int32_t* offs;
+  const int32_t* row_map;     // optional: row i goes to C row row_map[i] (dropped outside [0, c_rows))
+  void* C;                    // [c_rows, J] bf16 or fp32
+  int64_t I, J, Kc, c_rows;
+  int E, x_fp4, out_f32;
+};
+hipError_t launch_fp4_gemm(const Fp4GemmArgs& a, hipStream_t st);
 hipError_t launch_quant_weights_fp4(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* q, uint8_t* s,
                                     uint8_t* q_t, uint8_t* s_t, hipStream_t st);
 

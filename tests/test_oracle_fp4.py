@@ -78,3 +78,46 @@ def test_binding_refusals():
         mx._scale_shape("gemm", (), 4, 96)
     with pytest.raises(ValueError, match="scale_layout"):
         mx._scale_shape("blocked", (), 4, 96)
+
+
+def test_product_refusals():
+    lib = _lib()
+    g = lib.mx_grouped_gemm_mxfp4
+    G = mx.SCALES_GEMM
+
+    def call(X=FAKE, xf=0, Y=FAKE, lay=G, offs=FAKE, I=64, J=64, Kc=256, E=2, rm=None, cr=0, C=FAKE):
+        return g(X, FAKE, xf, Y, FAKE, lay, offs, I, J, Kc, E, rm, cr, C, 0, None)
+
+    assert call(lay=mx.SCALES_ROWMAJOR) == 6
+    assert call(xf=2) == 2 and "x_format" in _err(lib)
+    assert call(Kc=192) == 2 and call(Kc=0) == 2 and call(J=60) == 2 and call(I=-1) == 2
+    assert call(E=0) == 2 and call(E=1025) == 2 and call(Kc=(1 << 23) + 128) == 2
+    assert call(I=(1 << 31) - 1, J=1 << 20) == 2 and "tiles" in _err(lib)
+    assert call(Y=None) == 1 and call(C=None) == 1 and call(offs=None) == 1
+    assert call(X=FAKE + 8) == 3 and call(rm=FAKE + 2, cr=5) == 3
+    assert call(rm=FAKE, cr=-1) == 2
+    assert call(I=0) == 0 and call(J=0) == 0 and call(rm=FAKE, cr=0) == 0
+    ws = lib.mx_grouped_mm_fp4_workspace_bytes
+    assert ws(100, 256, 0) >= 100 * 264 > ws(100, 256, 1) >= 100 * 136
+    assert ws(-1, 256, 0) == 0 and ws(100, 192, 0) == 0 and ws(100, 256, 2) == 0
+    f, d = lib.mx_grouped_mm_fwd_fp4, lib.mx_grouped_mm_dgrad_fp4
+    need = ws(256, 256, 0)
+    assert f(FAKE, FAKE, FAKE, FAKE, 256, 512, 256, 2, 0, FAKE, FAKE, need - 1, None) == 4
+    assert f(FAKE, FAKE, None, FAKE, 256, 512, 256, 2, 0, FAKE, FAKE, need, None) == 1
+    assert f(FAKE, FAKE, FAKE, FAKE, 256, 512, 192, 2, 0, FAKE, FAKE, 1 << 40, None) == 2
+    assert f(FAKE, FAKE, FAKE, FAKE, 256, 516, 256, 2, 0, FAKE, FAKE, 1 << 40, None) == 2
+    assert f(FAKE, FAKE, FAKE, FAKE, 256, 512, 256, 2, 3, FAKE, FAKE, 1 << 40, None) == 2
+    assert f(FAKE, FAKE, FAKE, FAKE, 256, 512, 256, 2, 0, FAKE, FAKE + 16, 1 << 40, None) == 3
+    assert d(FAKE, FAKE, FAKE, FAKE, 256, 192, 256, 2, 0, FAKE, FAKE, 1 << 40, None) == 2
+
+
+def test_product_binding_refusals():
+    import torch
+    _lib()
+    with pytest.raises(ValueError, match="x_format"):
+        mx.mx_grouped_gemm_mxfp4(*[None] * 5, x_format="fp4")
+    with pytest.raises(ValueError, match="GPU tensor"):
+        u8 = torch.zeros((4, 128), dtype=torch.uint8)
+        mx.mx_grouped_gemm_mxfp4(u8, u8, u8, u8, u8)
+    with pytest.raises(ValueError, match="act_format"):
+        mx.mx_grouped_mm_fwd_fp4(*[None] * 4, act_format="bf16")
