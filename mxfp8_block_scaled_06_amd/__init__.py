@@ -589,17 +589,18 @@ def mx_grouped_mm_fwd_q_noalloc(A, qW, sW, offs, out):
     return out
 
 
-def mx_grouped_mm(A, W, offs, check_offsets: bool = True, weights=None, cache=None):
+def mx_grouped_mm(A, W, offs, check_offsets: bool = True, weights=None, cache=None, weight_format: str = "mxfp8"):
     """Differentiable MXFP8 grouped GEMM (forward, dgrad, wgrad in the library's kernels);
-    expert weights quantized once and cached across micro-batches until they change."""
+    expert weights quantized once and cached across micro-batches until they change.
+    weight_format="mxfp4": 4-bit weights, quantized in every call unless `weights` or a `cache` is given."""
     from .autograd import mx_grouped_mm as _f
-    return _f(A, W, offs, check_offsets, weights, cache)
+    return _f(A, W, offs, check_offsets, weights, cache, weight_format)
 
 
-def mx_linear(x, weight):
+def mx_linear(x, weight, weight_format: str = "mxfp8"):
     """Differentiable dense MXFP8 linear y = x @ weight^T (one expert of mx_grouped_mm)."""
     from .autograd import mx_linear as _f
-    return _f(x, weight)
+    return _f(x, weight, weight_format)
 
 
 def mx_quantize_rowwise_gather(x, rows, q=None, s=None):
@@ -687,14 +688,14 @@ def mx_quantize_dual_gather(x, rows, topk: int = 1, ldq: Optional[int] = None, q
     return q, s, q_t, s_t
 
 
-def mx_routed_experts(x, expert_idx, W, check: bool = True, weights=None, cache=None):
+def mx_routed_experts(x, expert_idx, W, check: bool = True, weights=None, cache=None, weight_format: str = "mxfp8"):
     """Differentiable routed experts: out[t] = x[t] @ W[expert_idx[t]]^T for a
     top-1 router (expert_idx [T]), out[t, j] = x[t] @ W[expert_idx[t, j]]^T for
     a top-k router (expert_idx [T, k]), with the grouping, the token gather
     (inside the quantizer) and the scatter back to item order (inside the GEMM
     epilogue) on the device."""
     from .autograd import mx_routed_experts as _f
-    return _f(x, expert_idx, W, check, weights, cache)
+    return _f(x, expert_idx, W, check, weights, cache, weight_format)
 
 
 # ---------------------------------------------------------------------------
