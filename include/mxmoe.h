@@ -453,6 +453,35 @@ mx_status mx_grouped_mm_dgrad_fp4(const uint16_t* dOut, const uint8_t* qWt, cons
                                   int64_t M, int64_t N, int64_t K, int64_t E, int act_format, uint16_t* dA, void* ws,
                                   size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A whole gated MoE layer for a few tokens (decoding), in two kernels:
+ *   g, u   = MX8(x[t]) W13[e]^T        gate rows 0..N-1, up rows N..2N-1
+ *   h      = MX8(silu(g) * u)
+ *   out[t] = bf16(sum_j combine[t, j] * (h W2[e]^T)),   e = expert_idx[t, j]
+ * MX8 is the MXFP8 quantization in 1x32 blocks along the contraction
+ * (mx_quantize_rowwise), of h taken from its fp32 values; sums are fp32, the
+ * sum over a token's slots is rounded once, and the order of additions is
+ * fixed.  x bf16 [T, K], expert_idx int32 and combine float [T, topk], W13
+ * [E, 2N, K] as (q13, s13) and W2 [E, K, N] as (q2, s2): codes in w_format
+ * (MX_FMT_FP8: mx_quantize_weights, or MX_FMT_FP4: mx_quantize_weights_fp4),
+ * scales in the GEMM layout; out bf16 [T, K].
+ * A slot whose id lies outside [0, E) adds nothing (a token with no other
+ * slot gets a row of zeros); status, if not NULL, is set to 1 when there is
+ * one, else to 0 (T = 0 enqueues nothing and leaves it).  An expert named twice by a token counts with the sum of
+ * the two combine weights.
+ * Requires 0 <= T <= MX_MOE_MAX_TOKENS, 1 <= topk <= MX_MOE_MAX_TOPK, K and N
+ * multiples of 128 in [128, 2^20], 1 <= E <= 1024; x, codes, out 16-byte and
+ * the rest 4-byte aligned.  Larger batches go through mx_route and the
+ * grouped GEMMs.  ws: mx_moe_few_tokens_workspace_bytes, 256-byte aligned,
+ * the caller's, one per call in flight; needs no initialisation. */
+#define MX_MOE_MAX_TOKENS 128
+#define MX_MOE_MAX_TOPK 32
+size_t mx_moe_few_tokens_workspace_bytes(int64_t T, int64_t topk, int64_t N);
+mx_status mx_moe_few_tokens(const uint16_t* x, const int32_t* expert_idx, const float* combine, const uint8_t* q13,
+                            const uint8_t* s13, const uint8_t* q2, const uint8_t* s2, int w_format, int64_t T,
+                            int64_t topk, int64_t K, int64_t N, int64_t E, uint16_t* out, int32_t* status, void* ws,
+                            size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,10 +27,12 @@ __all__ = [
     "mx_topk_sum_rows", "mx_route_workspace_bytes",
     "mx_quantize_rowwise_fp4", "mx_dequantize_fp4", "mx_quantize_weights_fp4",
     "mx_grouped_gemm_mxfp4", "mx_grouped_mm_fwd_fp4", "mx_grouped_mm_dgrad_fp4", "mx_grouped_mm_fp4_workspace_bytes",
+    "mx_moe_few_tokens", "mx_moe_few_tokens_workspace_bytes", "MOE_MAX_TOKENS", "MOE_MAX_TOPK",
 ]
 
 OP_FWD, OP_DGRAD, OP_WGRAD, OP_FWD_Q, OP_DGRAD_Q = 0, 1, 2, 3, 4
 SCALES_ROWMAJOR, SCALES_GEMM = 0, 1
+MOE_MAX_TOKENS, MOE_MAX_TOPK = 128, 32     # MX_MOE_MAX_TOKENS, MX_MOE_MAX_TOPK
 FORMATS = {"mxfp8": 0, "mxfp4": 1}    # MX_FMT_FP8, MX_FMT_FP4
 OFFS_DECREASING, OFFS_RANGE, OFFS_LAST, OFFS_ALIGN = 1, 2, 4, 8
 NOALLOC_SCRATCH_BYTES = 128 << 20     # MX_NOALLOC_SCRATCH_BYTES of include/mxmoe.h
@@ -127,6 +129,11 @@ def load_library():
         f = getattr(lib, name)
         f.restype = c_int
         f.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_sz, c_vp]
+    lib.mx_moe_few_tokens_workspace_bytes.restype = c_sz
+    lib.mx_moe_few_tokens_workspace_bytes.argtypes = [c_i64, c_i64, c_i64]
+    lib.mx_moe_few_tokens.restype = c_int
+    lib.mx_moe_few_tokens.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_i64,
+                                      c_i64, c_vp, c_vp, c_vp, c_sz, c_vp]
     _lib = lib
     return lib
 
@@ -887,3 +894,72 @@ def mx_grouped_mm_dgrad_fp4(dOut, qWt, sWt, offs, act_format: str = "mxfp8", out
     """dA [M, K] = dOut [M, N] @ W[e] per expert group, W given as (q_t, s_t)
     of mx_quantize_weights_fp4 (qWt uint8 [E, K, N/2], sWt [E, N/128, K, 4])."""
     return _mm_fp4("mx_grouped_mm_dgrad_fp4", dOut, qWt, sWt, offs, act_format, out, ws)
+
+
+# ---------------------------------------------------------------------------
+# A whole MoE layer for a few tokens
+# ---------------------------------------------------------------------------
+def mx_moe_few_tokens_workspace_bytes(T: int, topk: int, N: int) -> int:
+    return int(load_library().mx_moe_few_tokens_workspace_bytes(int(T), int(topk), int(N)))
+
+
+def mx_moe_few_tokens(x, expert_idx, combine, w13, w2, weight_format: str = "mxfp4", check: bool = True, out=None,
+                      ws=None):
+    """A gated MoE layer for up to MOE_MAX_TOKENS tokens (decoding):
+        out[t] = sum_j combine[t, j] * (silu(g) * u) @ W2[e]^T,
+        g, u = x[t] @ W13[e]^T split in halves,  e = expert_idx[t, j].
+    x bf16 [T, K]; expert_idx int32 and combine fp32, [T] or [T, k] (k up to
+    MOE_MAX_TOPK); w13 = (q, s) of the gate and up weights [E, 2N, K] (gate rows
+    first) and w2 = (q, s) of the down weights [E, K, N], the first two results
+    of mx_quantize_weights_fp4 (weight_format "mxfp4") or mx_quantize_weights
+    ("mxfp8").  K and N multiples of 128.  x and silu(g) * u are quantized to
+    MXFP8 in the kernels; sums are fp32, rounded once.  Returns bf16 [T, K].
+
+    check=True reads the routing status (one synchronization) and raises on an
+    expert id outside [0, E); with check=False such slots add nothing.  `ws`:
+    uint8 scratch of mx_moe_few_tokens_workspace_bytes(T, k, N) bytes, 256-byte
+    aligned (allocated when None), not shared by calls that overlap.  With
+    check=False, `out` and `ws` given, nothing is allocated or synchronized.
+    There is no backward: inputs that require a gradient are refused."""
+    import torch
+    lib = load_library()
+    fmt = _format(weight_format, "weight_format")
+    _require(x, torch.bfloat16, "x")
+    _require(expert_idx, torch.int32, "expert_idx")
+    _require(combine, torch.float32, "combine")
+    if torch.is_grad_enabled() and (x.requires_grad or combine.requires_grad):
+        raise ValueError("mx_moe_few_tokens has no backward: call it under torch.no_grad(), or train through "
+                         "mx_routed_experts")
+    (q13, s13), (q2, s2) = w13, w2
+    for t, n in ((q13, "w13 codes"), (s13, "w13 scales"), (q2, "w2 codes"), (s2, "w2 scales")):
+        _require(t, torch.uint8, n)
+    if x.dim() != 2 or q13.dim() != 3:
+        raise ValueError("x must be [T, K] and the codes of w13 [E, 2N, K]")
+    T, K = x.shape
+    if expert_idx.dim() not in (1, 2) or expert_idx.shape[0] != T or expert_idx.shape != combine.shape:
+        raise ValueError(f"expert_idx and combine must both be [T={T}] or [T={T}, k], got {tuple(expert_idx.shape)} "
+                         f"and {tuple(combine.shape)}")
+    topk = 1 if expert_idx.dim() == 1 else expert_idx.shape[1]
+    E, N = q13.shape[0], q13.shape[1] // 2
+    per = 2 if fmt else 1
+    for t, want, n in ((q13, (E, 2 * N, K // per), "w13 codes"), (s13, (E, K // 128, 2 * N, 4), "w13 scales"),
+                       (q2, (E, K, N // per), "w2 codes"), (s2, (E, N // 128, K, 4), "w2 scales")):
+        if tuple(t.shape) != want:
+            raise ValueError(f"{n} must be {want} in {weight_format}, got {tuple(t.shape)}")
+    _same_device(x, expert_idx, combine, q13, s13, q2, s2)
+    dev = x.device
+    out = _out(out, (T, K), torch.bfloat16, dev, "out")
+    if ws is None:
+        ws = torch.empty(max(mx_moe_few_tokens_workspace_bytes(T, topk, N), 1), dtype=torch.uint8, device=dev)
+    else:
+        _require(ws, torch.uint8, "ws")
+        _same_device(x, ws)
+    status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
+    with torch.cuda.device(dev):
+        _check("mx_moe_few_tokens",
+               lib.mx_moe_few_tokens(_ptr(x), _ptr(expert_idx), _ptr(combine), _ptr(q13), _ptr(s13), _ptr(q2),
+                                     _ptr(s2), fmt, T, topk, K, N, E, _ptr(out), _ptr(status), _ptr(ws), ws.numel(),
+                                     _stream(dev)))
+    if check and int(status.item()):
+        raise ValueError(f"mx_moe_few_tokens: an expert id lies outside [0, {E})")
+    return out

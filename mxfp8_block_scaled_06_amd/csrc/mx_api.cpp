@@ -707,3 +707,62 @@ mx_status mx_grouped_mm_dgrad_fp4(const uint16_t* dOut, const uint8_t* qWt, cons
 }
 
 }  // extern "C"
+
+extern "C" {
+
+size_t mx_moe_few_tokens_workspace_bytes(int64_t T, int64_t topk, int64_t N) {
+  if (T < 0 || T > MX_MOE_MAX_TOKENS || topk < 1 || topk > MX_MOE_MAX_TOPK) return 0;
+  if (N < 128 || N % 128 != 0 || N > ((int64_t)1 << 20)) return 0;
+  return align_up((size_t)(T * topk * N), 256) + align_up((size_t)(T * topk * (N / 32)), 256);
+}
+
+mx_status mx_moe_few_tokens(const uint16_t* x, const int32_t* expert_idx, const float* combine, const uint8_t* q13,
+                            const uint8_t* s13, const uint8_t* q2, const uint8_t* s2, int w_format, int64_t T,
+                            int64_t topk, int64_t K, int64_t N, int64_t E, uint16_t* out, int32_t* status, void* ws,
+                            size_t ws_bytes, void* stream) {
+  const char* fn = "mx_moe_few_tokens";
+  if (w_format != MX_FMT_FP8 && w_format != MX_FMT_FP4)
+    return fail(MX_ERR_SHAPE, "%s: w_format must be MX_FMT_FP8 = %d or MX_FMT_FP4 = %d (got %d)", fn, MX_FMT_FP8,
+                MX_FMT_FP4, w_format);
+  if (T < 0 || T > MX_MOE_MAX_TOKENS)
+    return fail(MX_ERR_SHAPE, "%s: T=%lld outside [0, %d] (larger batches: mx_route and the grouped GEMMs)", fn,
+                (long long)T, MX_MOE_MAX_TOKENS);
+  if (topk < 1 || topk > MX_MOE_MAX_TOPK)
+    return fail(MX_ERR_SHAPE, "%s: topk=%lld outside [1, %d]", fn, (long long)topk, MX_MOE_MAX_TOPK);
+  if (E < 1 || E > mxk::kMaxExperts)
+    return fail(MX_ERR_SHAPE, "%s: number of experts E=%lld outside [1, %d]", fn, (long long)E, mxk::kMaxExperts);
+  if (K < 128 || N < 128 || K % 128 != 0 || N % 128 != 0 || K > ((int64_t)1 << 20) || N > ((int64_t)1 << 20))
+    return fail(MX_ERR_SHAPE, "%s: K=%lld and N=%lld must be multiples of 128 in [128, 2^20]", fn, (long long)K,
+                (long long)N);
+  if (T == 0) return MX_OK;
+  if (!x || !expert_idx || !combine || !q13 || !s13 || !q2 || !s2 || !out)
+    return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(x, 16) || !aligned(q13, 16) || !aligned(q2, 16) || !aligned(out, 16) || !aligned(expert_idx, 4) ||
+      !aligned(combine, 4) || !aligned(s13, 4) || !aligned(s2, 4) || !aligned(status, 4))
+    return fail(MX_ERR_ALIGN, "%s: x, codes and out must be 16-byte, the other tensors 4-byte aligned", fn);
+  const size_t need = mx_moe_few_tokens_workspace_bytes(T, topk, N);
+  if (!ws || ws_bytes < need)
+    return fail(MX_ERR_WORKSPACE, "%s: workspace of %zu bytes at %p, need %zu", fn, ws_bytes, ws, need);
+  if (!aligned(ws, 256)) return fail(MX_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
+  mxk::MoeArgs a{};
+  a.x = x;
+  a.ids = expert_idx;
+  a.combine = combine;
+  a.q13 = q13;
+  a.s13 = s13;
+  a.q2 = q2;
+  a.s2 = s2;
+  a.h = (uint8_t*)ws;
+  a.hs = a.h + align_up((size_t)(T * topk * N), 256);
+  a.out = out;
+  a.status = status;
+  a.K = K;
+  a.N = N;
+  a.T = (int)T;
+  a.topk = (int)topk;
+  a.E = (int)E;
+  a.w_fp4 = w_format == MX_FMT_FP4;
+  return hip_status(mxk::launch_moe_few_tokens(a, (hipStream_t)stream), fn);
+}
+
+}  // extern "C"

@@ -92,6 +92,25 @@ hipError_t launch_quant_weights_fp4(const uint16_t* w, int64_t E, int64_t N, int
 
 constexpr int kMaxExperts = 1024;
 
+// Gated MoE layer for a few tokens (see mx_moe.hip).
+constexpr int kMoeMaxTokens = MX_MOE_MAX_TOKENS, kMoeMaxTopk = MX_MOE_MAX_TOPK;
+struct MoeArgs {
+  const uint16_t* x;          // bf16 [T, K]
+  const int32_t* ids;         // [T, topk]
+  const float* combine;       // [T, topk]
+  const uint8_t* q13;         // [E, 2N, K] E4M3 or [E, 2N, K/2] E2M1
+  const uint8_t* s13;         // [E, K/128, 2N, 4]
+  const uint8_t* q2;          // [E, K, N] or [E, K, N/2]
+  const uint8_t* s2;          // [E, N/128, K, 4]
+  uint8_t* h;                 // [T * topk, N] E4M3
+  uint8_t* hs;                // [T * topk, N/32]
+  uint16_t* out;              // bf16 [T, K]
+  int32_t* status;            // optional: 1 when an id lies outside [0, E), else 0
+  int64_t K, N;
+  int T, topk, E, w_fp4;
+};
+hipError_t launch_moe_few_tokens(const MoeArgs& a, hipStream_t st);
+
 // Record `text` as the calling thread's mx_last_error() and return `st`.
 mx_status set_last_error(mx_status st, const char* text);
 

@@ -121,3 +121,40 @@ def test_product_binding_refusals():
         mx.mx_grouped_gemm_mxfp4(u8, u8, u8, u8, u8)
     with pytest.raises(ValueError, match="act_format"):
         mx.mx_grouped_mm_fwd_fp4(*[None] * 4, act_format="bf16")
+
+
+def test_moe_refusals():
+    lib = _lib()
+    need = lib.mx_moe_few_tokens_workspace_bytes(8, 2, 256)
+    assert need >= 16 * 264 and need % 256 == 0
+    assert lib.mx_moe_few_tokens_workspace_bytes(129, 2, 256) == 0
+    assert lib.mx_moe_few_tokens_workspace_bytes(8, 33, 256) == 0
+    assert lib.mx_moe_few_tokens_workspace_bytes(8, 2, 192) == 0
+
+    def call(x=FAKE, ids=FAKE, c=FAKE, q=FAKE, s=FAKE, wf=1, T=8, k=2, K=256, N=256, E=4, out=FAKE, st=None, ws=FAKE,
+             nb=need):
+        return lib.mx_moe_few_tokens(x, ids, c, q, s, q, s, wf, T, k, K, N, E, out, st, ws, nb, None)
+
+    assert call(wf=2) == 2
+    assert call(T=129) == 2 and "grouped GEMMs" in _err(lib)
+    assert call(T=-1) == 2 and call(k=0) == 2 and call(k=33) == 2 and call(E=0) == 2 and call(E=1025) == 2
+    assert call(K=192) == 2 and call(N=0) == 2 and call(K=(1 << 20) + 128) == 2
+    for name in ("x", "ids", "c", "q", "s", "out"):
+        assert call(**{name: None}) == 1, name
+    assert call(x=FAKE + 8) == 3 and call(q=FAKE + 8) == 3 and call(out=FAKE + 8) == 3 and call(ids=FAKE + 2) == 3
+    assert call(st=FAKE + 2) == 3 and call(ws=FAKE + 16) == 3
+    assert call(nb=need - 1) == 4 and call(ws=None) == 4
+    assert call(x=None, T=0) == 0
+
+
+def test_moe_oracle_by_hand():
+    """One token, one expert, values that every format holds: g = 2, u = 3 in
+    every row, h = MX8(silu(2) * 3), out = combine * N * h."""
+    from oracle import moe
+    K = N = 128
+    x = _bits(np.concatenate([[1.0], np.zeros(K - 1)]))[None]
+    w13 = np.zeros((1, 2 * N, K))
+    w13[0, :N, 0], w13[0, N:, 0] = 2.0, 3.0
+    out, tol = moe.moe_layer(x, np.array([[0]]), np.array([[0.5]], dtype=np.float32), w13, np.ones((1, K, N)), 0.0)
+    h = 2 / (1 + np.exp(-2.0)) * 3                    # 5.28: on the grid of halves, 5.5 (step 0.5 in [4, 8))
+    assert abs(h - 5.28) < 0.01 and np.allclose(out, 0.5 * N * 5.5) and (tol < 3).all()
