@@ -14,6 +14,8 @@
 // 4g .. 4g+3.  (32x32x64: l%32, g = l/32, pieces g and g+2, rows
 // 8(r/4) + 4g + r%4.)  Y is the first operand, so a lane holds runs of four
 // output columns of one output row.
+#include <type_traits>
+
 #include "mx_device.h"
 #include "mx_kernels.h"
 #include "mx_rows_tiles.h"
@@ -113,17 +115,338 @@ __global__ __launch_bounds__(kSmWaves * 64) void fp4_rows_small_kernel(Fp4GemmAr
   }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows per expert: 256 x 256 output tiles, 8 waves (two per SIMD) of
+// 128 x 64, 128 fp32 accumulators per lane.  A stage is 128 contraction
+// elements; its codes and scales move from memory into LDS by direct loads
+// (no registers between), kBufs stages deep.  Waves 0..3, one per SIMD, issue
+// all of the loads, so that a wave held up by a full address queue leaves its
+// SIMD's matrix core to the other one; waves 4..7 only read LDS and multiply.
+// A stage has two 64-element windows.  Each wave reads the next window's
+// fragments while the current one's matrix instructions run, and there is one
+// barrier per stage, at the start of its second window: by then every wave has
+// the stage's last fragments in registers, so its buffer can take the stage
+// kBufs later, and the next stage has landed.
+// ---------------------------------------------------------------------------
+typedef __attribute__((address_space(3))) void lds_ptr;
+
+constexpr int kBM = 256, kBN = 256, kThreads = 512;
+constexpr int kOutPitch = kBN * 2 + 16;        // bytes per staged bf16 output row (+16: spreads banks)
+
+template <int XF>
+struct Stage {
+  static constexpr int kXRow = XF == kFmtE4M3 ? 128 : 64, kYRow = 64;   // code bytes per row
+  static constexpr int kX = kBM * kXRow, kY = kBN * kYRow, kScale = 256 * 4;
+  static constexpr int kBytes = kX + kY + 2 * kScale;
+  // the deepest that fits in 160 KiB with the epilogue's tile inside it
+  static constexpr int kBufs = XF == kFmtE4M3 ? 3 : 4;
+  static constexpr int kXLoads = kX / 4096, kYLoads = kY / 4096;        // one-KiB loads per loading wave
+  static constexpr int kLoads = kXLoads + kYLoads + 2;                  // and the scales of its 64 rows, twice 256 B
+};
+static_assert(kBM * kOutPitch <= Stage<kFmtE4M3>::kBytes * 3 && kBM * kOutPitch <= Stage<kFmtE2M1>::kBytes * 4, "epilogue");
+
+// 16-byte slot of a piece in its LDS row: the lanes that read one logical
+// piece of consecutive rows spread over all banks (rows of 128 or 64 bytes).
+template <int ROW>
+__device__ __forceinline__ int swz(int row) {
+  return ROW == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+}
+
+// One stage's loads: descriptors and the LDS buffer.
+struct Dma {
+  __amdgpu_buffer_rsrc_t rx, ry, rsx, rsy;
+  uint8_t* st;
+};
+
+struct Frag {
+  v8i v;
+  int s;      // the row's scale dword, shifted so that bytes 0 and 2 are this lane's blocks of windows 0 and 1
+};
+
+template <int M, int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (M < N) {
+    f(std::integral_constant<int, M>{});
+    static_for<M + 1, N>(f);
+  }
+}
+
+template <int XF, bool OUT_F32>
+__global__ __launch_bounds__(kThreads, 1) void fp4_rows_kernel(Fp4GemmArgs a) {
+  using S = Stage<XF>;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  int* s_offs = (int*)smem;
+  const rows::Tile t = rows::find_tile<kBM, kBN, kThreads>(a.offs, a.E, a.I, a.J, s_offs, s_offs + kMaxExperts,
+                                                           s_offs + 2 * kMaxExperts);
+  if (!t.valid) return;
+  __syncthreads();      // the scheduler's arrays make room for the first stages
+  const int tid = threadIdx.x, lane = tid & 63, wv = rows::uni32(tid >> 6);
+  const int iw = wv >> 2, jw = wv & 3;        // the wave's 128 x 64 block
+  const int half = lane >> 5, l32 = lane & 31;
+  const int e = rows::uni32(t.e);
+  const int64_t i0 = rows::uni64(t.i0), i_end = rows::uni64(t.i_end), j0 = rows::uni64(t.j0);
+  const int rows_x = (int)min((int64_t)kBM, i_end - i0), rows_y = (int)min((int64_t)kBN, a.J - j0);
+  const int ns = (int)(a.Kc / 128);
+  const int64_t ldx = XF == kFmtE4M3 ? a.Kc : a.Kc / 2, ldy = a.Kc / 2;
+  const uint8_t* xb = a.X + i0 * ldx;
+  const uint8_t* yb = a.Y + ((int64_t)e * a.J + j0) * ldy;
+  const uint8_t* sxb = a.sX + i0 * 4;
+  const uint8_t* syb = a.sY + (int64_t)e * a.J * (a.Kc / 32) + j0 * 4;
+
+  // this lane's part of a one-KiB load: rows of 128 bytes (8 lanes each) or 64
+  constexpr int kXLanes = S::kXRow / 16, kYLanes = S::kYRow / 16;
+  const int lw = wv & 3;
+  int xoff, yoff;      // byte offsets of load 0; load u is u * (64 / lanes per row) rows on, same slot
+  {
+    const int xr = lw * 64 + lane / kXLanes, yr = lw * 64 + lane / kYLanes;
+    xoff = xr * (int)ldx + (((lane % kXLanes) ^ swz<S::kXRow>(xr)) << 4);
+    yoff = yr * (int)ldy + (((lane % kYLanes) ^ swz<S::kYRow>(yr)) << 4);
+  }
+  // 128-byte rows: load u covers rows 8u.., whose swizzle repeats every 16 rows
+  const int xoff1 = XF == kFmtE4M3
+                        ? (lw * 64 + 8 + lane / kXLanes) * (int)ldx +
+                              (((lane % kXLanes) ^ swz<S::kXRow>(lw * 64 + 8 + lane / kXLanes)) << 4)
+                        : 0;
+  // Stages at or past ns get empty ranges: no data moves, but the loads are
+  // issued, so that the counts that the waits go by are the same throughout.
+  auto make_dma = [&](int buf, int kt) __attribute__((always_inline)) {
+    Dma d;
+    d.st = smem + buf * S::kBytes;
+    const bool live = kt < ns;
+    const int64_t kx = (int64_t)kt * S::kXRow, ky = (int64_t)kt * S::kYRow;
+    d.rx = rows::rsrc(xb + kx, live ? rows_x * ldx - kx : 0);
+    d.ry = rows::rsrc(yb + ky, live ? rows_y * ldy - ky : 0);
+    d.rsx = rows::rsrc(sxb + (int64_t)kt * a.I * 4, live ? (a.I - i0) * 4 : 0);
+    d.rsy = rows::rsrc(syb + (int64_t)kt * a.J * 4, live ? (a.J - j0) * 4 : 0);
+    return d;
+  };
+  auto issue = [&](auto nc, const Dma& d) __attribute__((always_inline)) {
+    constexpr int n = decltype(nc)::value;
+    if constexpr (n < S::kXLoads) {
+      const int vo = XF == kFmtE4M3 ? ((n & 1) ? xoff1 : xoff) + (n >> 1) * 16 * (int)ldx : xoff + n * 16 * (int)ldx;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(d.rx, (lds_ptr*)(d.st + (lw * S::kXLoads + n) * 1024), 16, vo, 0, 0, 0);
+    } else if constexpr (n < S::kXLoads + S::kYLoads) {
+      constexpr int u = n - S::kXLoads;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(d.ry, (lds_ptr*)(d.st + S::kX + (lw * S::kYLoads + u) * 1024), 16,
+                                               yoff + u * 16 * (int)ldy, 0, 0, 0);
+    } else if constexpr (n == S::kXLoads + S::kYLoads) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(d.rsx, (lds_ptr*)(d.st + S::kX + S::kY + lw * 256), 4,
+                                               (lw * 64 + lane) * 4, 0, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(d.rsy, (lds_ptr*)(d.st + S::kX + S::kY + S::kScale + lw * 256), 4,
+                                               (lw * 64 + lane) * 4, 0, 0, 0);
+    }
+  };
+
+  v16f acc[2][4];
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[y][x] = (v16f){};
+
+  // this lane's fragment addresses inside a stage (the swizzle goes by l32 alone)
+  const int xrow = iw * 128 + l32, yrow = jw * 64 + l32;
+  int xo[2][2], yo[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    yo[w] = S::kX + yrow * S::kYRow + (((2 * w + half) ^ swz<S::kYRow>(l32)) << 4);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      xo[w][c] = xrow * S::kXRow +
+                 (((XF == kFmtE4M3 ? 4 * w + half + 2 * c : 2 * w + half) ^ swz<S::kXRow>(l32)) << 4);
+  }
+  const int sxo = S::kX + S::kY + xrow * 4, syo = S::kX + S::kY + S::kScale + yrow * 4;
+  auto read_x = [&](const uint8_t* st, int w, int sub, Frag& f) __attribute__((always_inline)) {
+    const v4i p = *(const v4i*)(st + xo[w][0] + sub * 32 * S::kXRow);
+    if (XF == kFmtE4M3) {
+      const v4i q = *(const v4i*)(st + xo[w][1] + sub * 32 * S::kXRow);
+      f.v = (v8i){p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
+    } else {
+      f.v = __builtin_shufflevector(p, p, 0, 1, 2, 3, -1, -1, -1, -1);
+    }
+    if (w == 0) f.s = *(const int*)(st + sxo + sub * 32 * 4) >> (8 * half);
+  };
+  auto read_y = [&](const uint8_t* st, int w, int sub, Frag& f) __attribute__((always_inline)) {
+    const v4i p = *(const v4i*)(st + yo[w] + sub * 32 * S::kYRow);
+    f.v = __builtin_shufflevector(p, p, 0, 1, 2, 3, -1, -1, -1, -1);
+    if (w == 0) f.s = *(const int*)(st + syo + sub * 32 * 4) >> (8 * half);
+  };
+
+  // X sub-tiles qx = 0..3 in FX[0..2] and FX[3 + window] (the last one alternates
+  // so that its refill does not wait for the window's last instruction), Y
+  // sub-tiles in FY[window].
+  Frag FX[5], FY[2][2];
+  auto window = [&](auto w_c, auto nxs_c, auto loads_c, const uint8_t* src, const Dma& pend)
+                    __attribute__((always_inline)) {
+    constexpr int W = decltype(w_c)::value, NW = W ^ 1, NXS = decltype(nxs_c)::value;
+    constexpr bool LOADS = decltype(loads_c)::value;
+    static_for<0, 8>([&](auto mc) {
+      constexpr int m = decltype(mc)::value, qx = m >> 1, qy = m & 1, xi = qx < 3 ? qx : 3 + W;
+      if constexpr (qx < NXS)
+        acc[qy][qx] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(FY[W][qy].v, FX[xi].v, acc[qy][qx], kFmtE2M1, XF,
+                                                                      2 * W, FY[W][qy].s, 2 * W, FX[xi].s);
+      if constexpr (LOADS) {
+        // spread over the window's instructions
+        constexpr int lo = m * S::kLoads / 8, hi = (m + 1) * S::kLoads / 8;
+        static_for<lo, hi>([&](auto nc) { issue(nc, pend); });
+      }
+      if constexpr (NXS > 0) {
+        if constexpr (m < 2) {
+          read_y(src, NW, m, FY[NW][m]);
+          if constexpr (W == 0) FY[NW][m].s = FY[W][m].s;
+        }
+        if constexpr (m == 0 && NXS > 3) {
+          read_x(src, NW, 3, FX[3 + NW]);
+          if constexpr (W == 0) FX[3 + NW].s = FX[3 + W].s;
+        }
+        if constexpr (m == 1 || m == 3 || m == 5) {
+          if constexpr ((m >> 1) < NXS) read_x(src, NW, m >> 1, FX[m >> 1]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  auto run = [&](auto nxs_c, auto dma_c) __attribute__((always_inline)) {
+    constexpr int NXS = decltype(nxs_c)::value;
+    constexpr bool DMA = decltype(dma_c)::value;
+    if constexpr (DMA) {
+      static_for<0, S::kBufs>([&](auto bc) {
+        const Dma d = make_dma(decltype(bc)::value, decltype(bc)::value);
+        static_for<0, S::kLoads>([&](auto nc) { issue(nc, d); });
+      });
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(S::kLoads * (S::kBufs - 1)) : "memory");
+    } else {
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    if constexpr (NXS > 0) {
+      read_y(smem, 0, 0, FY[0][0]);
+      read_y(smem, 0, 1, FY[0][1]);
+    }
+    static_for<0, 4>([&](auto fc) {
+      constexpr int f = decltype(fc)::value;
+      if constexpr (f < NXS) read_x(smem, 0, f, FX[f]);
+    });
+    int buf = 0;
+    for (int kt = 0; kt < ns; ++kt) {
+      const int nbuf = buf + 1 == S::kBufs ? 0 : buf + 1;
+      const uint8_t* cs = smem + buf * S::kBytes;
+      const uint8_t* nst = smem + nbuf * S::kBytes;
+      const Dma none{};
+      window(std::integral_constant<int, 0>{}, nxs_c, std::false_type{}, cs, none);
+      // stage kt+1 has landed; every wave is done reading this buffer
+      if constexpr (DMA)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(S::kLoads * (S::kBufs - 2)) : "memory");
+      else
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      const Dma pend = make_dma(buf, kt + S::kBufs);
+      window(std::integral_constant<int, 1>{}, nxs_c, dma_c, nst, pend);
+      buf = nbuf;
+    }
+  };
+  // 32-row sub-tiles of this wave that hold rows of the group: a partial last
+  // M-tile multiplies no others
+  const int nxs = min(max((rows_x - iw * 128 + 31) >> 5, 0), 4);
+  auto by_nxs = [&](auto dma_c) __attribute__((always_inline)) {
+    if (nxs >= 4) run(std::integral_constant<int, 4>{}, dma_c);
+    else if (nxs == 3) run(std::integral_constant<int, 3>{}, dma_c);
+    else if (nxs == 2) run(std::integral_constant<int, 2>{}, dma_c);
+    else if (nxs == 1) run(std::integral_constant<int, 1>{}, dma_c);
+    else run(std::integral_constant<int, 0>{}, dma_c);
+  };
+  if (wv < 4) by_nxs(std::true_type{});
+  else by_nxs(std::false_type{});
+  // the empty loads still in flight end before the workgroup does, and before
+  // the epilogue writes their LDS
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // lane: output row i0 + 128 iw + 32 qx + l32; register group gr holds columns
+  // j0 + 64 jw + 32 qy + 8 gr + 4 half + 0..3
+  if (OUT_F32) {
+    int64_t dsts[4];      // before any store: a load issued after one waits for it
+#pragma unroll
+    for (int qx = 0; qx < 4; ++qx) {
+      const int64_t i = i0 + iw * 128 + qx * 32 + l32;
+      dsts[qx] = i >= i_end ? -1 : (a.row_map ? (int64_t)a.row_map[i] : i);
+    }
+#pragma unroll
+    for (int qx = 0; qx < 4; ++qx) {
+      if (dsts[qx] < 0 || dsts[qx] >= a.c_rows) continue;
+      float* crow = (float*)a.C + dsts[qx] * a.J;
+#pragma unroll
+      for (int qy = 0; qy < 2; ++qy) {
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) {
+          const int64_t j = j0 + jw * 64 + qy * 32 + 8 * gr + 4 * half;
+          const v16f& v = acc[qy][qx];
+          if (j < a.J)
+            *(float4*)(crow + j) = make_float4(v[4 * gr], v[4 * gr + 1], v[4 * gr + 2], v[4 * gr + 3]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  } else {
+    // through the idle LDS, so that the stores write whole 512-byte row segments
+#pragma unroll
+    for (int qx = 0; qx < 4; ++qx) {
+      const int row = iw * 128 + qx * 32 + l32;
+#pragma unroll
+      for (int qy = 0; qy < 2; ++qy) {
+        const v16f& v = acc[qy][qx];
+        // trading groups with lane l ^ 32 leaves each lane 8 consecutive columns
+#pragma unroll
+        for (int pr = 0; pr < 2; ++pr) {
+          const int g0 = 8 * pr, g1 = 8 * pr + 4;
+          const auto x = __builtin_amdgcn_permlane32_swap(pack_bf16x2_rne(v[g0], v[g0 + 1]),
+                                                          pack_bf16x2_rne(v[g1], v[g1 + 1]), false, false);
+          const auto y = __builtin_amdgcn_permlane32_swap(pack_bf16x2_rne(v[g0 + 2], v[g0 + 3]),
+                                                          pack_bf16x2_rne(v[g1 + 2], v[g1 + 3]), false, false);
+          const int col = jw * 64 + qy * 32 + 16 * pr + 8 * half;
+          *(v4i*)(smem + row * kOutPitch + col * 2) = (v4i){(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    __syncthreads();
+    // 16 bytes (8 columns, wholly inside or past J) of row 16 it + tid / 32; the
+    // output is not read here: streaming stores leave the operands in L2
+    const int c8 = (tid & 31) * 8;
+    const int64_t j = j0 + c8;
+    int dst[kBM / 16];
+#pragma unroll
+    for (int it = 0; it < kBM / 16; ++it) {
+      const int64_t i = i0 + it * 16 + (tid >> 5);
+      dst[it] = i < i_end ? (a.row_map ? a.row_map[i] : (int)i) : -1;
+    }
+#pragma unroll 4
+    for (int it = 0; it < kBM / 16; ++it) {
+      const v4i w = *(const v4i*)(smem + (it * 16 + (tid >> 5)) * kOutPitch + c8 * 2);
+      if (dst[it] >= 0 && dst[it] < a.c_rows && j < a.J)
+        __builtin_nontemporal_store(w, (v4i*)((uint16_t*)a.C + (int64_t)dst[it] * a.J + j));
+    }
+  }
+}
+
+template <int XF, bool OUT_F32>
+static hipError_t launch_rows(const Fp4GemmArgs& a, bool small, hipStream_t st) {
+  if (small) {
+    hipLaunchKernelGGL((fp4_rows_small_kernel<XF, OUT_F32>), dim3((unsigned)rows::grid<kSmBM, kSmBN>(a.I, a.J, a.E)),
+                       dim3(kSmWaves * 64), 0, st, a);
+    return hipGetLastError();
+  }
+  const size_t lds = (size_t)Stage<XF>::kBytes * Stage<XF>::kBufs;
+  const hipError_t e = hipFuncSetAttribute((const void*)fp4_rows_kernel<XF, OUT_F32>,
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((fp4_rows_kernel<XF, OUT_F32>), dim3((unsigned)rows::grid<kBM, kBN>(a.I, a.J, a.E)),
+                     dim3(kThreads), lds, st, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_fp4_gemm(const Fp4GemmArgs& a, hipStream_t st) {
   if (a.I == 0 || a.J == 0) return hipSuccess;
-  const dim3 grid((unsigned)rows::grid<kSmBM, kSmBN>(a.I, a.J, a.E)), block(kSmWaves * 64);
-  if (a.x_fp4) {
-    if (a.out_f32) hipLaunchKernelGGL((fp4_rows_small_kernel<kFmtE2M1, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((fp4_rows_small_kernel<kFmtE2M1, false>), grid, block, 0, st, a);
-  } else {
-    if (a.out_f32) hipLaunchKernelGGL((fp4_rows_small_kernel<kFmtE4M3, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((fp4_rows_small_kernel<kFmtE4M3, false>), grid, block, 0, st, a);
-  }
-  return hipGetLastError();
+  const bool small = a.I < 64 * (int64_t)a.E;
+  if (a.x_fp4) return a.out_f32 ? launch_rows<kFmtE2M1, true>(a, small, st) : launch_rows<kFmtE2M1, false>(a, small, st);
+  return a.out_f32 ? launch_rows<kFmtE4M3, true>(a, small, st) : launch_rows<kFmtE4M3, false>(a, small, st);
 }
 
 }  // namespace mxk
