@@ -126,7 +126,16 @@ __global__ __launch_bounds__(kSmWaves * 64) void fp4_rows_small_kernel(Fp4GemmAr
 // fragments while the current one's matrix instructions run, and there is one
 // barrier per stage, at the start of its second window: by then every wave has
 // the stage's last fragments in registers, so its buffer can take the stage
-// kBufs later, and the next stage has landed.
+// kBufs later, and the next stage has landed.  That stage's loads are spread
+// over this window and the first one of the next stage: half of them in each
+// took 605-614 us where all in the first took 627-632 (16384 x 8192 x 5120
+// over 16 experts, MXFP8 activations), 409 against 424 on Zipf routing.
+//
+// What bounds it: the power of moving operands.  On constant data the same
+// launch (dense 16384 x 8192 x 5120, MXFP8) takes 400 us instead of 494, and
+// 366 when no operand moves.  MXFP4 rows arrive as 64-byte halves of lines;
+// stages of 256 elements (whole lines) leave room for two buffers instead of
+// four and were slower on ragged groups (445 against 430 us).
 // ---------------------------------------------------------------------------
 typedef __attribute__((address_space(3))) void lds_ptr;
 
@@ -142,6 +151,7 @@ struct Stage {
   static constexpr int kBufs = XF == kFmtE4M3 ? 3 : 4;
   static constexpr int kXLoads = kX / 4096, kYLoads = kY / 4096;        // one-KiB loads per loading wave
   static constexpr int kLoads = kXLoads + kYLoads + 2;                  // and the scales of its 64 rows, twice 256 B
+  static constexpr int kFirst = kLoads / 2;                             // of them in the stage's second window
 };
 static_assert(kBM * kOutPitch <= Stage<kFmtE4M3>::kBytes * 3 && kBM * kOutPitch <= Stage<kFmtE2M1>::kBytes * 4, "epilogue");
 
@@ -276,10 +286,13 @@ __global__ __launch_bounds__(kThreads, 1) void fp4_rows_kernel(Fp4GemmArgs a) {
   // so that its refill does not wait for the window's last instruction), Y
   // sub-tiles in FY[window].
   Frag FX[5], FY[2][2];
+  // Window W: its eight matrix instructions, the reads of the other window of
+  // `src`, and this wave's part of the loads of `pend`.
   auto window = [&](auto w_c, auto nxs_c, auto loads_c, const uint8_t* src, const Dma& pend)
                     __attribute__((always_inline)) {
     constexpr int W = decltype(w_c)::value, NW = W ^ 1, NXS = decltype(nxs_c)::value;
     constexpr bool LOADS = decltype(loads_c)::value;
+    constexpr int kFrom = W == 1 ? 0 : S::kFirst, kTo = W == 1 ? S::kFirst : S::kLoads;
     static_for<0, 8>([&](auto mc) {
       constexpr int m = decltype(mc)::value, qx = m >> 1, qy = m & 1, xi = qx < 3 ? qx : 3 + W;
       if constexpr (qx < NXS)
@@ -287,8 +300,7 @@ __global__ __launch_bounds__(kThreads, 1) void fp4_rows_kernel(Fp4GemmArgs a) {
                                                                       2 * W, FY[W][qy].s, 2 * W, FX[xi].s);
       if constexpr (LOADS) {
         // spread over the window's instructions
-        constexpr int lo = m * S::kLoads / 8, hi = (m + 1) * S::kLoads / 8;
-        static_for<lo, hi>([&](auto nc) { issue(nc, pend); });
+        static_for<kFrom + m * (kTo - kFrom) / 8, kFrom + (m + 1) * (kTo - kFrom) / 8>([&](auto nc) { issue(nc, pend); });
       }
       if constexpr (NXS > 0) {
         if constexpr (m < 2) {
@@ -312,9 +324,10 @@ __global__ __launch_bounds__(kThreads, 1) void fp4_rows_kernel(Fp4GemmArgs a) {
     if constexpr (DMA) {
       static_for<0, S::kBufs>([&](auto bc) {
         const Dma d = make_dma(decltype(bc)::value, decltype(bc)::value);
-        static_for<0, S::kLoads>([&](auto nc) { issue(nc, d); });
+        static_for<0, decltype(bc)::value == S::kBufs - 1 ? S::kFirst : S::kLoads>([&](auto nc) { issue(nc, d); });
       });
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(S::kLoads * (S::kBufs - 1)) : "memory");
+      // stage 0 has landed
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(S::kLoads * (S::kBufs - 2) + S::kFirst) : "memory");
     } else {
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
@@ -326,13 +339,13 @@ __global__ __launch_bounds__(kThreads, 1) void fp4_rows_kernel(Fp4GemmArgs a) {
       constexpr int f = decltype(fc)::value;
       if constexpr (f < NXS) read_x(smem, 0, f, FX[f]);
     });
-    int buf = 0;
+    int buf = 0, last = S::kBufs - 1;      // buffers of stages kt and kt - 1
     for (int kt = 0; kt < ns; ++kt) {
       const int nbuf = buf + 1 == S::kBufs ? 0 : buf + 1;
       const uint8_t* cs = smem + buf * S::kBytes;
       const uint8_t* nst = smem + nbuf * S::kBytes;
-      const Dma none{};
-      window(std::integral_constant<int, 0>{}, nxs_c, std::false_type{}, cs, none);
+      const Dma rest = make_dma(last, kt + S::kBufs - 1);
+      window(std::integral_constant<int, 0>{}, nxs_c, dma_c, cs, rest);
       // stage kt+1 has landed; every wave is done reading this buffer
       if constexpr (DMA)
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(S::kLoads * (S::kBufs - 2)) : "memory");
@@ -340,6 +353,7 @@ __global__ __launch_bounds__(kThreads, 1) void fp4_rows_kernel(Fp4GemmArgs a) {
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       const Dma pend = make_dma(buf, kt + S::kBufs);
       window(std::integral_constant<int, 1>{}, nxs_c, dma_c, nst, pend);
+      last = buf;
       buf = nbuf;
     }
   };

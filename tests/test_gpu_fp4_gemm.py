@@ -34,7 +34,7 @@ def _operands(counts, N, K, fmt, seed, outliers=True):
 
 CASES = [
     ([1], 8, 128), ([0, 1, 0], 16, 128), ([5, 0, 40, 19], 72, 384), ([64, 65, 63, 1], 264, 256), ([96, 160], 512, 256),
-    ([300, 0, 513, 2], 520, 640), ([256, 257], 256, 1152), ([3] * 33, 136, 256),
+    ([300, 0, 513, 2], 520, 640), ([256, 257], 256, 1152), ([3] * 33, 136, 256), ([300, 400], 264, 128), ([700], 8, 384),
 ]
 
 
