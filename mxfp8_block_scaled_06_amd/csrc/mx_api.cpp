@@ -708,12 +708,32 @@ mx_status mx_grouped_mm_dgrad_fp4(const uint16_t* dOut, const uint8_t* qWt, cons
 
 }  // extern "C"
 
+namespace {
+
+// Regions of the MoE layer's workspace: h codes, h scales, the hit experts,
+// their tokens.
+struct MoeWs {
+  size_t hs, meta, list, total;
+};
+
+MoeWs moe_ws(int64_t T, int64_t topk, int64_t N) {
+  const size_t n = (size_t)(T * topk), slots = n < (size_t)mxk::kMaxExperts ? n : (size_t)mxk::kMaxExperts;
+  MoeWs w;
+  w.hs = align_up(n * (size_t)N, 256);
+  w.meta = w.hs + align_up(n * (size_t)(N / 32), 256);
+  w.list = w.meta + align_up((slots + 1) * sizeof(int32_t), 256);
+  w.total = w.list + align_up(n * sizeof(int2), 256);
+  return w;
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t mx_moe_few_tokens_workspace_bytes(int64_t T, int64_t topk, int64_t N) {
   if (T < 0 || T > MX_MOE_MAX_TOKENS || topk < 1 || topk > MX_MOE_MAX_TOPK) return 0;
-  if (N < 128 || N % 128 != 0 || N > ((int64_t)1 << 20)) return 0;
-  return align_up((size_t)(T * topk * N), 256) + align_up((size_t)(T * topk * (N / 32)), 256);
+  if (N < 128 || N % 128 != 0 || N > ((int64_t)1 << 20) || T * topk * N > ((int64_t)1 << 30)) return 0;
+  return moe_ws(T, topk, N).total;
 }
 
 mx_status mx_moe_few_tokens(const uint16_t* x, const int32_t* expert_idx, const float* combine, const uint8_t* q13,
@@ -731,9 +751,12 @@ mx_status mx_moe_few_tokens(const uint16_t* x, const int32_t* expert_idx, const 
     return fail(MX_ERR_SHAPE, "%s: topk=%lld outside [1, %d]", fn, (long long)topk, MX_MOE_MAX_TOPK);
   if (E < 1 || E > mxk::kMaxExperts)
     return fail(MX_ERR_SHAPE, "%s: number of experts E=%lld outside [1, %d]", fn, (long long)E, mxk::kMaxExperts);
-  if (K < 128 || N < 128 || K % 128 != 0 || N % 128 != 0 || K > ((int64_t)1 << 20) || N > ((int64_t)1 << 20))
-    return fail(MX_ERR_SHAPE, "%s: K=%lld and N=%lld must be multiples of 128 in [128, 2^20]", fn, (long long)K,
-                (long long)N);
+  if (K < 128 || N < 128 || K % 128 != 0 || N % 128 != 0 || K > ((int64_t)1 << 16) || N > ((int64_t)1 << 20))
+    return fail(MX_ERR_SHAPE, "%s: K=%lld and N=%lld must be multiples of 128, from 128 to 2^16 (K) and 2^20 (N)", fn,
+                (long long)K, (long long)N);
+  if (T * topk * N > ((int64_t)1 << 30))
+    return fail(MX_ERR_SHAPE, "%s: T*topk*N = %lld exceeds 2^30 (the hidden layer's 32-bit offsets)", fn,
+                (long long)(T * topk * N));
   if (T == 0) return MX_OK;
   if (!x || !expert_idx || !combine || !q13 || !s13 || !q2 || !s2 || !out)
     return fail(MX_ERR_NULL, "%s: null pointer", fn);
@@ -752,8 +775,11 @@ mx_status mx_moe_few_tokens(const uint16_t* x, const int32_t* expert_idx, const 
   a.s13 = s13;
   a.q2 = q2;
   a.s2 = s2;
+  const MoeWs w = moe_ws(T, topk, N);
   a.h = (uint8_t*)ws;
-  a.hs = a.h + align_up((size_t)(T * topk * N), 256);
+  a.hs = a.h + w.hs;
+  a.meta = (int32_t*)(a.h + w.meta);
+  a.list = (int2*)(a.h + w.list);
   a.out = out;
   a.status = status;
   a.K = K;

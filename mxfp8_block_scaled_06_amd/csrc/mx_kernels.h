@@ -104,6 +104,8 @@ struct MoeArgs {
   const uint8_t* s2;          // [E, N/128, K, 4]
   uint8_t* h;                 // [T * topk, N] E4M3
   uint8_t* hs;                // [T * topk, N/32]
+  int32_t* meta;              // number of hit experts, then of each: expert | tokens << 16
+  int2* list;                 // their tokens: row of h | token << 16, combine weight (float bits)
   uint16_t* out;              // bf16 [T, K]
   int32_t* status;            // optional: 1 when an id lies outside [0, E), else 0
   int64_t K, N;

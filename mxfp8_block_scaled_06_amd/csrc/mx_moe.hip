@@ -17,10 +17,11 @@
 //                       workgroup (one block of h), for all its tokens;
 //   moe_down_kernel     16 output columns per workgroup, all hit experts, all
 //                       tokens; the sum over a token's experts stays in fp32
-//                       registers, so nothing is added through memory and the
+//                       on the CU, so nothing is added through memory and the
 //                       order of additions is fixed.
 // Both split their contraction over the eight waves of the workgroup and add
-// the partial sums in wave order.
+// the partial sums in wave order.  A wave keeps the next chunks of its weights
+// in flight while it multiplies one.
 //
 // Matrix operand layout (v_mfma_scale_f32_16x16x128_f8f6f4): lane l holds row
 // l%16, group g = l/16: E2M1 elements 32g..32g+31 in 16 bytes, E4M3 the
@@ -28,6 +29,7 @@
 // column l%16, rows 4g..4g+3.  Weights are the first operand (rows), tokens
 // the second (columns).
 #include <algorithm>
+#include <type_traits>
 
 #include "mx_device.h"
 #include "mx_kernels.h"
@@ -35,46 +37,18 @@
 namespace mxk {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kMoeWaves = 8, kMoeThreads = kMoeWaves * 64;
-constexpr int kMoeRows = 32;                       // rows of h per workgroup: one scale block
-constexpr int kMoeItems = kMoeMaxTokens * kMoeMaxTopk;
+constexpr int kMoeRows = 32;                       // rows of h per block: one scale block
+constexpr int kMoeCols = 16;                       // tokens per matrix tile
 constexpr int kFmtE4M3 = 0, kFmtE2M1 = 4;          // the instruction's operand formats
+constexpr int kLds = 160 * 1024;                   // of a CU
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// ids of the call in LDS, and the set of experts that any of them names.
-// Ids outside [0, E) name none.
-__device__ __forceinline__ void load_ids(const MoeArgs& a, int* s_ids, uint32_t* s_bits) {
-  const int tid = threadIdx.x, n = a.T * a.topk;
-  if (tid < kMaxExperts / 32) s_bits[tid] = 0u;
-  __syncthreads();
-  for (int i = tid; i < n; i += kMoeThreads) {
-    const int e = a.ids[i];
-    s_ids[i] = e;
-    if (e >= 0 && e < a.E) atomicOr(&s_bits[e >> 5], 1u << (e & 31));
-  }
-  __syncthreads();
-}
-
-// Hit experts in ascending order: how many there are, and with them how many
-// come before this lane's 32 (lanes 0..31).
-__device__ __forceinline__ int count_hit(const uint32_t* s_bits, uint32_t& word, int& before) {
-  const int lane = threadIdx.x & 63;
-  word = lane < kMaxExperts / 32 ? s_bits[lane] : 0u;
-  int incl = __popc(word);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d);
-    if (lane >= d) incl += v;
-  }
-  before = incl - __popc(word);
-  return uni(__shfl(incl, 63));
-}
-
-// First slot of token t that names expert e (or -1), and the sum of the
-// combine weights of all its slots that do: a token that names an expert twice
-// is one row of that expert.
+// Slot of token t that names expert e first, or -1: a token that names an
+// expert twice is one row of that expert.
 __device__ __forceinline__ int slot_of(const int* s_ids, int t, int topk, int e) {
   int found = -1;
   for (int j = topk - 1; j >= 0; --j)
@@ -82,16 +56,76 @@ __device__ __forceinline__ int slot_of(const int* s_ids, int t, int topk, int e)
   return found;
 }
 
-// 16 bytes of E2M1 or two 16-byte pieces of E4M3 of a weight row's chunk.
-template <int WF>
-__device__ __forceinline__ v8i load_weight(const uint8_t* row, int ch, int g) {
-  if (WF == kFmtE2M1) {
-    const v4i w = __builtin_nontemporal_load((const v4i*)(row + (int64_t)ch * 64 + 16 * g));
-    return (v8i){w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+// ids of the call in LDS, and how many tokens name each expert.  Ids outside
+// [0, E) name none.  (Whole numbers are added: the order does not matter.)
+__device__ __forceinline__ void load_ids(const MoeArgs& a, int* s_ids, int* s_count) {
+  const int tid = threadIdx.x, n = a.T * a.topk;
+  for (int i = tid; i < a.E; i += kMoeThreads) s_count[i] = 0;
+  for (int i = tid; i < n; i += kMoeThreads) s_ids[i] = a.ids[i];
+  __syncthreads();
+  for (int i = tid; i < n; i += kMoeThreads) {
+    const int e = s_ids[i], t = i / a.topk;
+    if (e >= 0 && e < a.E && slot_of(s_ids, t, a.topk, e) == i - t * a.topk) atomicAdd(&s_count[e], 1);
   }
-  const v4i w = __builtin_nontemporal_load((const v4i*)(row + (int64_t)ch * 128 + 16 * g));
-  const v4i v = __builtin_nontemporal_load((const v4i*)(row + (int64_t)ch * 128 + 64 + 16 * g));
-  return (v8i){w[0], w[1], w[2], w[3], v[0], v[1], v[2], v[3]};
+  __syncthreads();
+}
+
+// Tokens of expert e in ascending order, found by a whole wave: token t goes to
+// put(position, t, first slot); returns how many.
+template <class F>
+__device__ __forceinline__ int tokens_of(const MoeArgs& a, const int* s_ids, int e, F&& put) {
+  const int lane = threadIdx.x & 63;
+  int m = 0;
+  for (int t0 = 0; t0 < a.T; t0 += 64) {
+    const int t = t0 + lane;
+    const int j = t < a.T ? slot_of(s_ids, t, a.topk, e) : -1;
+    const uint64_t mask = __ballot(j >= 0);
+    if (j >= 0) put(m + __builtin_popcountll(mask & ((1ull << lane) - 1)), t, j);
+    m += __builtin_popcountll(mask);
+  }
+  return m;
+}
+
+// Buffer descriptor of `bytes` bytes from `base`.  Reads past the end give 0
+// and touch no memory: kPast is an offset past every end, for loads that a
+// pipeline issues beyond its last step.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+constexpr int kPast = 0x7FFFFFF0;
+
+// Weights are read a line (128 bytes) of each row at a time, which is one
+// 128-element chunk of E4M3 or two of E2M1: read by 64-byte halves, with other
+// loads between, E2M1 lines came from memory twice and the layer ran at half
+// the bandwidth.  A lane's two 16-byte pieces of a line are its operand of the
+// chunk (E4M3), or those of the two chunks (E2M1).
+template <int WF>
+constexpr int kUnit = WF == kFmtE2M1 ? 2 : 1;      // chunks of a line
+
+struct Weight {
+  v4i p[2];
+};
+
+// Line `u` of the weight row at byte offset `row`.
+__device__ __forceinline__ Weight load_weight(__amdgpu_buffer_rsrc_t r, int row, int u, int g, bool live) {
+  const int o = live ? row + u * 128 + 16 * g : kPast - 64;
+  return {{__builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0),
+           __builtin_amdgcn_raw_buffer_load_b128(r, o + 64, 0, 0)}};
+}
+
+// Chunk `i` of a line as the instruction's first operand.
+template <int WF>
+__device__ __forceinline__ v8i operand(const Weight& w, int i) {
+  if (WF == kFmtE2M1) return __builtin_shufflevector(w.p[i], w.p[i], 0, 1, 2, 3, -1, -1, -1, -1);
+  return __builtin_shufflevector(w.p[0], w.p[1], 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+template <int M, int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (M < N) {
+    f(std::integral_constant<int, M>{});
+    static_for<M + 1, N>(f);
+  }
 }
 
 template <int WF>
@@ -99,295 +133,495 @@ __device__ __forceinline__ v4f mfma(const v8i& w, int ws, const v8i& x, int xs, 
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, WF, kFmtE4M3, 0, ws, 0, xs);
 }
 
-// The lane's part of 128 bf16 values of its token in MXFP8: pieces g and g+4
-// (w: 16 + 16 values) and the scale byte of block g.  Piece p belongs to block
-// p/2, so a block's amax takes the neighbouring group's lane too.
-__device__ __forceinline__ v8i quantize_operand(const v4i w[4], int lane, int& scale) {
-  const int g = lane >> 4, l16 = lane & 15;
-  uint32_t lo = max(absmax8(w[0]), absmax8(w[1])), hi = max(absmax8(w[2]), absmax8(w[3]));
-  uint32_t both = lo | hi << 16;       // |bf16| bits fit 15 bits
-  const uint32_t other = (uint32_t)__shfl_xor((int)both, 16);
-  lo = max(lo, other & 0xFFFFu);
-  hi = max(hi, other >> 16);
-  const uint32_t blo = e8m0_from_absbits(lo), bhi = e8m0_from_absbits(hi);
-  const float mlo = inv_scale_from_e8m0(blo == 0xFFu ? 127u : blo);
-  const float mhi = inv_scale_from_e8m0(bhi == 0xFFu ? 127u : bhi);
-  v8i q;
+// The wave's share of `n` units, within one of its fellows'.
+__device__ __forceinline__ int share(int n, int wv) { return (int)((int64_t)n * wv / kMoeWaves); }
+
+// Workgroup barrier that orders LDS accesses and leaves loads from memory in
+// flight (__syncthreads() would wait for them).
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// A dword per row in the lanes' four groups of 16 (a, b, c, d) -> lo: a and b
+// each in all four groups, hi: c and d.
+struct Spread {
+  uint32_t lo[2], hi[2];
+};
+__device__ __forceinline__ Spread spread_rows(uint32_t v) {
+  const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);      // [a b a b], [c d c d]
+  const auto l = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+  const auto u = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+  return {{l[0], l[1]}, {u[0], u[1]}};
+}
+
+// Four packed bf16 pairs of a block with scale byte `byte` -> eight E4M3
+// codes.  The convert divides by the scale and rounds to nearest even but does
+// not saturate, so magnitudes are clamped to 448 * 2^(byte - 127) first, as
+// bf16 bits (1.75 * 2^(byte + 8 - 127): mantissa bits 0x60).
+__device__ __forceinline__ v2i quantize8(v4i w, uint32_t byte, uint32_t most) {
+  const float scale = __uint_as_float(byte << 23);
+  v2i q;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const v2i c = quant8(w[i], i < 2 ? mlo : mhi);
-    const bool nan = (i < 2 ? blo : bhi) == 0xFFu;
-    q[2 * i] = nan ? 0x7F7F7F7F : c[0];
-    q[2 * i + 1] = nan ? 0x7F7F7F7F : c[1];
+  for (int i = 0; i < 2; ++i) {
+    s16x2 r = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t u = (uint32_t)w[2 * i + j];
+      const us2 m = __builtin_elementwise_min(__builtin_bit_cast(us2, u & 0x7FFF7FFFu), __builtin_bit_cast(us2, most));
+      const uint32_t v = __builtin_bit_cast(uint32_t, m) | (u & 0x80008000u);
+      if (j == 0) r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, v), scale, 0);
+      else r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, v), scale, 1);
+    }
+    q[i] = __builtin_bit_cast(int, r);
   }
-  // block 0: low half of groups 0, 1; block 1: of 2, 3; blocks 2, 3: high half
-  const int src = g == 1 ? l16 + 32 : g == 2 ? l16 : lane;
-  const uint32_t bytes = (uint32_t)__shfl((int)(blo | bhi << 8), src);
-  scale = (int)(g < 2 ? bytes & 0xFFu : bytes >> 8);
   return q;
 }
 
-// ---------------------------------------------------------------------------
-// Gate and up projection, SwiGLU and the quantization of h.  Workgroup
-// (n-block, hit expert): up to 16 * CT tokens of that expert.
-// ---------------------------------------------------------------------------
-template <int WF, int CT>
-__global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(MoeArgs a) {
-  __shared__ int s_ids[kMoeItems];
-  __shared__ uint32_t s_bits[kMaxExperts / 32];
-  __shared__ int s_item[kMoeMaxTokens];
-  __shared__ v4f part[kMoeWaves][4][64];
-  load_ids(a, s_ids, s_bits);
-  const int tid = threadIdx.x, lane = tid & 63, wv = uni(tid >> 6), l16 = lane & 15, g = lane >> 4;
-  uint32_t word;
-  int before;
-  const int hit = count_hit(s_bits, word, before);
-  const int slot = blockIdx.y;
-  if (slot >= hit) return;
-  // the slot-th hit expert
-  const uint64_t owner = __ballot(slot >= before && slot < before + __popc(word));
-  const int src = __builtin_ctzll(owner);
-  uint32_t w = (uint32_t)__shfl((int)word, src);
-  for (int i = slot - __shfl(before, src); i > 0; --i) w &= w - 1u;
-  const int e = uni(src * 32 + __builtin_ctz(w));
-  // its tokens, in order: item = t * topk + slot
-  int m = 0;
+// Largest |bf16| bits of eight values, as a packed pair still to be combined.
+__device__ __forceinline__ us2 absmax8x2(v4i w) {
+  us2 m = __builtin_bit_cast(us2, (uint32_t)w[0] & 0x7FFF7FFFu);
 #pragma unroll
-  for (int t0 = 0; t0 < kMoeMaxTokens; t0 += 64) {
-    const int t = t0 + lane;
-    const int j = t < a.T ? slot_of(s_ids, t, a.topk, e) : -1;
-    const uint64_t mask = __ballot(j >= 0);
-    if (wv == 0 && j >= 0) s_item[m + __builtin_popcountll(mask & ((1ull << lane) - 1))] = t * a.topk + j;
-    m += __builtin_popcountll(mask);
+  for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(us2, (uint32_t)w[i] & 0x7FFF7FFFu));
+  return m;
+}
+
+// 128 consecutive MXFP8 elements of a token in LDS: the codes, then the four
+// scale bytes.  144 bytes apart, one 16-byte piece of 16 tokens falls into 16
+// different banks groups.
+constexpr int kRec = 144;
+
+// The lane's operand from a record: pieces g and g+4, scale byte g.
+__device__ __forceinline__ v8i read_record(const uint8_t* rec, int g, int& scale) {
+  const v4i p = *(const v4i*)(rec + 16 * g), q = *(const v4i*)(rec + 64 + 16 * g);
+  scale = rec[128 + g];
+  return (v8i){p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
+}
+
+// ---------------------------------------------------------------------------
+// Gate and up projection, SwiGLU and the quantization of h.  A workgroup takes
+// `blocks` consecutive 32-row blocks of one work entry: one hit expert with up
+// to `rows` of its tokens, whose x it quantizes into LDS once for all blocks.
+// An expert with more tokens has another entry; the two run side by side and
+// share the weights in L2.
+//
+// Loads from memory are waited for in the order of their issue, so the wave's
+// stream of weights, D lines of each row ahead and across the blocks, has no
+// load in it that is wanted sooner: x is in LDS by then, and the scales come
+// with the weights, one dword per row and chunk.
+// ---------------------------------------------------------------------------
+template <int WF, int D>
+__global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))) void moe_gate_up_kernel(MoeArgs a,
+                                                                                                          int rows,
+                                                                                                          int blocks) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ v4f part[kMoeWaves][2][64];
+  __shared__ int s_count[kMaxExperts];
+  __shared__ int s_item[kMoeMaxTokens], s_token[kMoeMaxTokens], s_expert, s_pass;
+  constexpr int U = kUnit<WF>;
+  const int tid = threadIdx.x, lane = tid & 63, wv = uni(tid >> 6), l16 = lane & 15, g = lane >> 4;
+  const int64_t K = a.K, N = a.N;
+  const int nch = (int)(K / 128), units = (nch + U - 1) / U;
+  int* s_ids = (int*)(smem + nch * rows * kRec);
+  load_ids(a, s_ids, s_count);
+  if (wv == 0) {
+    // the blockIdx.y-th work entry, experts in ascending order; how many experts
+    // are hit, and how many of them and of their tokens come before this one
+    int hit = 0, entries = 0, e = -1, pass = 0, rank = 0, off = 0;
+    for (int base = 0; base < a.E; base += 64) {
+      const int c = base + lane < a.E ? s_count[base + lane] : 0, p = (c + rows - 1) / rows;
+      int ip = p;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(ip, d);
+        if (lane >= d) ip += v;
+      }
+      const uint64_t mask = __ballot(c > 0), own = __ballot(entries + ip > (int)blockIdx.y);
+      if (e < 0) {
+        const int at = own ? __builtin_ctzll(own) : 64;      // the first expert whose entries reach past it
+        int before = lane < at ? c : 0;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) before += __shfl_xor(before, d);
+        off += before;
+        rank += __builtin_popcountll(at < 64 ? mask & ((1ull << at) - 1) : mask);
+        if (own) {
+          e = base + at;
+          pass = (int)blockIdx.y - entries - __shfl(ip - p, at);
+        }
+      }
+      entries += __shfl(ip, 63);
+      hit += __builtin_popcountll(mask);
+    }
+    if (lane == 0) {
+      s_expert = e;
+      s_pass = pass;
+      if (blockIdx.x == 0 && blockIdx.y == 0) a.meta[0] = hit;
+    }
+    if (e >= 0) {
+      const bool leave = blockIdx.x == 0 && pass == 0;
+      const int m = tokens_of(a, s_ids, e, [&](int i, int t, int j) {
+        s_token[i] = t;
+        s_item[i] = t * a.topk + j;
+        if (leave) {
+          // for the down kernel: the row of h, the token and its weight (the
+          // sum, where it names the expert twice)
+          float c = 0.f;
+          for (int k = 0; k < a.topk; ++k)
+            if (s_ids[t * a.topk + k] == e) c += a.combine[t * a.topk + k];
+          a.list[off + i] = make_int2((t * a.topk + j) | t << 16, __float_as_int(c));
+        }
+      });
+      if (leave && lane == 0) a.meta[1 + rank] = e | m << 16;
+    }
   }
   __syncthreads();
-  m = uni(m);
-  const int nct = (m + 15) / 16;
-  const int64_t K = a.K, N = a.N, n0 = (int64_t)blockIdx.x * kMoeRows;
-  const int64_t ldw = WF == kFmtE2M1 ? K / 2 : K;
-  const uint8_t* wrow[4];
-  const uint8_t* srow[4];
+  const int e = uni(s_expert);
+  if (e < 0) return;
+  const int m0 = uni(s_pass) * rows, mp = min(uni(s_count[e]) - m0, rows);
+  const int begin = share(units, wv), end = share(units, wv + 1), count = end - begin;
+  const int b0 = blockIdx.x * blocks, nb = min(blocks, (int)(N / kMoeRows) - b0);
+  const int ldw = (int)(WF == kFmtE2M1 ? K / 2 : K);
+  const uint8_t* wbase = a.q13 + ((int64_t)e * 2 * N + (int64_t)b0 * kMoeRows) * ldw;
+  // scales: lane l's row is gate row l or up row l - 32
+  const uint8_t* sbase = a.s13 + (int64_t)e * 2 * N * (K / 32) +
+                         ((int64_t)b0 * kMoeRows + (lane < 32 ? lane : N + lane - 32)) * 4;
+
+  const int tasks = (min(end * U, nch) - begin * U) * mp;
+  uint8_t* rec = smem + begin * U * mp * kRec;      // [chunk][token]; the wave's own chunks
+  // x: 16 lanes take 128 elements of a token; four loads, 16 of them, at a time
+  v4i xw[4];
+  auto load_x = [&](int q0) __attribute__((always_inline)) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int64_t n = (r < 2 ? n0 : N + n0) + 16 * (r & 1) + l16;
-    wrow[r] = a.q13 + ((int64_t)e * 2 * N + n) * ldw;
-    srow[r] = a.s13 + (int64_t)e * 2 * N * (K / 32) + n * 4 + g;
-  }
-  const uint16_t* xrow[CT];
-  bool have[CT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    have[c] = 16 * c + l16 < m;
-    xrow[c] = a.x + (int64_t)(have[c] ? s_item[16 * c + l16] / a.topk : 0) * K;
-  }
-  v4f acc[4][CT];
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) acc[r][c] = (v4f){0.f, 0.f, 0.f, 0.f};
-  const int nch = (int)(K / 128), per = (nch + kMoeWaves - 1) / kMoeWaves;
-  const int end = min((wv + 1) * per, nch);
-  for (int ch = wv * per; ch < end; ++ch) {
-    v8i wq[4];
-    int ws[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      wq[r] = load_weight<WF>(wrow[r], ch, g);
-      ws[r] = srow[r][(int64_t)ch * 2 * N * 4];
+    for (int i = 0; i < 4; ++i) {
+      const int q = min(q0 + 4 * i + g, tasks - 1), ch = q / mp, row = q - ch * mp;
+      xw[i] = *(const v4i*)(a.x + (int64_t)s_token[m0 + row] * K + (begin * U + ch) * 128 + 8 * l16);
     }
+  };
+  auto store_x = [&](int q0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      if (c >= nct) continue;
-      v4i xw[4] = {(v4i){0, 0, 0, 0}, (v4i){0, 0, 0, 0}, (v4i){0, 0, 0, 0}, (v4i){0, 0, 0, 0}};
-      if (have[c]) {
-        const v4i* p = (const v4i*)(xrow[c] + ch * 128 + 16 * g);
-        xw[0] = p[0];
-        xw[1] = p[1];
-        xw[2] = p[8];        // 64 values on
-        xw[3] = p[9];
+    for (int i = 0; i < 4; ++i) {
+      const int q = q0 + 4 * i + g;
+      const us2 top = absmax8x2(xw[i]);
+      const uint32_t byte = e8m0_from_absbits(quad_max(max(top[0], top[1])));
+      const v2i c = quantize8(xw[i], byte, ((byte + 8u) << 7 | 0x60u) * 0x10001u);
+      if (q < tasks) {
+        uint8_t* r = rec + q * kRec;
+        *(v2i*)(r + 8 * l16) = byte == 0xFFu ? (v2i){0x7F7F7F7F, 0x7F7F7F7F} : c;
+        if ((l16 & 3) == 0) r[128 + (l16 >> 2)] = (uint8_t)byte;
       }
-      int xs;
-      const v8i xq = quantize_operand(xw, lane, xs);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r][c] = mfma<WF>(wq[r], ws[r], xq, xs, acc[r][c]);
     }
-  }
-  for (int c = 0; c < CT; ++c) {
-    if (c >= nct) break;
-    __syncthreads();
+  };
+  v4f acc[4];
+  float h[8];
+  uint32_t am = 0;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) part[wv][r][lane] = acc[r][c];
-    __syncthreads();
-    if (wv != 0) continue;
-    v4f s[4];
+  for (int r = 0; r < 4; ++r) acc[r] = (v4f){0.f, 0.f, 0.f, 0.f};
+  // Block `b` is done: the waves' sums meet in LDS, row tile by row tile, and
+  // one wave (another one each time) turns them into h.
+  auto finish = [&](int b) __attribute__((always_inline)) {
+    const bool mine = wv == (b & (kMoeWaves - 1));
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      s[r] = part[0][r][lane];
+    for (int r = 0; r < 2; ++r) {
+      lds_barrier();
+      part[wv][0][lane] = acc[r];
+      part[wv][1][lane] = acc[2 + r];
+      lds_barrier();
+      if (mine) {
+        v4f gs = part[0][0][lane], us = part[0][1][lane];
 #pragma unroll
-      for (int v = 1; v < kMoeWaves; ++v) s[r] += part[v][r][lane];
+        for (int v = 1; v < kMoeWaves; ++v) {
+          gs += part[v][0][lane];
+          us += part[v][1][lane];
+        }
+        if (r == 0) am = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          h[4 * r + i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
+          am = max(am, __float_as_uint(h[4 * r + i]) & 0x7FFFFFFFu);
+        }
+      }
     }
-    // h of rows 4g..4g+3 and 16 + 4g..; quantized from fp32, with no bf16 between
-    float h[8];
-    uint32_t am = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float gv = s[i >> 2][i & 3], uv = s[2 + (i >> 2)][i & 3];
-      h[i] = gv / (1.0f + expf(-gv)) * uv;
-      am = max(am, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-    }
+    for (int r = 0; r < 4; ++r) acc[r] = (v4f){0.f, 0.f, 0.f, 0.f};
+    if (!mine) return;
+    // rows 4g..4g+3 and 16 + 4g..; quantized from fp32, with no bf16 between
     am = max(am, (uint32_t)__shfl_xor((int)am, 16));
     am = max(am, (uint32_t)__shfl_xor((int)am, 32));
     const bool nan = am >= 0x7F800000u;
     const uint32_t byte = nan ? 0xFFu : (uint32_t)max((int)(am >> 23) - 8, 0);
     const float mul = inv_scale_from_e8m0(nan ? 127u : byte);
-    if (16 * c + l16 < m) {
-      const int64_t item = s_item[16 * c + l16];
+    if (l16 < mp) {
+      const int64_t item = s_item[m0 + l16];
+      const int n0 = (b0 + b) * kMoeRows;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        int q = cvt2_e4m3<false>(h[4 * b] * mul, h[4 * b + 1] * mul, 0);
-        q = cvt2_e4m3<true>(h[4 * b + 2] * mul, h[4 * b + 3] * mul, q);
-        *(int*)(a.h + item * N + n0 + 16 * b + 4 * g) = nan ? 0x7F7F7F7F : q;
+      for (int r = 0; r < 2; ++r) {
+        int q = cvt2_e4m3<false>(h[4 * r] * mul, h[4 * r + 1] * mul, 0);
+        q = cvt2_e4m3<true>(h[4 * r + 2] * mul, h[4 * r + 3] * mul, q);
+        *(int*)(a.h + item * N + n0 + 16 * r + 4 * g) = nan ? 0x7F7F7F7F : q;
       }
       if (g == 0) a.hs[item * (N / 32) + (n0 >> 5)] = (uint8_t)byte;
+    }
+  };
+  if (count == 0) {
+    for (int b = 0; b < nb; ++b) finish(b);
+  } else {
+    Weight wq[D][4];
+    uint32_t ws[D][U];
+    int lb = 0, lu = begin;      // block and line of the next load
+    auto load_w = [&](auto slot_c) __attribute__((always_inline)) {
+      constexpr int S = decltype(slot_c)::value;
+      const bool live = lb < nb;
+      const int b = min(lb, nb - 1);
+      const uint8_t* wb = wbase + (int64_t)b * kMoeRows * ldw;
+      const __amdgpu_buffer_rsrc_t rg = rsrc(wb, (int64_t)kMoeRows * ldw);
+      const __amdgpu_buffer_rsrc_t ru = rsrc(wb + N * ldw, (int64_t)kMoeRows * ldw);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        wq[S][r] = load_weight(r < 2 ? rg : ru, (16 * (r & 1) + l16) * ldw, lu, g, live);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        ws[S][i] = *(const uint32_t*)(sbase + ((int64_t)min(lu * U + i, nch - 1) * 2 * N + b * kMoeRows) * 4);
+      if (++lu == end) {
+        lu = begin;
+        ++lb;
+      }
+    };
+    load_x(0);       // ahead of the weights, which then load while it is quantized
+    static_for<0, D>([&](auto sc) { load_w(sc); });
+    store_x(0);
+    for (int q0 = 16; q0 < tasks; q0 += 16) {
+      load_x(q0);
+      store_x(q0);
+    }
+    int b = 0, u = begin;
+    while (b < nb) {
+      static_for<0, D>([&](auto sc) __attribute__((always_inline)) {
+        constexpr int S = decltype(sc)::value;
+        if (b < nb) {
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            // an odd last chunk has no second one: its record is read again, its products dropped
+            const int ch = min(u * U + i, nch - 1);
+            int xs;
+            const v8i xq = read_record(rec + ((ch - begin * U) * mp + min(l16, mp - 1)) * kRec, g, xs);
+            const Spread sc4 = spread_rows(ws[S][i]);
+            const uint32_t rs[4] = {sc4.lo[0], sc4.lo[1], sc4.hi[0], sc4.hi[1]};
+            if (U == 1 || u * U + i < nch) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                acc[r] = mfma<WF>(operand<WF>(wq[S][r], i), (int)(rs[r] >> (8 * g)), xq, xs, acc[r]);
+            }
+          }
+          load_w(sc);
+          if (++u == end) {
+            u = begin;
+            finish(b++);
+          }
+        }
+      });
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Down projection and the weighted sum over a token's experts.  Columns of the
-// matrix tile are tokens; a token that an expert does not have keeps its sum
-// (a select, not a multiplication by zero, so that another token's expert with
-// NaN weights does not reach it).
+// Down projection and the weighted sum over a token's experts.  A work entry
+// is one hit expert with up to 16 of its tokens (the columns of the matrix
+// tile); the wave's share is a run of (entry, line) units, of which D are in
+// registers or on their way, across the border between entries.  At the end
+// of an entry its sums, times the combine weights, are added to the wave's own
+// sums of those tokens in LDS.
 // ---------------------------------------------------------------------------
-template <int WF, int CT>
-__global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a) {
-  __shared__ int s_ids[kMoeItems];
-  __shared__ uint32_t s_bits[kMaxExperts / 32];
-  __shared__ int s_hit[kMaxExperts];
-  __shared__ v4f part[kMoeWaves][CT][64];
-  load_ids(a, s_ids, s_bits);
+template <int WF, int RT, int D>
+__global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))) void moe_down_kernel(MoeArgs a,
+                                                                                                       int slots) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int s_entries;
+  constexpr int U = kUnit<WF>;
   const int tid = threadIdx.x, lane = tid & 63, wv = uni(tid >> 6), l16 = lane & 15, g = lane >> 4;
-  uint32_t word;
-  int before;
-  const int hit = count_hit(s_bits, word, before);
+  const int64_t K = a.K, N = a.N, k0 = (int64_t)blockIdx.x * 16 * RT;
+  const int n = a.T * a.topk;
+  // the waves' sums [T][16 RT], the tokens of all hit experts, the work entries
+  // (expert | tokens << 16, and where they begin), what the gate kernel left
+  v4f* sums = (v4f*)smem + (int64_t)wv * a.T * 4 * RT;
+  int2* s_list = (int2*)(smem + (size_t)kMoeWaves * a.T * 64 * RT);
+  int2* s_work = s_list + n;
+  int* s_meta = (int*)(s_work + slots + n / kMoeCols);
+  for (int i = tid; i < n; i += kMoeThreads) s_list[i] = a.list[i];      // past the hit experts' tokens: not used
+  for (int i = tid; i <= slots; i += kMoeThreads) s_meta[i] = a.meta[i];
+  for (int i = lane; i < a.T * 4 * RT; i += 64) sums[i] = (v4f){0.f, 0.f, 0.f, 0.f};
+  __syncthreads();
   if (wv == 0) {
-    for (int i = before; word; ++i, word &= word - 1u) s_hit[i] = lane * 32 + __builtin_ctz(word);
-  }
-  if (a.status != nullptr && blockIdx.x == 0 && wv == 1) {
+    const int hit = s_meta[0];
+    int carry = 0, off = 0;
+    for (int base = 0; base < hit; base += 64) {
+      const int meta = base + lane < hit ? s_meta[1 + base + lane] : 0, m = meta >> 16;
+      const int p = (m + kMoeCols - 1) / kMoeCols;
+      int incl = p | m << 16;        // both running sums at once (at most 1280 entries, 4096 tokens)
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(incl, d);
+        if (lane >= d) incl += v;
+      }
+      const int at = carry + (incl & 0xFFFF) - p, first = off + (incl >> 16) - m;
+      for (int i = 0; i < p; ++i)
+        s_work[at + i] = make_int2((meta & 0xFFFF) | min(m - i * kMoeCols, kMoeCols) << 16, first + i * kMoeCols);
+      const int last = __shfl(incl, 63);
+      carry += last & 0xFFFF;
+      off += last >> 16;
+    }
+    if (lane == 0) s_entries = carry;
+  } else if (a.status != nullptr && blockIdx.x == 0 && wv == 1) {
     bool bad = false;
-    for (int i = lane; i < a.T * a.topk; i += 64) bad |= s_ids[i] < 0 || s_ids[i] >= a.E;
+    for (int i = lane; i < n; i += 64) bad |= a.ids[i] < 0 || a.ids[i] >= a.E;
     const uint64_t any = __ballot(bad);
     if (lane == 0) a.status[0] = any != 0;
   }
   __syncthreads();
-  const int64_t K = a.K, N = a.N, k0 = (int64_t)blockIdx.x * 16;
-  const int64_t ldw = WF == kFmtE2M1 ? N / 2 : N;
-  const int nch = (int)(N / 128), units = hit * nch, per = (units + kMoeWaves - 1) / kMoeWaves;
-  v4f tot[CT], acc[CT];
-  const uint8_t* hrow[CT];
-  const uint8_t* hsrow[CT];
-  bool have[CT], any[CT];
-  float comb[CT];
+  const int ldw = (int)(WF == kFmtE2M1 ? N / 2 : N);
+  const int entries = uni(s_entries);
+  const int nch = (int)(N / 128), lines = (nch + U - 1) / U, units = entries * lines;
+  const int begin = share(units, wv), end = share(units, wv + 1);
+  const __amdgpu_buffer_rsrc_t rh = rsrc(a.h, (int64_t)n * N);
+  const __amdgpu_buffer_rsrc_t rhs = rsrc(a.hs, (int64_t)n * (N / 32));
+  if (begin < end) {
+    // this lane's token of a work entry: row of h | token << 16 (or -1), combine weight
+    auto token_of = [&](int2 work) __attribute__((always_inline)) {
+      return l16 < work.x >> 16 ? s_list[work.y + l16] : make_int2(-1, 0);
+    };
+    Weight wq[D][RT];
+    v8i hq[D][U];
+    uint32_t ws[D];
+    int hs[D][U];
+    int lx = begin / lines, lu = begin - lx * lines;      // entry and line of the next unit to load
+    int item = -1;
+    const uint8_t *wbase = nullptr, *sbase = nullptr;
+    auto enter_load = [&]() __attribute__((always_inline)) {
+      const int2 work = s_work[min(lx, entries - 1)];
+      const int64_t e = uni(work.x & 0xFFFF);
+      const int2 t = token_of(work);
+      item = t.x < 0 ? -1 : t.x & 0xFFFF;
+      wbase = a.q2 + (e * K + k0) * ldw;
+      // scales: lane l's row is l % 32, of the line's second chunk for l >= 32
+      sbase = a.s2 + (e * K * (N / 128) + k0 + lane % (16 * RT)) * 4;
+    };
+    auto load = [&](auto slot_c, int u) __attribute__((always_inline)) {
+      constexpr int S = decltype(slot_c)::value;
+      const bool live = u < end;
+      const __amdgpu_buffer_rsrc_t rw = rsrc(wbase, (int64_t)16 * RT * ldw);
 #pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    tot[c] = acc[c] = (v4f){0.f, 0.f, 0.f, 0.f};
-    have[c] = any[c] = false;
-    comb[c] = 0.f;
-    hrow[c] = a.h;
-    hsrow[c] = a.hs;
-  }
-  const uint8_t *wrow = a.q2, *srow = a.s2;
-  auto flush = [&]() {
+      for (int r = 0; r < RT; ++r) wq[S][r] = load_weight(rw, (16 * r + l16) * ldw, lu, g, live);
+      ws[S] = *(const uint32_t*)(sbase + (int64_t)min(lu * U + (U > 1 ? lane >> 5 : 0), nch - 1) * K * 4);
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      if (!any[c]) continue;
-      if (have[c]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tot[c][i] += comb[c] * acc[c][i];
+      for (int i = 0; i < U; ++i) {
+        const int ch = min(lu * U + i, nch - 1);       // a line's second chunk past the end is not used
+        const bool have = live && item >= 0;
+        const int o = have ? item * (int)N + ch * 128 + 16 * g : kPast - 64;
+        const v4i p = __builtin_amdgcn_raw_buffer_load_b128(rh, o, 0, 0);
+        const v4i q = __builtin_amdgcn_raw_buffer_load_b128(rh, o + 64, 0, 0);
+        hq[S][i] = (v8i){p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
+        hs[S][i] = __builtin_amdgcn_raw_buffer_load_b8(rhs, have ? item * (int)(N / 32) + ch * 4 + g : kPast, 0, 0);
       }
-      acc[c] = (v4f){0.f, 0.f, 0.f, 0.f};
-    }
-  };
-  int cur = -1;
-  const int end = min((wv + 1) * per, units);
-  for (int u = wv * per; u < end; ++u) {
-    const int x = u / nch, ch = u - x * nch;
-    if (x != cur) {
-      flush();
-      cur = x;
-      const int e = uni(s_hit[x]);
-      wrow = a.q2 + ((int64_t)e * K + k0 + l16) * ldw;
-      srow = a.s2 + (int64_t)e * K * (N / 32) + (k0 + l16) * 4 + g;
+      if (++lu == lines) {
+        lu = 0;
+        ++lx;
+        enter_load();
+      }
+    };
+    v4f acc[RT];
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        const int t = 16 * c + l16;
-        int first = -1;
-        comb[c] = 0.f;
-        if (t < a.T) {
-          for (int j = 0; j < a.topk; ++j) {
-            if (s_ids[t * a.topk + j] != e) continue;
-            if (first < 0) first = t * a.topk + j;
-            comb[c] += a.combine[t * a.topk + j];
+    for (int r = 0; r < RT; ++r) acc[r] = (v4f){0.f, 0.f, 0.f, 0.f};
+    int mx = lx, mu = lu;      // entry and line of the next unit to multiply
+    auto flush = [&]() __attribute__((always_inline)) {
+      const int2 mine = token_of(s_work[mx]);
+      const float w = __int_as_float(mine.y);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (mine.x >= 0) {
+          v4f* p = sums + ((mine.x >> 16) * RT + r) * 4 + g;
+          v4f v = *p;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] += w * acc[r][i];
+          *p = v;
+        }
+        acc[r] = (v4f){0.f, 0.f, 0.f, 0.f};
+      }
+    };
+    enter_load();
+    static_for<0, D>([&](auto sc) { load(sc, begin + decltype(sc)::value); });
+    for (int u0 = begin; u0 < end; u0 += D) {
+      static_for<0, D>([&](auto sc) __attribute__((always_inline)) {
+        constexpr int S = decltype(sc)::value;
+        if (u0 + S < end) {
+          // row tiles r of chunk i: lo (i = 0) and hi (i = 1) hold theirs
+          const Spread sp = spread_rows(ws[S]);
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            if (U > 1 && mu * U + i >= nch) continue;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              const uint32_t rs = i == 0 ? sp.lo[r] : sp.hi[r];
+              acc[r] = mfma<WF>(operand<WF>(wq[S][r], i), (int)(rs >> (8 * g)), hq[S][i], hs[S][i], acc[r]);
+            }
+          }
+          if (++mu == lines) {
+            flush();
+            mu = 0;
+            ++mx;
           }
         }
-        have[c] = first >= 0;
-        any[c] = __ballot(have[c]) != 0;
-        hrow[c] = a.h + (int64_t)max(first, 0) * N;
-        hsrow[c] = a.hs + (int64_t)max(first, 0) * (N / 32) + g;
-      }
+        load(sc, u0 + S + D);
+      });
     }
-    const v8i wq = load_weight<WF>(wrow, ch, g);
-    const int ws = srow[(int64_t)ch * K * 4];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      if (!any[c]) continue;
-      v8i hq = (v8i){0, 0, 0, 0, 0, 0, 0, 0};
-      int hs = 127;
-      if (have[c]) {
-        const v4i p = *(const v4i*)(hrow[c] + ch * 128 + 16 * g), q = *(const v4i*)(hrow[c] + ch * 128 + 64 + 16 * g);
-        hq = (v8i){p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
-        hs = hsrow[c][ch * 4];
-      }
-      acc[c] = mfma<WF>(wq, ws, hq, hs, acc[c]);
-    }
+    if (mu > 0) flush();
   }
-  flush();
-#pragma unroll
-  for (int c = 0; c < CT; ++c) part[wv][c][lane] = tot[c];
   __syncthreads();
-  for (int c = wv; c < CT; c += kMoeWaves) {
-    const int t = 16 * c + l16;
-    if (t >= a.T) continue;
-    v4f s = part[0][c][lane];
+  for (int i = tid; i < a.T * 4 * RT; i += kMoeThreads) {
+    v4f s = ((const v4f*)smem)[i];
 #pragma unroll
-    for (int v = 1; v < kMoeWaves; ++v) s += part[v][c][lane];
-    *(v2i*)(a.out + (int64_t)t * K + k0 + 4 * g) =
+    for (int v = 1; v < kMoeWaves; ++v) s += ((const v4f*)smem)[(int64_t)v * a.T * 4 * RT + i];
+    *(v2i*)(a.out + (int64_t)(i / (4 * RT)) * K + k0 + 4 * (i % (4 * RT))) =
         (v2i){(int)pack_bf16x2_rne(s[0], s[1]), (int)pack_bf16x2_rne(s[2], s[3])};
   }
 }
 
-template <int WF, int CT>
-static hipError_t launch_moe_ct(const MoeArgs& a, hipStream_t st) {
-  const int64_t slots = std::min<int64_t>(a.E, (int64_t)a.T * a.topk);
-  hipLaunchKernelGGL((moe_gate_up_kernel<WF, CT>), dim3((unsigned)(a.N / kMoeRows), (unsigned)slots), dim3(kMoeThreads),
-                     0, st, a);
-  hipError_t e = hipGetLastError();
+template <int WF, int RT>
+static hipError_t launch_moe(const MoeArgs& a, size_t down, hipStream_t st) {
+  constexpr int DU = 2, DD = 2;
+  const int64_t n = (int64_t)a.T * a.topk, slots = std::min<int64_t>(a.E, n);
+  // x of as many tokens as LDS holds beside the partial sums and the lists
+  const int64_t per_row = a.K / 128 * kRec;
+  const int64_t fit = (kLds - 16384 - kMaxExperts * 4 - kMoeMaxTokens * 8 - 256 - n * 4) / per_row;
+  const int rows = (int)std::min<int64_t>(std::min(a.T, kMoeCols), fit);
+  const size_t up = (size_t)(rows * per_row + n * 4);
+  const int64_t entries = std::min(n, slots + n / rows);      // sum over the hit experts of ceil(tokens / rows)
+  // about one workgroup per CU: x is quantized once for all of its blocks
+  const int64_t all = a.N / kMoeRows;
+  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(8, all * slots / 256));
+  hipError_t e = hipFuncSetAttribute((const void*)moe_gate_up_kernel<WF, DU>,
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)up);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down_kernel<WF, CT>), dim3((unsigned)(a.K / 16)), dim3(kMoeThreads), 0, st, a);
+  e = hipFuncSetAttribute((const void*)moe_down_kernel<WF, RT, DD>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                          (int)down);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((moe_gate_up_kernel<WF, DU>), dim3((unsigned)((all + blocks - 1) / blocks), (unsigned)entries),
+                     dim3(kMoeThreads), up, st, a, rows, blocks);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((moe_down_kernel<WF, RT, DD>), dim3((unsigned)(a.K / (16 * RT))), dim3(kMoeThreads), down, st, a,
+                     (int)slots);
   return hipGetLastError();
 }
 
-// CT: tiles of 16 tokens that the accumulators hold.
-template <int WF>
-static hipError_t launch_moe_wf(const MoeArgs& a, hipStream_t st) {
-  if (a.T <= 16) return launch_moe_ct<WF, 1>(a, st);
-  if (a.T <= 32) return launch_moe_ct<WF, 2>(a, st);
-  if (a.T <= 64) return launch_moe_ct<WF, 4>(a, st);
-  return launch_moe_ct<WF, 8>(a, st);
+// LDS of the down kernel with `rt` column tiles per workgroup.
+static size_t down_lds(const MoeArgs& a, int rt) {
+  const size_t n = (size_t)a.T * a.topk, slots = std::min<size_t>(a.E, n);
+  return (size_t)kMoeWaves * a.T * 64 * rt + n * 8 + (slots + n / kMoeCols) * 8 + (slots + 1) * 4;
 }
 
+// Two column tiles per workgroup of the down kernel (h is read half as often)
+// where the waves' sums of all tokens leave LDS for the lists, else one.
 hipError_t launch_moe_few_tokens(const MoeArgs& a, hipStream_t st) {
-  return a.w_fp4 ? launch_moe_wf<kFmtE2M1>(a, st) : launch_moe_wf<kFmtE4M3>(a, st);
+  const size_t two = down_lds(a, 2);
+  if (two + 64 <= kLds) return a.w_fp4 ? launch_moe<kFmtE2M1, 2>(a, two, st) : launch_moe<kFmtE4M3, 2>(a, two, st);
+  const size_t one = down_lds(a, 1);
+  return a.w_fp4 ? launch_moe<kFmtE2M1, 1>(a, one, st) : launch_moe<kFmtE4M3, 1>(a, one, st);
 }
 
 }  // namespace mxk

@@ -138,7 +138,7 @@ def test_moe_refusals():
     assert call(wf=2) == 2
     assert call(T=129) == 2 and "grouped GEMMs" in _err(lib)
     assert call(T=-1) == 2 and call(k=0) == 2 and call(k=33) == 2 and call(E=0) == 2 and call(E=1025) == 2
-    assert call(K=192) == 2 and call(N=0) == 2 and call(K=(1 << 20) + 128) == 2
+    assert call(K=192) == 2 and call(N=0) == 2 and call(K=(1 << 16) + 128) == 2 and call(N=(1 << 20) + 128) == 2
     for name in ("x", "ids", "c", "q", "s", "out"):
         assert call(**{name: None}) == 1, name
     assert call(x=FAKE + 8) == 3 and call(q=FAKE + 8) == 3 and call(out=FAKE + 8) == 3 and call(ids=FAKE + 2) == 3
@@ -158,3 +158,11 @@ def test_moe_oracle_by_hand():
     out, tol = moe.moe_layer(x, np.array([[0]]), np.array([[0.5]], dtype=np.float32), w13, np.ones((1, K, N)), 0.0)
     h = 2 / (1 + np.exp(-2.0)) * 3                    # 5.28: on the grid of halves, 5.5 (step 0.5 in [4, 8))
     assert abs(h - 5.28) < 0.01 and np.allclose(out, 0.5 * N * 5.5) and (tol < 3).all()
+
+
+def test_moe_refuses_hidden_layers_past_its_offsets():
+    lib = _lib()
+    assert lib.mx_moe_few_tokens_workspace_bytes(128, 32, 1 << 18) > 0
+    assert lib.mx_moe_few_tokens_workspace_bytes(128, 32, (1 << 18) + 128) == 0
+    assert lib.mx_moe_few_tokens(*[FAKE] * 7, 1, 128, 32, 256, (1 << 18) + 128, 4, FAKE, None, FAKE, 1 << 40, None) == 2
+    assert "2^30" in _err(lib)
