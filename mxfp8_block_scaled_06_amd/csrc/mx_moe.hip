@@ -38,6 +38,7 @@ namespace mxk {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kMoeWaves = 8, kMoeThreads = kMoeWaves * 64;
 constexpr int kMoeRows = 32;                       // rows of h per block: one scale block
@@ -133,6 +134,25 @@ __device__ __forceinline__ v4f mfma(const v8i& w, int ws, const v8i& x, int xs, 
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, WF, kFmtE4M3, 0, ws, 0, xs);
 }
 
+// 32 E4M3 elements (two pieces, each of one block) as bf16 values, exactly:
+// four operands of eight for the bf16 instruction.
+__device__ __forceinline__ void to_bf16(const v4i p[2], uint32_t byte0, uint32_t byte1, v8bf out[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float scale = __uint_as_float((i == 0 ? byte0 : byte1) << 23);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)p[i][j], scale, false);
+      const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)p[i][j], scale, true);
+      v8bf& o = out[2 * i + j / 2];
+      o[4 * (j & 1)] = lo[0];
+      o[4 * (j & 1) + 1] = lo[1];
+      o[4 * (j & 1) + 2] = hi[0];
+      o[4 * (j & 1) + 3] = hi[1];
+    }
+  }
+}
+
 // The wave's share of `n` units, within one of its fellows'.
 __device__ __forceinline__ int share(int n, int wv) { return (int)((int64_t)n * wv / kMoeWaves); }
 
@@ -206,6 +226,11 @@ __device__ __forceinline__ v8i read_record(const uint8_t* rec, int g, int& scale
 // stream of weights, D lines of each row ahead and across the blocks, has no
 // load in it that is wanted sooner: x is in LDS by then, and the scales come
 // with the weights, one dword per row and chunk.
+//
+// MXFP8 weights multiply as bf16 here: E4M3 x E4M3 products span so many
+// binades that the block-scaled instruction drops the low bits of small ones
+// (1.5e-4 of the sum of magnitudes on tokens with outliers), which moves some
+// values of h to a neighbouring code.  E4M3 values are bf16 numbers.
 // ---------------------------------------------------------------------------
 template <int WF, int D>
 __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))) void moe_gate_up_kernel(MoeArgs a,
@@ -399,14 +424,32 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
           for (int i = 0; i < U; ++i) {
             // an odd last chunk has no second one: its record is read again, its products dropped
             const int ch = min(u * U + i, nch - 1);
-            int xs;
-            const v8i xq = read_record(rec + ((ch - begin * U) * mp + min(l16, mp - 1)) * kRec, g, xs);
+            const uint8_t* xr = rec + ((ch - begin * U) * mp + min(l16, mp - 1)) * kRec;
             const Spread sc4 = spread_rows(ws[S][i]);
             const uint32_t rs[4] = {sc4.lo[0], sc4.lo[1], sc4.hi[0], sc4.hi[1]};
-            if (U == 1 || u * U + i < nch) {
+            if constexpr (WF == kFmtE2M1) {
+              int xs;
+              const v8i xq = read_record(xr, g, xs);
+              if (u * U + i < nch) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                acc[r] = mfma<WF>(operand<WF>(wq[S][r], i), (int)(rs[r] >> (8 * g)), xq, xs, acc[r]);
+                for (int r = 0; r < 4; ++r)
+                  acc[r] = mfma<WF>(operand<WF>(wq[S][r], i), (int)(rs[r] >> (8 * g)), xq, xs, acc[r]);
+              }
+            } else {
+              // pieces g and g+4 are of blocks g/2 and 2 + g/2
+              const int b4 = 8 * (g >> 1);
+              const v4i xp[2] = {*(const v4i*)(xr + 16 * g), *(const v4i*)(xr + 64 + 16 * g)};
+              const uint32_t xs = *(const uint32_t*)(xr + 128);
+              v8bf x4[4];
+              to_bf16(xp, xs >> b4 & 0xFFu, xs >> (16 + b4) & 0xFFu, x4);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                v8bf w4[4];
+                to_bf16(wq[S][r].p, rs[r] >> b4 & 0xFFu, rs[r] >> (16 + b4) & 0xFFu, w4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w4[j], x4[j], acc[r], 0, 0, 0);
+              }
             }
           }
           load_w(sc);
