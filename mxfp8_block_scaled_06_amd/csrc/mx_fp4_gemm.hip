@@ -14,6 +14,7 @@
 // 4g .. 4g+3.  (32x32x64: l%32, g = l/32, pieces g and g+2, rows
 // 8(r/4) + 4g + r%4.)  Y is the first operand, so a lane holds runs of four
 // output columns of one output row.
+#include <algorithm>
 #include <type_traits>
 
 #include "mx_device.h"
@@ -27,12 +28,11 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 constexpr int kFmtE4M3 = 0, kFmtE2M1 = 4;      // the instruction's operand formats
 
 // ---------------------------------------------------------------------------
-// Few rows per expert: the product streams the weights once and is bound by
-// that.  A workgroup of 8 waves takes 64 rows x 32 columns and splits the
-// contraction: wave w multiplies a contiguous eighth of the 128-element
-// chunks straight from global memory (each weight byte is used by one
-// workgroup row only, so LDS would add a copy and a barrier), and the partial
-// sums meet in LDS, added in wave order.
+// Few output tiles: the product streams the weights once and is bound by that,
+// and 256 x 256 tiles would leave CUs idle.  A workgroup of 8 waves takes 64
+// rows x 32 columns and splits the contraction: each wave multiplies its run of
+// 256-element units (whole 128-byte lines of the weight rows) straight from
+// memory, and the partial sums meet in LDS, added in wave order.
 // ---------------------------------------------------------------------------
 constexpr int kSmBM = 64, kSmBN = 32, kSmWaves = 8;
 constexpr int kSmCT = kSmBM / 16, kSmRT = kSmBN / 16;
@@ -55,41 +55,59 @@ __global__ __launch_bounds__(kSmWaves * 64) void fp4_rows_small_kernel(Fp4GemmAr
   const __amdgpu_buffer_rsrc_t ry = rows::rsrc(a.Y + ((int64_t)e * a.J + j0) * ldy, ny * ldy);
   const uint8_t* sx = a.sX + i0 * 4 + g;
   const uint8_t* sy = a.sY + (int64_t)e * a.J * (a.Kc / 32) + j0 * 4 + g;
-  const int nch = (int)(a.Kc / 128), per = (nch + kSmWaves - 1) / kSmWaves;
+  const int nch = (int)(a.Kc / 128), units = (nch + 1) / 2;
   const int nct = (nx + 15) / 16;     // column tiles that hold rows of the group
   v4f acc[kSmRT][kSmCT];
 #pragma unroll
   for (int r = 0; r < kSmRT; ++r)
 #pragma unroll
     for (int c = 0; c < kSmCT; ++c) acc[r][c] = (v4f){0.f, 0.f, 0.f, 0.f};
-  const int c_end = min((wv + 1) * per, nch);
-  for (int ch = wv * per; ch < c_end; ++ch) {
-    v8i y[kSmRT];
-    int ys[kSmRT];
+  const int end = units * (wv + 1) / kSmWaves;
+  for (int u = units * wv / kSmWaves; u < end; ++u) {
+    v4i y[kSmRT][2], x[kSmCT][2][XF == kFmtE4M3 ? 2 : 1];
+    int ys[kSmRT][2], xs[kSmCT][2];
+    // a line's second chunk past the end is not multiplied
+    const int ch[2] = {2 * u, min(2 * u + 1, nch - 1)};
 #pragma unroll
     for (int r = 0; r < kSmRT; ++r) {
       const int row = 16 * r + l16;
-      const v4i w = __builtin_amdgcn_raw_buffer_load_b128(ry, (int)(row * ldy) + ch * 64 + 16 * g, 0, 0);
-      y[r] = (v8i){w[0], w[1], w[2], w[3], 0, 0, 0, 0};
-      ys[r] = sy[(ch * a.J + min(row, ny - 1)) * 4];      // rows past the end are read as zeros and never stored
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        y[r][i] = __builtin_amdgcn_raw_buffer_load_b128(ry, (int)(row * ldy) + u * 128 + 64 * i + 16 * g, 0, 0);
+        ys[r][i] = sy[(ch[i] * a.J + min(row, ny - 1)) * 4];      // rows past the end are read as zeros and never stored
+      }
     }
 #pragma unroll
     for (int c = 0; c < kSmCT; ++c) {
       if (c >= nct) continue;
       const int row = 16 * c + l16;
-      v8i x;
-      if (XF == kFmtE4M3) {
-        const v4i p = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(row * ldx) + ch * 128 + 16 * g, 0, 0);
-        const v4i q = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(row * ldx) + ch * 128 + 64 + 16 * g, 0, 0);
-        x = (v8i){p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
-      } else {
-        const v4i p = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(row * ldx) + ch * 64 + 16 * g, 0, 0);
-        x = (v8i){p[0], p[1], p[2], p[3], 0, 0, 0, 0};
-      }
-      const int xs = sx[(ch * a.I + min(row, nx - 1)) * 4];
 #pragma unroll
-      for (int r = 0; r < kSmRT; ++r)
-        acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(y[r], x, acc[r][c], kFmtE2M1, XF, 0, ys[r], 0, xs);
+      for (int i = 0; i < 2; ++i) {
+        if (XF == kFmtE4M3) {
+          x[c][i][0] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(row * ldx) + ch[i] * 128 + 16 * g, 0, 0);
+          x[c][i][XF == kFmtE4M3] =
+              __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(row * ldx) + ch[i] * 128 + 64 + 16 * g, 0, 0);
+        } else {
+          x[c][i][0] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(row * ldx) + ch[i] * 64 + 16 * g, 0, 0);
+        }
+        xs[c][i] = sx[(ch[i] * a.I + min(row, nx - 1)) * 4];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kSmCT; ++c) {
+      if (c >= nct) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (2 * u + i >= nch) continue;
+        v8i xv;
+        if (XF == kFmtE4M3) xv = __builtin_shufflevector(x[c][i][0], x[c][i][XF == kFmtE4M3], 0, 1, 2, 3, 4, 5, 6, 7);
+        else xv = __builtin_shufflevector(x[c][i][0], x[c][i][0], 0, 1, 2, 3, -1, -1, -1, -1);
+#pragma unroll
+        for (int r = 0; r < kSmRT; ++r)
+          acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              __builtin_shufflevector(y[r][i], y[r][i], 0, 1, 2, 3, -1, -1, -1, -1), xv, acc[r][c], kFmtE2M1, XF, 0,
+              ys[r][i], 0, xs[c][i]);
+      }
     }
   }
 #pragma unroll
@@ -458,7 +476,15 @@ static hipError_t launch_rows(const Fp4GemmArgs& a, bool small, hipStream_t st) 
 
 hipError_t launch_fp4_gemm(const Fp4GemmArgs& a, hipStream_t st) {
   if (a.I == 0 || a.J == 0) return hipSuccess;
-  const bool small = a.I < 64 * (int64_t)a.E;
+  // The small workgroups while about 2.5 of them per CU cover the output (their
+  // number from the row count alone: each group may add a partial tile), the
+  // large tiles past that.  Measured, E4M3 rows, small / large, us:
+  //   E  1 4096 x 4096:   1 row 7 / 23    256 rows (640) 30 / 38   384 (896) 44 / 38
+  //   E  2 4096 x 5120:   1 row 8 / 27    64 rows (512) 19 / 31    256 (1280) 68 / 47
+  //   E  8 2048 x 7168:   1 row 18 / 36   16 rows (640) 24 / 36    64 (1024) 48 / 41
+  //   E 16 8192 x 5120:   1 row (4352) 124 / 94, 256 rows 1097 / 151
+  const int64_t groups = std::min<int64_t>(a.E, a.I);
+  const bool small = (a.I / kSmBM + groups) * ((a.J + kSmBN - 1) / kSmBN) <= 640;
   if (a.x_fp4) return a.out_f32 ? launch_rows<kFmtE2M1, true>(a, small, st) : launch_rows<kFmtE2M1, false>(a, small, st);
   return a.out_f32 ? launch_rows<kFmtE4M3, true>(a, small, st) : launch_rows<kFmtE4M3, false>(a, small, st);
 }
