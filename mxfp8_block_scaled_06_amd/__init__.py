@@ -10,6 +10,7 @@ Build:  python -m mxfp8_block_scaled_06_amd.build
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -721,6 +722,15 @@ def _scale_shape(scale_layout, lead, R, C):
     raise ValueError("scale_layout must be 'gemm' or 'rowmajor'")
 
 
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(device):
+    """Makes `device` the current one for a launch; no cost where it is."""
+    import torch
+    return _CURRENT if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
 def _same_device(first, *rest):
     """Every tensor on the device of the first one (the kernels run there)."""
     for t in rest:
@@ -740,7 +750,7 @@ def mx_quantize_rowwise_fp4(x, q=None, s=None, scale_layout: str = "rowmajor"):
     s_shape, layout = _scale_shape(scale_layout, x.shape[:-2], R, C)
     q = _out(q, (*x.shape[:-1], C // 2), torch.uint8, x.device, "q")
     s = _out(s, s_shape, torch.uint8, x.device, "s")
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         _check("mx_quantize_rowwise_fp4",
                lib.mx_quantize_rowwise_fp4(_ptr(x), B, R, C, _ptr(q), _ptr(s), layout, _stream(x.device)))
     return q, s
@@ -761,7 +771,7 @@ def mx_dequantize_fp4(q, s, scale_layout: str = "rowmajor", out=None):
         raise ValueError(f"s must have shape {s_shape} for codes {tuple(q.shape)}, got {tuple(s.shape)}")
     _same_device(q, s)
     out = _out(out, (*q.shape[:-1], C), torch.bfloat16, q.device, "out")
-    with torch.cuda.device(q.device):
+    with _on(q.device):
         _check("mx_dequantize_fp4",
                lib.mx_dequantize_fp4(_ptr(q), _ptr(s), B, R, C, layout, _ptr(out), _stream(q.device)))
     return out
@@ -783,7 +793,7 @@ def mx_quantize_weights_fp4(W, q=None, s=None, q_t=None, s_t=None):
     s = _out(s, (E, K // 128, N, 4), torch.uint8, dev, "s")
     q_t = _out(q_t, (E, K, N // 2), torch.uint8, dev, "q_t")
     s_t = _out(s_t, (E, N // 128, K, 4), torch.uint8, dev, "s_t")
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check("mx_quantize_weights_fp4", lib.mx_quantize_weights_fp4(_ptr(W), E, N, K, _ptr(q), _ptr(s), _ptr(q_t),
                                                                       _ptr(s_t), _stream(dev)))
     return q, s, q_t, s_t
@@ -840,7 +850,7 @@ def mx_grouped_gemm_mxfp4(X, sX, Y, sY, offs, x_format: str = "mxfp8", row_map=N
     if out is None and row_map is not None:
         out = torch.zeros((c_rows, J), dtype=out_dtype, device=X.device)
     out = _out(out, (c_rows, J), out_dtype, X.device, "out")
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         _check("mx_grouped_gemm_mxfp4",
                lib.mx_grouped_gemm_mxfp4(_ptr(X), _ptr(sX), fmt, _ptr(Y), _ptr(sY), SCALES_GEMM, _ptr(offs), I, J, Kc,
                                          E, _ptr(row_map), int(c_rows), _ptr(out), int(out_dtype == torch.float32),
@@ -877,7 +887,7 @@ def _mm_fp4(name, a, q, s, offs, act_format, out, ws):
     _require(ws, torch.uint8, "ws")
     _same_device(a, ws)
     sizes = (M, J, C) if name == "mx_grouped_mm_fwd_fp4" else (M, C, J)
-    with torch.cuda.device(a.device):
+    with _on(a.device):
         _check(name, getattr(lib, name)(_ptr(a), _ptr(q), _ptr(s), _ptr(offs), *sizes, E, fmt, _ptr(out), _ptr(ws),
                                         ws.numel(), _stream(a.device)))
     return out
@@ -955,7 +965,7 @@ def mx_moe_few_tokens(x, expert_idx, combine, w13, w2, weight_format: str = "mxf
         _require(ws, torch.uint8, "ws")
         _same_device(x, ws)
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check("mx_moe_few_tokens",
                lib.mx_moe_few_tokens(_ptr(x), _ptr(expert_idx), _ptr(combine), _ptr(q13), _ptr(s13), _ptr(q2),
                                      _ptr(s2), fmt, T, topk, K, N, E, _ptr(out), _ptr(status), _ptr(ws), ws.numel(),

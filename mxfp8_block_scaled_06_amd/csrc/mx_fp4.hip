@@ -43,25 +43,53 @@ __device__ __forceinline__ uint32_t quant8_fp4(v4i w, uint32_t byte) {
   return byte == 0xFFu ? 0u : c;
 }
 
-// Index of block `kb` of row `r` (row of its batch entry `b`) in the scales:
-// row-major [rows][KB], or with rows_per_batch > 0 the GEMM layout
-// [batch][KB/4][rows_per_batch][4].
-__device__ __forceinline__ int64_t scale_index(int64_t block, int64_t kb_per_row, int64_t rows_per_batch) {
-  if (rows_per_batch == 0) return block;
-  const int64_t r = block / kb_per_row, kb = block - r * kb_per_row;
-  const int64_t b = r / rows_per_batch, rr = r - b * rows_per_batch;
-  return (b * (kb_per_row >> 2) + (kb >> 2)) * rows_per_batch * 4 + rr * 4 + (kb & 3);
+constexpr int kF4Threads = 256;
+
+// Two ways over the values, 8 of them (a chunk) per lane and step, a DPP quad on
+// one block.  Row-major scales: chunks in order, scale of chunk c at c / 4.  GEMM
+// scales [batch][cols/128][rows][4]: tiles of 256 columns (whole 128-byte lines
+// of codes) x 8 NC rows, so that a tile's scales are two runs of 4 bytes per
+// row; with the chunks in order every lane computed its scale's place with two
+// 64-bit divisions and a wave's 16 scales lay in four far lines.
+constexpr int kT4Cols = 256, kT4Rows = kF4Threads / 32;   // rows of one step
+// Steps per workgroup: 8 keep enough loads in flight for the bandwidth, 1 spreads
+// a small input over the CUs.
+constexpr int kT4Steps = 8;
+
+inline int t4_steps(int64_t batch, int64_t rows, int64_t cols) {
+  return batch * ((rows + kT4Rows * kT4Steps - 1) / (kT4Rows * kT4Steps)) * ((cols + kT4Cols - 1) / kT4Cols) >= 1024
+             ? kT4Steps
+             : 1;
+}
+
+inline dim3 t4_grid(int64_t batch, int64_t rows, int64_t cols, int steps) {
+  return dim3((unsigned)(batch * ((rows + kT4Rows * steps - 1) / (kT4Rows * steps)) * ((cols + kT4Cols - 1) / kT4Cols)));
+}
+
+// A workgroup's tile: batch entry, first row and first column, column tiles
+// fastest.
+struct Tile4 {
+  int64_t b, r0;
+  int k0;
+};
+template <int NC>
+__device__ __forceinline__ Tile4 tile4(int64_t rows, int cols) {
+  const uint32_t kt = (uint32_t)(cols + kT4Cols - 1) / kT4Cols;
+  const uint32_t rt = (uint32_t)((rows + kT4Rows * NC - 1) / (kT4Rows * NC));
+  const uint32_t t = blockIdx.x / kt;
+  Tile4 o;
+  o.k0 = (int)(blockIdx.x - t * kt) * kT4Cols;
+  o.b = t / rt;
+  o.r0 = (int64_t)(t - (uint32_t)o.b * rt) * (kT4Rows * NC);
+  return o;
 }
 
 // ---------------------------------------------------------------------------
-// Rowwise: one 16-byte chunk (8 values) per lane, a DPP quad holds one block.
+// Rowwise quantizer.
 // ---------------------------------------------------------------------------
-constexpr int kF4Threads = 256;
-
 __global__ __launch_bounds__(kF4Threads) void quant_rowwise_fp4_kernel(const uint16_t* __restrict__ x,
                                                                        int64_t nchunks, uint8_t* __restrict__ q,
-                                                                       uint8_t* __restrict__ s, int64_t kb_per_row,
-                                                                       int64_t rows_per_batch) {
+                                                                       uint8_t* __restrict__ s) {
   const int64_t idx = (int64_t)blockIdx.x * kF4Threads + threadIdx.x;
   v4i w = (v4i){0, 0, 0, 0};
   if (idx < nchunks) w = __builtin_nontemporal_load((const v4i*)(x + idx * 8));
@@ -69,7 +97,39 @@ __global__ __launch_bounds__(kF4Threads) void quant_rowwise_fp4_kernel(const uin
   const uint32_t byte = e8m0_fp4_from_absbits(quad_max(absmax8(w)));
   if (idx < nchunks) {
     *(uint32_t*)(q + idx * 4) = quant8_fp4(w, byte);
-    if ((threadIdx.x & 3) == 0) s[scale_index(idx >> 2, kb_per_row, rows_per_batch)] = (uint8_t)byte;
+    if ((threadIdx.x & 3) == 0) s[idx >> 2] = (uint8_t)byte;
+  }
+}
+
+template <int NC>
+__global__ __launch_bounds__(kF4Threads) void quant_tiles_fp4_kernel(const uint16_t* __restrict__ x, int64_t rows,
+                                                                     int cols, uint8_t* __restrict__ q,
+                                                                     uint8_t* __restrict__ s) {
+  __shared__ uint8_t sc[2][kT4Rows * NC][4];     // [chunk of 128][row][block]
+  const Tile4 t = tile4<NC>(rows, cols);
+  const int pc = threadIdx.x & 31, r = threadIdx.x >> 5;
+  const bool k_in = t.k0 + 8 * pc < cols;
+  v4i w[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int64_t row = t.r0 + kT4Rows * i + r;
+    w[i] = (v4i){0, 0, 0, 0};
+    if (k_in && row < rows)
+      w[i] = __builtin_nontemporal_load((const v4i*)(x + (t.b * rows + row) * cols + t.k0 + 8 * pc));
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int64_t row = t.r0 + kT4Rows * i + r;
+    const uint32_t byte = e8m0_fp4_from_absbits(quad_max(absmax8(w[i])));
+    if (k_in && row < rows) *(uint32_t*)(q + ((t.b * rows + row) * cols + t.k0) / 2 + 4 * pc) = quant8_fp4(w[i], byte);
+    if ((pc & 3) == 0) sc[pc >> 4][kT4Rows * i + r][(pc >> 2) & 3] = (uint8_t)byte;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * kT4Rows * NC; i += kF4Threads) {
+    const int ch = i / (kT4Rows * NC), rr = i % (kT4Rows * NC);
+    if (t.k0 + 128 * ch < cols && t.r0 + rr < rows)
+      *(uint32_t*)(s + (t.b * (cols / 128) + t.k0 / 128 + ch) * rows * 4 + (t.r0 + rr) * 4) =
+          *(const uint32_t*)sc[ch][rr];
   }
 }
 
@@ -77,8 +137,18 @@ hipError_t launch_quant_rowwise_fp4(const uint16_t* x, int64_t rows_total, int64
                                     int64_t gemm_rows_per_batch, hipStream_t st) {
   const int64_t nchunks = rows_total * (cols / 8);
   if (nchunks == 0) return hipSuccess;
-  hipLaunchKernelGGL(quant_rowwise_fp4_kernel, dim3((unsigned)((nchunks + kF4Threads - 1) / kF4Threads)),
-                     dim3(kF4Threads), 0, st, x, nchunks, q, s, cols / 32, gemm_rows_per_batch);
+  if (gemm_rows_per_batch == 0) {
+    hipLaunchKernelGGL(quant_rowwise_fp4_kernel, dim3((unsigned)((nchunks + kF4Threads - 1) / kF4Threads)),
+                       dim3(kF4Threads), 0, st, x, nchunks, q, s);
+    return hipGetLastError();
+  }
+  const int64_t rows = gemm_rows_per_batch, batch = rows_total / rows;
+  const int steps = t4_steps(batch, rows, cols);
+  const dim3 grid = t4_grid(batch, rows, cols, steps);
+  if (steps == kT4Steps)
+    hipLaunchKernelGGL(quant_tiles_fp4_kernel<kT4Steps>, grid, dim3(kF4Threads), 0, st, x, rows, (int)cols, q, s);
+  else
+    hipLaunchKernelGGL(quant_tiles_fp4_kernel<1>, grid, dim3(kF4Threads), 0, st, x, rows, (int)cols, q, s);
   return hipGetLastError();
 }
 
@@ -104,26 +174,64 @@ __device__ __forceinline__ uint32_t dequant2_bits(uint32_t codes, uint32_t byte)
   return out;
 }
 
+__device__ __forceinline__ v4i dequant8(uint32_t codes, uint32_t byte) {
+  v4i o;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) o[d] = (int)dequant2_bits(codes >> (8 * d), byte);
+  return o;
+}
+
 __global__ __launch_bounds__(kF4Threads) void dequant_fp4_kernel(const uint8_t* __restrict__ q,
                                                                  const uint8_t* __restrict__ s, int64_t nchunks,
-                                                                 uint16_t* __restrict__ out, int64_t kb_per_row,
-                                                                 int64_t rows_per_batch) {
+                                                                 uint16_t* __restrict__ out) {
   const int64_t idx = (int64_t)blockIdx.x * kF4Threads + threadIdx.x;
   if (idx >= nchunks) return;
   const uint32_t c = *(const uint32_t*)(q + idx * 4);
-  const uint32_t byte = s[scale_index(idx >> 2, kb_per_row, rows_per_batch)];
-  v4i o;
+  __builtin_nontemporal_store(dequant8(c, s[idx >> 2]), (v4i*)(out + idx * 8));
+}
+
+template <int NC>
+__global__ __launch_bounds__(kF4Threads) void dequant_tiles_fp4_kernel(const uint8_t* __restrict__ q,
+                                                                       const uint8_t* __restrict__ s, int64_t rows,
+                                                                       int cols, uint16_t* __restrict__ out) {
+  const Tile4 t = tile4<NC>(rows, cols);
+  const int pc = threadIdx.x & 31, r = threadIdx.x >> 5;
+  if (t.k0 + 8 * pc >= cols) return;
+  const uint8_t* sb = s + (t.b * (cols / 128) + t.k0 / 128 + (pc >> 4)) * rows * 4 + ((pc >> 2) & 3);
+  uint32_t c[NC], byte[NC];
 #pragma unroll
-  for (int d = 0; d < 4; ++d) o[d] = (int)dequant2_bits(c >> (8 * d), byte);
-  __builtin_nontemporal_store(o, (v4i*)(out + idx * 8));
+  for (int i = 0; i < NC; ++i) {
+    const int64_t row = t.r0 + kT4Rows * i + r;
+    c[i] = byte[i] = 0;
+    if (row < rows) {
+      c[i] = *(const uint32_t*)(q + ((t.b * rows + row) * cols + t.k0) / 2 + 4 * pc);
+      byte[i] = sb[row * 4];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int64_t row = t.r0 + kT4Rows * i + r;
+    if (row < rows)
+      __builtin_nontemporal_store(dequant8(c[i], byte[i]), (v4i*)(out + (t.b * rows + row) * cols + t.k0 + 8 * pc));
+  }
 }
 
 hipError_t launch_dequant_fp4(const uint8_t* q, const uint8_t* s, int64_t rows_total, int64_t cols, uint16_t* out,
                               int64_t gemm_rows_per_batch, hipStream_t st) {
   const int64_t nchunks = rows_total * (cols / 8);
   if (nchunks == 0) return hipSuccess;
-  hipLaunchKernelGGL(dequant_fp4_kernel, dim3((unsigned)((nchunks + kF4Threads - 1) / kF4Threads)), dim3(kF4Threads),
-                     0, st, q, s, nchunks, out, cols / 32, gemm_rows_per_batch);
+  if (gemm_rows_per_batch == 0) {
+    hipLaunchKernelGGL(dequant_fp4_kernel, dim3((unsigned)((nchunks + kF4Threads - 1) / kF4Threads)), dim3(kF4Threads),
+                       0, st, q, s, nchunks, out);
+    return hipGetLastError();
+  }
+  const int64_t rows = gemm_rows_per_batch, batch = rows_total / rows;
+  const int steps = t4_steps(batch, rows, cols);
+  const dim3 grid = t4_grid(batch, rows, cols, steps);
+  if (steps == kT4Steps)
+    hipLaunchKernelGGL(dequant_tiles_fp4_kernel<kT4Steps>, grid, dim3(kF4Threads), 0, st, q, s, rows, (int)cols, out);
+  else
+    hipLaunchKernelGGL(dequant_tiles_fp4_kernel<1>, grid, dim3(kF4Threads), 0, st, q, s, rows, (int)cols, out);
   return hipGetLastError();
 }
 
