@@ -15,7 +15,7 @@
 // quantization and the weighted sum happen inside them:
 //   moe_gate_up_kernel  32 gate and 32 up rows of one hit expert per
 //                       workgroup (one block of h), for all its tokens;
-//   moe_down_kernel     16 output columns per workgroup, all hit experts, all
+//   moe_down_kernel     32 or 16 output columns per workgroup, all hit experts, all
 //                       tokens; the sum over a token's experts stays in fp32
 //                       on the CU, so nothing is added through memory and the
 //                       order of additions is fixed.
@@ -26,7 +26,8 @@
 // Matrix operand layout (v_mfma_scale_f32_16x16x128_f8f6f4): lane l holds row
 // l%16, group g = l/16: E2M1 elements 32g..32g+31 in 16 bytes, E4M3 the
 // 16-byte pieces g and g+4; its scale byte is block g's; its accumulators are
-// column l%16, rows 4g..4g+3.  Weights are the first operand (rows), tokens
+// column l%16, rows 4g..4g+3 (as with v_mfma_f32_16x16x32_bf16, which takes 8
+// elements a lane, the same ones of both operands).  Weights are the first operand (rows), tokens
 // the second (columns).
 #include <algorithm>
 #include <type_traits>
@@ -134,26 +135,42 @@ __device__ __forceinline__ v4f mfma(const v8i& w, int ws, const v8i& x, int xs, 
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, WF, kFmtE4M3, 0, ws, 0, xs);
 }
 
-// 32 E4M3 elements (two pieces, each of one block) as bf16 values, exactly:
-// four operands of eight for the bf16 instruction.
-__device__ __forceinline__ void to_bf16(const v4i p[2], uint32_t byte0, uint32_t byte1, v8bf out[4]) {
+// The lane's 32 elements of a chunk as bf16 values, four operands of eight for
+// the bf16 instruction.  Exact: E4M3 and E2M1 values times a power of two are
+// bf16 numbers (NaN at scale byte 255; elements the library's quantizers made
+// of bf16 values stay in range).
+__device__ __forceinline__ void put_pair(v8bf& o, int at, bf16x2_t v) {
+  o[at] = v[0];
+  o[at + 1] = v[1];
+}
+// E4M3: two 16-byte pieces, each of one block.
+__device__ __forceinline__ void to_bf16(const v4i p[2], float scale0, float scale1, v8bf out[4]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float scale = __uint_as_float((i == 0 ? byte0 : byte1) << 23);
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)p[i][j], scale, false);
-      const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)p[i][j], scale, true);
+      const float scale = i == 0 ? scale0 : scale1;
       v8bf& o = out[2 * i + j / 2];
-      o[4 * (j & 1)] = lo[0];
-      o[4 * (j & 1) + 1] = lo[1];
-      o[4 * (j & 1) + 2] = hi[0];
-      o[4 * (j & 1) + 3] = hi[1];
+      put_pair(o, 4 * (j & 1), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)p[i][j], scale, false));
+      put_pair(o, 4 * (j & 1) + 2, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)p[i][j], scale, true));
     }
+}
+// E2M1: one 16-byte piece of one block.
+__device__ __forceinline__ void to_bf16(const v4i& p, float scale, v8bf out[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    put_pair(out[i], 0, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)p[i], scale, 0));
+    put_pair(out[i], 2, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)p[i], scale, 1));
+    put_pair(out[i], 4, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)p[i], scale, 2));
+    put_pair(out[i], 6, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)p[i], scale, 3));
   }
 }
+// 2^(byte - 127) of byte `i` of four, for the converts (byte 0: as they read it).
+__device__ __forceinline__ float scale_of(uint32_t bytes, int i) {
+  return __uint_as_float((bytes >> (8 * i) & 0xFFu) << 23);
+}
 
-// The wave's share of `n` units, within one of its fellows'.
+// First of the wave's `n` units; shares differ by one unit at most.
 __device__ __forceinline__ int share(int n, int wv) { return (int)((int64_t)n * wv / kMoeWaves); }
 
 // Workgroup barrier that orders LDS accesses and leaves loads from memory in
@@ -204,16 +221,9 @@ __device__ __forceinline__ us2 absmax8x2(v4i w) {
 }
 
 // 128 consecutive MXFP8 elements of a token in LDS: the codes, then the four
-// scale bytes.  144 bytes apart, one 16-byte piece of 16 tokens falls into 16
-// different banks groups.
+// scale bytes.  144 bytes apart, the same 16-byte piece of eight consecutive
+// tokens covers all banks.
 constexpr int kRec = 144;
-
-// The lane's operand from a record: pieces g and g+4, scale byte g.
-__device__ __forceinline__ v8i read_record(const uint8_t* rec, int g, int& scale) {
-  const v4i p = *(const v4i*)(rec + 16 * g), q = *(const v4i*)(rec + 64 + 16 * g);
-  scale = rec[128 + g];
-  return (v8i){p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
-}
 
 // ---------------------------------------------------------------------------
 // Gate and up projection, SwiGLU and the quantization of h.  A workgroup takes
@@ -227,10 +237,11 @@ __device__ __forceinline__ v8i read_record(const uint8_t* rec, int g, int& scale
 // load in it that is wanted sooner: x is in LDS by then, and the scales come
 // with the weights, one dword per row and chunk.
 //
-// MXFP8 weights multiply as bf16 here: E4M3 x E4M3 products span so many
-// binades that the block-scaled instruction drops the low bits of small ones
-// (1.5e-4 of the sum of magnitudes on tokens with outliers), which moves some
-// values of h to a neighbouring code.  E4M3 values are bf16 numbers.
+// The products are bf16 ones here, of the exact values: the block-scaled
+// instruction drops the low bits of small products beside large ones (1.5e-4 of
+// the sum of magnitudes on tokens with outliers), which moved values of h to a
+// neighbouring code, and with one or seven tokens the output's error from 0.0017
+// to 0.0042 and 0.0027.  It costs 21.9 -> 23.1 us (1 token) and 127 -> 130 (7).
 // ---------------------------------------------------------------------------
 template <int WF, int D>
 __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))) void moe_gate_up_kernel(MoeArgs a,
@@ -427,25 +438,20 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
             const uint8_t* xr = rec + ((ch - begin * U) * mp + min(l16, mp - 1)) * kRec;
             const Spread sc4 = spread_rows(ws[S][i]);
             const uint32_t rs[4] = {sc4.lo[0], sc4.lo[1], sc4.hi[0], sc4.hi[1]};
-            if constexpr (WF == kFmtE2M1) {
-              int xs;
-              const v8i xq = read_record(xr, g, xs);
-              if (u * U + i < nch) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  acc[r] = mfma<WF>(operand<WF>(wq[S][r], i), (int)(rs[r] >> (8 * g)), xq, xs, acc[r]);
-              }
-            } else {
-              // pieces g and g+4 are of blocks g/2 and 2 + g/2
-              const int b4 = 8 * (g >> 1);
-              const v4i xp[2] = {*(const v4i*)(xr + 16 * g), *(const v4i*)(xr + 64 + 16 * g)};
-              const uint32_t xs = *(const uint32_t*)(xr + 128);
-              v8bf x4[4];
-              to_bf16(xp, xs >> b4 & 0xFFu, xs >> (16 + b4) & 0xFFu, x4);
+            // elements 32g.. of E2M1, one block; pieces g and g+4 of E4M3, of
+            // blocks g/2 and 2 + g/2
+            constexpr bool F4 = WF == kFmtE2M1;
+            const int s0 = F4 ? g : g >> 1, s1 = F4 ? g : 2 + (g >> 1);
+            const v4i xp[2] = {*(const v4i*)(xr + (F4 ? 32 : 16) * g), *(const v4i*)(xr + (F4 ? 32 * g + 16 : 64 + 16 * g))};
+            const uint32_t xs = *(const uint32_t*)(xr + 128);
+            v8bf x4[4];
+            to_bf16(xp, scale_of(xs, s0), scale_of(xs, s1), x4);
+            if (u * U + i < nch) {
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 v8bf w4[4];
-                to_bf16(wq[S][r].p, rs[r] >> b4 & 0xFFu, rs[r] >> (16 + b4) & 0xFFu, w4);
+                if constexpr (F4) to_bf16(wq[S][r].p[i], scale_of(rs[r], s0), w4);
+                else to_bf16(wq[S][r].p, scale_of(rs[r], s0), scale_of(rs[r], s1), w4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                   acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w4[j], x4[j], acc[r], 0, 0, 0);
