@@ -173,7 +173,7 @@ def _out(t, shape, dtype, device, name):
     """An output buffer: allocated when None, else checked to be exactly what
     the kernel writes (the C ABI sees only a pointer and cannot)."""
     import torch
-    shape = tuple(int(d) for d in shape)
+    shape = tuple(map(int, shape))
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if isinstance(t, torch.Tensor) and tuple(t.shape) != shape:

@@ -13,15 +13,14 @@
 // the registers of the matrix instruction, and 16 tokens cost no more of them
 // than one.  Two kernels, since the down projection needs all of h; grouping,
 // quantization and the weighted sum happen inside them:
-//   moe_gate_up_kernel  32 gate and 32 up rows of one hit expert per
-//                       workgroup (one block of h), for all its tokens;
+//   moe_gate_up_kernel  blocks of 32 gate and 32 up rows of the hit experts (one
+//                       scale block of h), for 16 or 32 of their tokens;
 //   moe_down_kernel     32 or 16 output columns per workgroup, all hit experts, all
 //                       tokens; the sum over a token's experts stays in fp32
 //                       on the CU, so nothing is added through memory and the
 //                       order of additions is fixed.
-// Both split their contraction over the eight waves of the workgroup and add
-// the partial sums in wave order.  A wave keeps the next chunks of its weights
-// in flight while it multiplies one.
+// Partial sums of several waves are added in wave order.  A wave keeps the next
+// lines of its weights in flight while it multiplies one.
 //
 // Matrix operand layout (v_mfma_scale_f32_16x16x128_f8f6f4): lane l holds row
 // l%16, group g = l/16: E2M1 elements 32g..32g+31 in 16 bytes, E4M3 the
@@ -220,17 +219,24 @@ __device__ __forceinline__ us2 absmax8x2(v4i w) {
   return m;
 }
 
-// 128 consecutive MXFP8 elements of a token in LDS: the codes, then the four
-// scale bytes.  144 bytes apart, the same 16-byte piece of eight consecutive
-// tokens covers all banks.
-constexpr int kRec = 144;
+// x in LDS: 128 codes (eight 16-byte pieces) per token and chunk, and the four
+// scale bytes in an array of their own.  Piece p of token i is at p ^ i % 8: the
+// same piece of eight consecutive tokens covers all banks.
+constexpr int kCodes = 128, kRec = kCodes + 4;
+__device__ __forceinline__ int piece(int token, int p) { return 16 * (p ^ (token & 7)); }
 
 // ---------------------------------------------------------------------------
-// Gate and up projection, SwiGLU and the quantization of h.  A workgroup takes
-// `blocks` consecutive 32-row blocks of one work entry: one hit expert with up
-// to `rows` of its tokens, whose x it quantizes into LDS once for all blocks.
-// An expert with more tokens has another entry; the two run side by side and
-// share the weights in L2.
+// Gate and up projection, SwiGLU and the quantization of h.
+//
+// A work entry is one hit expert with up to `rows` of its tokens (as many as
+// LDS holds x of, 16 CT at most); the work is all entries' 32-row blocks of h,
+// in order, dealt to the workgroups in equal runs, and a run's lines of weights
+// to its eight waves in equal runs again.  A wave so has whole blocks, which it
+// finishes alone, and at most a part of one at each end; those meet in LDS once,
+// at the end of the run.  (With every block split over the eight waves, 28 lines
+// of E2M1 made shares of 3 and 4, and all waves waited at every block: 128
+// tokens, top 8 of 32 experts, K 7168, N 2048: 393 us the layer, 351 with whole
+// blocks.)
 //
 // Loads from memory are waited for in the order of their issue, so the wave's
 // stream of weights, D lines of each row ahead and across the blocks, has no
@@ -243,167 +249,190 @@ constexpr int kRec = 144;
 // neighbouring code, and with one or seven tokens the output's error from 0.0017
 // to 0.0042 and 0.0027.  It costs 21.9 -> 23.1 us (1 token) and 127 -> 130 (7).
 // ---------------------------------------------------------------------------
-template <int WF, int D>
+constexpr int kMoeGrid = 256;      // workgroups of the gate kernel, one per CU
+static_assert(kMoeGrid == 1 << 8, "shares are taken by shifts");
+
+template <int WF, int CT, int D>
 __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))) void moe_gate_up_kernel(MoeArgs a,
-                                                                                                          int rows,
-                                                                                                          int blocks) {
+                                                                                                          int rows) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ v4f part[kMoeWaves][2][64];
-  __shared__ int s_count[kMaxExperts];
-  __shared__ int s_item[kMoeMaxTokens], s_token[kMoeMaxTokens], s_expert, s_pass;
+  __shared__ int s_count[kMaxExperts], s_upto[kMaxExperts];
+  __shared__ int s_item[kMoeMaxTokens], s_token[kMoeMaxTokens], s_expert, s_pass, s_total;
   constexpr int U = kUnit<WF>;
+  constexpr bool F4 = WF == kFmtE2M1;
   const int tid = threadIdx.x, lane = tid & 63, wv = uni(tid >> 6), l16 = lane & 15, g = lane >> 4;
   const int64_t K = a.K, N = a.N;
-  const int nch = (int)(K / 128), units = (nch + U - 1) / U;
+  const int nch = (int)(K / 128), lines = (nch + U - 1) / U, all = (int)(N / kMoeRows);
+  const int ldw = (int)(F4 ? K / 2 : K);
+  // x in LDS, [chunk][token]: codes, scales
+  uint32_t* rsc = (uint32_t*)(smem + nch * rows * kCodes);
   int* s_ids = (int*)(smem + nch * rows * kRec);
   load_ids(a, s_ids, s_count);
-  if (wv == 0) {
-    // the blockIdx.y-th work entry, experts in ascending order; how many experts
-    // are hit, and how many of them and of their tokens come before this one
-    int hit = 0, entries = 0, e = -1, pass = 0, rank = 0, off = 0;
-    for (int base = 0; base < a.E; base += 64) {
-      const int c = base + lane < a.E ? s_count[base + lane] : 0, p = (c + rows - 1) / rows;
-      int ip = p;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(ip, d);
-        if (lane >= d) ip += v;
-      }
-      const uint64_t mask = __ballot(c > 0), own = __ballot(entries + ip > (int)blockIdx.y);
-      if (e < 0) {
-        const int at = own ? __builtin_ctzll(own) : 64;      // the first expert whose entries reach past it
-        int before = lane < at ? c : 0;
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) before += __shfl_xor(before, d);
-        off += before;
-        rank += __builtin_popcountll(at < 64 ? mask & ((1ull << at) - 1) : mask);
-        if (own) {
-          e = base + at;
-          pass = (int)blockIdx.y - entries - __shfl(ip - p, at);
-        }
-      }
-      entries += __shfl(ip, 63);
-      hit += __builtin_popcountll(mask);
+  // Work entry `entry` for the workgroup, by wave 0: its expert, pass and tokens;
+  // by the one that has the entry's first block, what the down kernel needs.
+  auto enter = [&](int entry, bool first_block) __attribute__((always_inline)) {
+    int e = -1, rank = 0, prev = 0;      // rank: hit experts before it
+    for (int base = 0; e < 0; base += 64) {
+      const int i = base + lane;
+      const uint64_t own = __ballot(i < a.E && (s_upto[min(i, a.E - 1)] & 0xFFFF) > entry);
+      const uint64_t hits = __ballot(i < a.E && s_count[min(i, a.E - 1)] > 0);
+      const int first = own ? __builtin_ctzll(own) : 64;
+      rank += __builtin_popcountll(own ? hits & ((1ull << first) - 1) : hits);
+      if (own) e = base + first;
     }
+    if (e > 0) prev = s_upto[e - 1];
+    const int pass = entry - (prev & 0xFFFF), off = prev >> 16;
+    const bool leave = first_block && pass == 0;
+    const int m = tokens_of(a, s_ids, e, [&](int i, int t, int j) {
+      s_token[i] = t;
+      s_item[i] = t * a.topk + j;
+      if (leave) {
+        // the row of h, the token and its weight (the sum, where it names the
+        // expert twice)
+        float c = 0.f;
+        for (int k = 0; k < a.topk; ++k)
+          if (s_ids[t * a.topk + k] == e) c += a.combine[t * a.topk + k];
+        a.list[off + i] = make_int2((t * a.topk + j) | t << 16, __float_as_int(c));
+      }
+    });
     if (lane == 0) {
+      if (leave) a.meta[1 + rank] = e | m << 16;
       s_expert = e;
       s_pass = pass;
-      if (blockIdx.x == 0 && blockIdx.y == 0) a.meta[0] = hit;
     }
-    if (e >= 0) {
-      const bool leave = blockIdx.x == 0 && pass == 0;
-      const int m = tokens_of(a, s_ids, e, [&](int i, int t, int j) {
-        s_token[i] = t;
-        s_item[i] = t * a.topk + j;
-        if (leave) {
-          // for the down kernel: the row of h, the token and its weight (the
-          // sum, where it names the expert twice)
-          float c = 0.f;
-          for (int k = 0; k < a.topk; ++k)
-            if (s_ids[t * a.topk + k] == e) c += a.combine[t * a.topk + k];
-          a.list[off + i] = make_int2((t * a.topk + j) | t << 16, __float_as_int(c));
-        }
-      });
-      if (leave && lane == 0) a.meta[1 + rank] = e | m << 16;
+  };
+  const uint32_t wg = blockIdx.x;
+  if (wv == 0) {
+    // entries (low half) and tokens (high half) of the experts up to each one:
+    // at most 4096 of both
+    int before = 0, hit = 0;
+    for (int base = 0; base < a.E; base += 64) {
+      const int c = base + lane < a.E ? s_count[base + lane] : 0;
+      int v = (c + rows - 1) / rows | c << 16;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int w = __shfl_up(v, d);
+        if (lane >= d) v += w;
+      }
+      v += before;
+      if (base + lane < a.E) s_upto[base + lane] = v;
+      before = __shfl(v, 63);
+      hit += __builtin_popcountll(__ballot(c > 0));
     }
+    const uint32_t total = (uint32_t)(uni(before) & 0xFFFF) * all;
+    if (lane == 0) {
+      s_total = (int)total;
+      if (wg == 0) a.meta[0] = hit;
+    }
+    const uint32_t at = (uint64_t)total * wg >> 8;
+    if (at < (uint32_t)((uint64_t)total * (wg + 1) >> 8)) enter(at / all, at % all == 0);
   }
   __syncthreads();
-  const int e = uni(s_expert);
-  if (e < 0) return;
-  const int m0 = uni(s_pass) * rows, mp = min(uni(s_count[e]) - m0, rows);
-  const int begin = share(units, wv), end = share(units, wv + 1), count = end - begin;
-  const int b0 = blockIdx.x * blocks, nb = min(blocks, (int)(N / kMoeRows) - b0);
-  const int ldw = (int)(WF == kFmtE2M1 ? K / 2 : K);
-  const uint8_t* wbase = a.q13 + ((int64_t)e * 2 * N + (int64_t)b0 * kMoeRows) * ldw;
-  // scales: lane l's row is gate row l or up row l - 32
-  const uint8_t* sbase = a.s13 + (int64_t)e * 2 * N * (K / 32) +
-                         ((int64_t)b0 * kMoeRows + (lane < 32 ? lane : N + lane - 32)) * 4;
+  const uint32_t total = (uint32_t)uni(s_total);
+  const int start = (int)((uint64_t)total * wg >> 8), stop = (int)((uint64_t)total * (wg + 1) >> 8);
+  for (int at = start; at < stop;) {
+    const int entry = at / all, b0 = at - entry * all, nb = min(all - b0, stop - at);
+    if (at > start) {
+      __syncthreads();      // the lists and x of the entry before
+      if (wv == 0) enter(entry, true);
+      __syncthreads();
+    }
+    at += nb;
+    const int e = uni(s_expert);
+    // an expert's entries share its tokens evenly: a second column tile only
+    // where the first one is full
+    const int me = uni(s_count[e]), passes = (me + rows - 1) / rows, per = (me + passes - 1) / passes;
+    const int m0 = uni(s_pass) * per, mp = min(me - m0, per);
+    const bool wide = CT > 1 && mp > kMoeCols;        // a second column tile has tokens
+    const uint8_t* wbase = a.q13 + ((int64_t)e * 2 * N + (int64_t)b0 * kMoeRows) * ldw;
+    // scales: lane l's row is gate row l or up row l - 32
+    const uint8_t* sbase = a.s13 + (int64_t)e * 2 * N * (K / 32) +
+                           ((int64_t)b0 * kMoeRows + (lane < 32 ? lane : N + lane - 32)) * 4;
+    // the wave's lines
+    const int begin = share(nb * lines, wv), end = share(nb * lines, wv + 1);
 
-  const int tasks = (min(end * U, nch) - begin * U) * mp;
-  uint8_t* rec = smem + begin * U * mp * kRec;      // [chunk][token]; the wave's own chunks
-  // x: 16 lanes take 128 elements of a token; four loads, 16 of them, at a time
-  v4i xw[4];
-  auto load_x = [&](int q0) __attribute__((always_inline)) {
+    // x: 16 lanes take 128 elements of a token; four loads, 16 of them, at a
+    // time; a wave quantizes its share of the chunks
+    const int q_begin = share(nch, wv) * mp, q_end = share(nch, wv + 1) * mp;
+    v4i xw[4];
+    auto load_x = [&](int q0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = min(q0 + 4 * i + g, tasks - 1), ch = q / mp, row = q - ch * mp;
-      xw[i] = *(const v4i*)(a.x + (int64_t)s_token[m0 + row] * K + (begin * U + ch) * 128 + 8 * l16);
-    }
-  };
-  auto store_x = [&](int q0) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = q0 + 4 * i + g;
-      const us2 top = absmax8x2(xw[i]);
-      const uint32_t byte = e8m0_from_absbits(quad_max(max(top[0], top[1])));
-      const v2i c = quantize8(xw[i], byte, ((byte + 8u) << 7 | 0x60u) * 0x10001u);
-      if (q < tasks) {
-        uint8_t* r = rec + q * kRec;
-        *(v2i*)(r + 8 * l16) = byte == 0xFFu ? (v2i){0x7F7F7F7F, 0x7F7F7F7F} : c;
-        if ((l16 & 3) == 0) r[128 + (l16 >> 2)] = (uint8_t)byte;
+      for (int i = 0; i < 4; ++i) {
+        const int q = max(min(q0 + 4 * i + g, q_end - 1), 0), ch = q / mp, row = q - ch * mp;
+        xw[i] = *(const v4i*)(a.x + (int64_t)s_token[m0 + row] * K + ch * 128 + 8 * l16);
       }
-    }
-  };
-  v4f acc[4];
-  float h[8];
-  uint32_t am = 0;
+    };
+    auto store_x = [&](int q0) __attribute__((always_inline)) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) acc[r] = (v4f){0.f, 0.f, 0.f, 0.f};
-  // Block `b` is done: the waves' sums meet in LDS, row tile by row tile, and
-  // one wave (another one each time) turns them into h.
-  auto finish = [&](int b) __attribute__((always_inline)) {
-    const bool mine = wv == (b & (kMoeWaves - 1));
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      lds_barrier();
-      part[wv][0][lane] = acc[r];
-      part[wv][1][lane] = acc[2 + r];
-      lds_barrier();
-      if (mine) {
-        v4f gs = part[0][0][lane], us = part[0][1][lane];
-#pragma unroll
-        for (int v = 1; v < kMoeWaves; ++v) {
-          gs += part[v][0][lane];
-          us += part[v][1][lane];
-        }
-        if (r == 0) am = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h[4 * r + i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
-          am = max(am, __float_as_uint(h[4 * r + i]) & 0x7FFFFFFFu);
+      for (int i = 0; i < 4; ++i) {
+        const int q = q0 + 4 * i + g;
+        const us2 top = absmax8x2(xw[i]);
+        const uint32_t byte = e8m0_from_absbits(quad_max(max(top[0], top[1])));
+        const v2i c = quantize8(xw[i], byte, ((byte + 8u) << 7 | 0x60u) * 0x10001u);
+        if (q < q_end) {
+          *(v2i*)(smem + q * kCodes + piece(q % mp, l16 >> 1) + 8 * (l16 & 1)) =
+              byte == 0xFFu ? (v2i){0x7F7F7F7F, 0x7F7F7F7F} : c;
+          if ((l16 & 3) == 0) ((uint8_t*)(rsc + q))[l16 >> 2] = (uint8_t)byte;
         }
       }
-    }
+    };
+    // Four row tiles (two of gate rows, two of up rows) of a block.
+    v4f acc[CT][4], head[CT][4];
+    auto clear = [&](v4f (&t)[CT][4]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) acc[r] = (v4f){0.f, 0.f, 0.f, 0.f};
-    if (!mine) return;
-    // rows 4g..4g+3 and 16 + 4g..; quantized from fp32, with no bf16 between
-    am = max(am, (uint32_t)__shfl_xor((int)am, 16));
-    am = max(am, (uint32_t)__shfl_xor((int)am, 32));
-    const bool nan = am >= 0x7F800000u;
-    const uint32_t byte = nan ? 0xFFu : (uint32_t)max((int)(am >> 23) - 8, 0);
-    const float mul = inv_scale_from_e8m0(nan ? 127u : byte);
-    if (l16 < mp) {
-      const int64_t item = s_item[m0 + l16];
-      const int n0 = (b0 + b) * kMoeRows;
+      for (int c = 0; c < CT; ++c)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        int q = cvt2_e4m3<false>(h[4 * r] * mul, h[4 * r + 1] * mul, 0);
-        q = cvt2_e4m3<true>(h[4 * r + 2] * mul, h[4 * r + 3] * mul, q);
-        *(int*)(a.h + item * N + n0 + 16 * r + 4 * g) = nan ? 0x7F7F7F7F : q;
+        for (int r = 0; r < 4; ++r) t[c][r] = (v4f){0.f, 0.f, 0.f, 0.f};
+    };
+    clear(acc);
+    clear(head);
+    float h[8];
+    uint32_t am;
+    auto swiglu = [&](int r, const v4f& gs, const v4f& us) __attribute__((always_inline)) {
+      if (r == 0) am = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[4 * r + i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
+        am = max(am, __float_as_uint(h[4 * r + i]) & 0x7FFFFFFFu);
       }
-      if (g == 0) a.hs[item * (N / 32) + (n0 >> 5)] = (uint8_t)byte;
-    }
-  };
-  if (count == 0) {
-    for (int b = 0; b < nb; ++b) finish(b);
-  } else {
+    };
+    auto store_h = [&](int b, int c) __attribute__((always_inline)) {
+      // rows 4g..4g+3 and 16 + 4g..; quantized from fp32, with no bf16 between
+      am = max(am, (uint32_t)__shfl_xor((int)am, 16));
+      am = max(am, (uint32_t)__shfl_xor((int)am, 32));
+      const bool nan = am >= 0x7F800000u;
+      const uint32_t byte = nan ? 0xFFu : (uint32_t)max((int)(am >> 23) - 8, 0);
+      const float mul = inv_scale_from_e8m0(nan ? 127u : byte);
+      const int token = kMoeCols * c + l16;
+      if (token < mp) {
+        const int64_t item = s_item[m0 + token];
+        const int n0 = (b0 + b) * kMoeRows;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          int q = cvt2_e4m3<false>(h[4 * r] * mul, h[4 * r + 1] * mul, 0);
+          q = cvt2_e4m3<true>(h[4 * r + 2] * mul, h[4 * r + 3] * mul, q);
+          *(int*)(a.h + item * N + n0 + 16 * r + 4 * g) = nan ? 0x7F7F7F7F : q;
+        }
+        if (g == 0) a.hs[item * (N / 32) + (n0 >> 5)] = (uint8_t)byte;
+      }
+    };
+    // Block `b` was wholly this wave's.
+    auto finish = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        if (c > 0 && !wide) continue;
+        swiglu(0, acc[c][0], acc[c][2]);
+        swiglu(1, acc[c][1], acc[c][3]);
+        store_h(b, c);
+      }
+    };
+
     Weight wq[D][4];
     uint32_t ws[D][U];
-    int lb = 0, lu = begin;      // block and line of the next load
-    auto load_w = [&](auto slot_c) __attribute__((always_inline)) {
+    int lb = begin / lines, lu = begin - lb * lines;      // block and line of the next load
+    auto load_w = [&](auto slot_c, bool live) __attribute__((always_inline)) {
       constexpr int S = decltype(slot_c)::value;
-      const bool live = lb < nb;
       const int b = min(lb, nb - 1);
       const uint8_t* wb = wbase + (int64_t)b * kMoeRows * ldw;
       const __amdgpu_buffer_rsrc_t rg = rsrc(wb, (int64_t)kMoeRows * ldw);
@@ -414,38 +443,45 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
 #pragma unroll
       for (int i = 0; i < U; ++i)
         ws[S][i] = *(const uint32_t*)(sbase + ((int64_t)min(lu * U + i, nch - 1) * 2 * N + b * kMoeRows) * 4);
-      if (++lu == end) {
-        lu = begin;
+      if (++lu == lines) {
+        lu = 0;
         ++lb;
       }
     };
-    load_x(0);       // ahead of the weights, which then load while it is quantized
-    static_for<0, D>([&](auto sc) { load_w(sc); });
-    store_x(0);
-    for (int q0 = 16; q0 < tasks; q0 += 16) {
+    load_x(q_begin);       // ahead of the weights, which then load while it is quantized
+    static_for<0, D>([&](auto sc) { load_w(sc, begin + decltype(sc)::value < end); });
+    store_x(q_begin);
+    for (int q0 = q_begin + 16; q0 < q_end; q0 += 16) {
       load_x(q0);
       store_x(q0);
     }
-    int b = 0, u = begin;
-    while (b < nb) {
+    lds_barrier();
+    int b = begin / lines, u = begin - b * lines;
+    bool whole = u == 0;       // this wave has the block's first line
+    for (int u0 = begin; u0 < end; u0 += D) {
       static_for<0, D>([&](auto sc) __attribute__((always_inline)) {
         constexpr int S = decltype(sc)::value;
-        if (b < nb) {
+        if (u0 + S < end) {
 #pragma unroll
           for (int i = 0; i < U; ++i) {
             // an odd last chunk has no second one: its record is read again, its products dropped
             const int ch = min(u * U + i, nch - 1);
-            const uint8_t* xr = rec + ((ch - begin * U) * mp + min(l16, mp - 1)) * kRec;
             const Spread sc4 = spread_rows(ws[S][i]);
             const uint32_t rs[4] = {sc4.lo[0], sc4.lo[1], sc4.hi[0], sc4.hi[1]};
             // elements 32g.. of E2M1, one block; pieces g and g+4 of E4M3, of
             // blocks g/2 and 2 + g/2
-            constexpr bool F4 = WF == kFmtE2M1;
             const int s0 = F4 ? g : g >> 1, s1 = F4 ? g : 2 + (g >> 1);
-            const v4i xp[2] = {*(const v4i*)(xr + (F4 ? 32 : 16) * g), *(const v4i*)(xr + (F4 ? 32 * g + 16 : 64 + 16 * g))};
-            const uint32_t xs = *(const uint32_t*)(xr + 128);
-            v8bf x4[4];
-            to_bf16(xp, scale_of(xs, s0), scale_of(xs, s1), x4);
+            v8bf x4[CT][4];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+              if (c > 0 && !wide) continue;
+              const int token = min(kMoeCols * c + l16, mp - 1), row = ch * mp + token;
+              const uint8_t* xr = smem + row * kCodes;
+              const v4i xp[2] = {*(const v4i*)(xr + piece(token, F4 ? 2 * g : g)),
+                                 *(const v4i*)(xr + piece(token, F4 ? 2 * g + 1 : 4 + g))};
+              const uint32_t xs = rsc[row];
+              to_bf16(xp, scale_of(xs, s0), scale_of(xs, s1), x4[c]);
+            }
             if (u * U + i < nch) {
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
@@ -453,36 +489,80 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
                 if constexpr (F4) to_bf16(wq[S][r].p[i], scale_of(rs[r], s0), w4);
                 else to_bf16(wq[S][r].p, scale_of(rs[r], s0), scale_of(rs[r], s1), w4);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w4[j], x4[j], acc[r], 0, 0, 0);
+                for (int c = 0; c < CT; ++c) {
+                  if (c > 0 && !wide) continue;
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w4[j], x4[c][j], acc[c][r], 0, 0, 0);
+                }
               }
             }
           }
-          load_w(sc);
-          if (++u == end) {
-            u = begin;
-            finish(b++);
+          load_w(sc, u0 + S + D < end);
+          if (++u == lines) {
+            if (whole) {
+              finish(b);
+            } else {
+#pragma unroll
+              for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) head[c][r] = acc[c][r];
+            }
+            clear(acc);
+            whole = true;
+            u = 0;
+            ++b;
           }
         }
       });
+    }
+    // Blocks that several waves share: the first one (`whole`: it has the first
+    // line) adds the others' sums, which are their heads, or all that they have.
+    const bool shared = begin < end && u > 0;
+    if (shared && !whole) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) head[c][r] = acc[c][r];
+    }
+    if (nb % kMoeWaves != 0) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        if (c > 0 && !wide) continue;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          lds_barrier();
+          part[wv][0][lane] = head[c][r];
+          part[wv][1][lane] = head[c][2 + r];
+          lds_barrier();
+          if (shared && whole) {
+            v4f gs = acc[c][r], us = acc[c][2 + r];
+            for (int v = wv + 1; v < kMoeWaves && share(nb * lines, v) < (b + 1) * lines; ++v) {
+              gs += part[v][0][lane];
+              us += part[v][1][lane];
+            }
+            swiglu(r, gs, us);
+            if (r == 1) store_h(b, c);
+          }
+        }
+      }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
 // Down projection and the weighted sum over a token's experts.  A work entry
-// is one hit expert with up to 16 of its tokens (the columns of the matrix
-// tile); the wave's share is a run of (entry, line) units, of which D are in
+// is one hit expert with up to 16 CT of its tokens (columns of matrix tiles); the wave's share is a run of (entry, line) units, of which D are in
 // registers or on their way, across the border between entries.  At the end
 // of an entry its sums, times the combine weights, are added to the wave's own
 // sums of those tokens in LDS.
 // ---------------------------------------------------------------------------
-template <int WF, int RT, int D>
+template <int WF, int RT, int CT, int D>
 __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))) void moe_down_kernel(MoeArgs a,
                                                                                                        int slots) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ int s_entries;
-  constexpr int U = kUnit<WF>;
+  constexpr int U = kUnit<WF>, kCols = kMoeCols * CT;
   const int tid = threadIdx.x, lane = tid & 63, wv = uni(tid >> 6), l16 = lane & 15, g = lane >> 4;
   const int64_t K = a.K, N = a.N, k0 = (int64_t)blockIdx.x * 16 * RT;
   const int n = a.T * a.topk;
@@ -501,7 +581,7 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
     int carry = 0, off = 0;
     for (int base = 0; base < hit; base += 64) {
       const int meta = base + lane < hit ? s_meta[1 + base + lane] : 0, m = meta >> 16;
-      const int p = (m + kMoeCols - 1) / kMoeCols;
+      const int p = (m + kCols - 1) / kCols;
       int incl = p | m << 16;        // both running sums at once (at most 1280 entries, 4096 tokens)
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
@@ -510,7 +590,7 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
       }
       const int at = carry + (incl & 0xFFFF) - p, first = off + (incl >> 16) - m;
       for (int i = 0; i < p; ++i)
-        s_work[at + i] = make_int2((meta & 0xFFFF) | min(m - i * kMoeCols, kMoeCols) << 16, first + i * kMoeCols);
+        s_work[at + i] = make_int2((meta & 0xFFFF) | min(m - i * kCols, kCols) << 16, first + i * kCols);
       const int last = __shfl(incl, 63);
       carry += last & 0xFFFF;
       off += last >> 16;
@@ -530,22 +610,27 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
   const __amdgpu_buffer_rsrc_t rh = rsrc(a.h, (int64_t)n * N);
   const __amdgpu_buffer_rsrc_t rhs = rsrc(a.hs, (int64_t)n * (N / 32));
   if (begin < end) {
-    // this lane's token of a work entry: row of h | token << 16 (or -1), combine weight
-    auto token_of = [&](int2 work) __attribute__((always_inline)) {
-      return l16 < work.x >> 16 ? s_list[work.y + l16] : make_int2(-1, 0);
+    // this lane's token in column tile c of a work entry: row of h | token << 16
+    // (or -1), combine weight
+    auto token_of = [&](int2 work, int c) __attribute__((always_inline)) {
+      const int i = kMoeCols * c + l16;
+      return i < work.x >> 16 ? s_list[work.y + i] : make_int2(-1, 0);
     };
     Weight wq[D][RT];
-    v8i hq[D][U];
+    v8i hq[D][CT][U];
     uint32_t ws[D];
-    int hs[D][U];
+    int hs[D][CT][U];
     int lx = begin / lines, lu = begin - lx * lines;      // entry and line of the next unit to load
-    int item = -1;
+    int item[CT];
     const uint8_t *wbase = nullptr, *sbase = nullptr;
     auto enter_load = [&]() __attribute__((always_inline)) {
       const int2 work = s_work[min(lx, entries - 1)];
       const int64_t e = uni(work.x & 0xFFFF);
-      const int2 t = token_of(work);
-      item = t.x < 0 ? -1 : t.x & 0xFFFF;
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const int2 t = token_of(work, c);
+        item[c] = t.x < 0 ? -1 : t.x & 0xFFFF;
+      }
       wbase = a.q2 + (e * K + k0) * ldw;
       // scales: lane l's row is l % 32, of the line's second chunk for l >= 32
       sbase = a.s2 + (e * K * (N / 128) + k0 + lane % (16 * RT)) * 4;
@@ -558,38 +643,46 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
       for (int r = 0; r < RT; ++r) wq[S][r] = load_weight(rw, (16 * r + l16) * ldw, lu, g, live);
       ws[S] = *(const uint32_t*)(sbase + (int64_t)min(lu * U + (U > 1 ? lane >> 5 : 0), nch - 1) * K * 4);
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int ch = min(lu * U + i, nch - 1);       // a line's second chunk past the end is not used
-        const bool have = live && item >= 0;
-        const int o = have ? item * (int)N + ch * 128 + 16 * g : kPast - 64;
-        const v4i p = __builtin_amdgcn_raw_buffer_load_b128(rh, o, 0, 0);
-        const v4i q = __builtin_amdgcn_raw_buffer_load_b128(rh, o + 64, 0, 0);
-        hq[S][i] = (v8i){p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
-        hs[S][i] = __builtin_amdgcn_raw_buffer_load_b8(rhs, have ? item * (int)(N / 32) + ch * 4 + g : kPast, 0, 0);
-      }
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int ch = min(lu * U + i, nch - 1);       // a line's second chunk past the end is not used
+          const bool have = live && item[c] >= 0;
+          const int o = have ? item[c] * (int)N + ch * 128 + 16 * g : kPast - 64;
+          const v4i p = __builtin_amdgcn_raw_buffer_load_b128(rh, o, 0, 0);
+          const v4i q = __builtin_amdgcn_raw_buffer_load_b128(rh, o + 64, 0, 0);
+          hq[S][c][i] = (v8i){p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
+          hs[S][c][i] =
+              __builtin_amdgcn_raw_buffer_load_b8(rhs, have ? item[c] * (int)(N / 32) + ch * 4 + g : kPast, 0, 0);
+        }
       if (++lu == lines) {
         lu = 0;
         ++lx;
         enter_load();
       }
     };
-    v4f acc[RT];
+    v4f acc[CT][RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r] = (v4f){0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[c][r] = (v4f){0.f, 0.f, 0.f, 0.f};
     int mx = lx, mu = lu;      // entry and line of the next unit to multiply
     auto flush = [&]() __attribute__((always_inline)) {
-      const int2 mine = token_of(s_work[mx]);
-      const float w = __int_as_float(mine.y);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if (mine.x >= 0) {
-          v4f* p = sums + ((mine.x >> 16) * RT + r) * 4 + g;
-          v4f v = *p;
+      for (int c = 0; c < CT; ++c) {
+        const int2 mine = token_of(s_work[mx], c);
+        const float w = __int_as_float(mine.y);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += w * acc[r][i];
-          *p = v;
+        for (int r = 0; r < RT; ++r) {
+          if (mine.x >= 0) {
+            v4f* p = sums + ((mine.x >> 16) * RT + r) * 4 + g;
+            v4f v = *p;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += w * acc[c][r][i];
+            *p = v;
+          }
+          acc[c][r] = (v4f){0.f, 0.f, 0.f, 0.f};
         }
-        acc[r] = (v4f){0.f, 0.f, 0.f, 0.f};
       }
     };
     enter_load();
@@ -606,7 +699,10 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
               const uint32_t rs = i == 0 ? sp.lo[r] : sp.hi[r];
-              acc[r] = mfma<WF>(operand<WF>(wq[S][r], i), (int)(rs >> (8 * g)), hq[S][i], hs[S][i], acc[r]);
+#pragma unroll
+              for (int c = 0; c < CT; ++c)
+                acc[c][r] =
+                    mfma<WF>(operand<WF>(wq[S][r], i), (int)(rs >> (8 * g)), hq[S][c][i], hs[S][c][i], acc[c][r]);
             }
           }
           if (++mu == lines) {
@@ -630,30 +726,25 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
   }
 }
 
-template <int WF, int RT>
+template <int WF, int RT, int CT>
 static hipError_t launch_moe(const MoeArgs& a, size_t down, hipStream_t st) {
   constexpr int DU = 2, DD = 2;
   const int64_t n = (int64_t)a.T * a.topk, slots = std::min<int64_t>(a.E, n);
   // x of as many tokens as LDS holds beside the partial sums and the lists
   const int64_t per_row = a.K / 128 * kRec;
-  const int64_t fit = (kLds - 16384 - kMaxExperts * 4 - kMoeMaxTokens * 8 - 256 - n * 4) / per_row;
-  const int rows = (int)std::min<int64_t>(std::min(a.T, kMoeCols), fit);
+  const int64_t fit = (kLds - 16384 - kMaxExperts * 8 - kMoeMaxTokens * 8 - 256 - n * 4) / per_row;
+  const int rows = (int)std::min<int64_t>(std::min(a.T, CT * kMoeCols), fit);
   const size_t up = (size_t)(rows * per_row + n * 4);
-  const int64_t entries = std::min(n, slots + n / rows);      // sum over the hit experts of ceil(tokens / rows)
-  // about one workgroup per CU: x is quantized once for all of its blocks
-  const int64_t all = a.N / kMoeRows;
-  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(8, all * slots / 256));
-  hipError_t e = hipFuncSetAttribute((const void*)moe_gate_up_kernel<WF, DU>,
+  hipError_t e = hipFuncSetAttribute((const void*)moe_gate_up_kernel<WF, CT, DU>,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)up);
   if (e != hipSuccess) return e;
-  e = hipFuncSetAttribute((const void*)moe_down_kernel<WF, RT, DD>, hipFuncAttributeMaxDynamicSharedMemorySize,
+  e = hipFuncSetAttribute((const void*)moe_down_kernel<WF, RT, CT, DD>, hipFuncAttributeMaxDynamicSharedMemorySize,
                           (int)down);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_gate_up_kernel<WF, DU>), dim3((unsigned)((all + blocks - 1) / blocks), (unsigned)entries),
-                     dim3(kMoeThreads), up, st, a, rows, blocks);
+  hipLaunchKernelGGL((moe_gate_up_kernel<WF, CT, DU>), dim3(kMoeGrid), dim3(kMoeThreads), up, st, a, rows);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down_kernel<WF, RT, DD>), dim3((unsigned)(a.K / (16 * RT))), dim3(kMoeThreads), down, st, a,
+  hipLaunchKernelGGL((moe_down_kernel<WF, RT, CT, DD>), dim3((unsigned)(a.K / (16 * RT))), dim3(kMoeThreads), down, st, a,
                      (int)slots);
   return hipGetLastError();
 }
@@ -664,13 +755,21 @@ static size_t down_lds(const MoeArgs& a, int rt) {
   return (size_t)kMoeWaves * a.T * 64 * rt + n * 8 + (slots + n / kMoeCols) * 8 + (slots + 1) * 4;
 }
 
-// Two column tiles per workgroup of the down kernel (h is read half as often)
-// where the waves' sums of all tokens leave LDS for the lists, else one.
+// Row tiles of the down kernel: two (h is read half as often) where the waves'
+// sums of all tokens leave LDS for the lists, else one: 128 tokens, top 4 of 32
+// experts, 8-bit: 405 us with two, 453 with one; 7 tokens, top 8, 4-bit: 135, 151.
+// Column tiles: two where an expert has more than 8 tokens on average, so that
+// few experts' weights are read twice: 128 tokens, top 4, 8-bit: 340 us with
+// two, 413 with one; 32 tokens, top 8, 4-bit (8 on average): 168, 162.
 hipError_t launch_moe_few_tokens(const MoeArgs& a, hipStream_t st) {
-  const size_t two = down_lds(a, 2);
-  if (two + 64 <= kLds) return a.w_fp4 ? launch_moe<kFmtE2M1, 2>(a, two, st) : launch_moe<kFmtE4M3, 2>(a, two, st);
-  const size_t one = down_lds(a, 1);
-  return a.w_fp4 ? launch_moe<kFmtE2M1, 1>(a, one, st) : launch_moe<kFmtE4M3, 1>(a, one, st);
+  const size_t two = down_lds(a, 2), one = down_lds(a, 1);
+  const bool wide = (int64_t)a.T * a.topk > 8 * (int64_t)a.E;
+  if (two + 64 <= kLds) {
+    if (a.w_fp4) return wide ? launch_moe<kFmtE2M1, 2, 2>(a, two, st) : launch_moe<kFmtE2M1, 2, 1>(a, two, st);
+    return wide ? launch_moe<kFmtE4M3, 2, 2>(a, two, st) : launch_moe<kFmtE4M3, 2, 1>(a, two, st);
+  }
+  if (a.w_fp4) return wide ? launch_moe<kFmtE2M1, 1, 2>(a, one, st) : launch_moe<kFmtE2M1, 1, 1>(a, one, st);
+  return wide ? launch_moe<kFmtE4M3, 1, 2>(a, one, st) : launch_moe<kFmtE4M3, 1, 1>(a, one, st);
 }
 
 }  // namespace mxk
