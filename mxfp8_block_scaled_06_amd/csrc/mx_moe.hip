@@ -26,8 +26,8 @@
 // l%16, group g = l/16: E2M1 elements 32g..32g+31 in 16 bytes, E4M3 the
 // 16-byte pieces g and g+4; its scale byte is block g's; its accumulators are
 // column l%16, rows 4g..4g+3 (as with v_mfma_f32_16x16x32_bf16, which takes 8
-// elements a lane, the same ones of both operands).  Weights are the first operand (rows), tokens
-// the second (columns).
+// elements a lane, the same ones of both operands).  Weights are the first
+// operand (rows), tokens the second (columns).
 #include <algorithm>
 #include <type_traits>
 
@@ -48,10 +48,23 @@ constexpr int kLds = 160 * 1024;                   // of a CU
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// Inclusive sum over the lanes of a wave: within rows of 16, then their totals
+// into the rows after them.
+__device__ __forceinline__ int scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);      // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);      // row_bcast:15, rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);      // row_bcast:31, rows 2 and 3
+  return v;
+}
+
 // Slot of token t that names expert e first, or -1: a token that names an
 // expert twice is one row of that expert.
 __device__ __forceinline__ int slot_of(const int* s_ids, int t, int topk, int e) {
   int found = -1;
+#pragma unroll 4
   for (int j = topk - 1; j >= 0; --j)
     if (s_ids[t * topk + j] == e) found = j;
   return found;
@@ -107,9 +120,9 @@ struct Weight {
   v4i p[2];
 };
 
-// Line `u` of the weight row at byte offset `row`.
-__device__ __forceinline__ Weight load_weight(__amdgpu_buffer_rsrc_t r, int row, int u, int g, bool live) {
-  const int o = live ? row + u * 128 + 16 * g : kPast - 64;
+// The line at the descriptor's start of the weight row at byte offset `row`.
+__device__ __forceinline__ Weight load_weight(__amdgpu_buffer_rsrc_t r, int row, int g) {
+  const int o = row + 16 * g;
   return {{__builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0),
            __builtin_amdgcn_raw_buffer_load_b128(r, o + 64, 0, 0)}};
 }
@@ -309,18 +322,12 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
     int before = 0, hit = 0;
     for (int base = 0; base < a.E; base += 64) {
       const int c = base + lane < a.E ? s_count[base + lane] : 0;
-      int v = (c + rows - 1) / rows | c << 16;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int w = __shfl_up(v, d);
-        if (lane >= d) v += w;
-      }
-      v += before;
+      const int v = before + scan((c + rows - 1) / rows | c << 16);
       if (base + lane < a.E) s_upto[base + lane] = v;
-      before = __shfl(v, 63);
+      before = __builtin_amdgcn_readlane(v, 63);
       hit += __builtin_popcountll(__ballot(c > 0));
     }
-    const uint32_t total = (uint32_t)(uni(before) & 0xFFFF) * all;
+    const uint32_t total = (uint32_t)(before & 0xFFFF) * all;
     if (lane == 0) {
       s_total = (int)total;
       if (wg == 0) a.meta[0] = hit;
@@ -345,21 +352,21 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
     const int me = uni(s_count[e]), passes = (me + rows - 1) / rows, per = (me + passes - 1) / passes;
     const int m0 = uni(s_pass) * per, mp = min(me - m0, per);
     const bool wide = CT > 1 && mp > kMoeCols;        // a second column tile has tokens
-    const uint8_t* wbase = a.q13 + ((int64_t)e * 2 * N + (int64_t)b0 * kMoeRows) * ldw;
-    // scales: lane l's row is gate row l or up row l - 32
-    const uint8_t* sbase = a.s13 + (int64_t)e * 2 * N * (K / 32) +
-                           ((int64_t)b0 * kMoeRows + (lane < 32 ? lane : N + lane - 32)) * 4;
-    // the wave's lines
+    // the wave's lines, and the first one's block and place in it
     const int begin = share(nb * lines, wv), end = share(nb * lines, wv + 1);
+    int b = begin / lines, u = begin - b * lines;
 
     // x: 16 lanes take 128 elements of a token; four loads, 16 of them, at a
     // time; a wave quantizes its share of the chunks
     const int q_begin = share(nch, wv) * mp, q_end = share(nch, wv + 1) * mp;
+    // q / mp: q < 2^11 (LDS holds no more), so q * (2^17 / mp rounded up) is exact enough
+    const uint32_t inv = ((1u << 17) + mp - 1) / mp;
+    static_assert(kLds / kRec < 1 << 11 && (1 << 11) * 2 * kMoeCols < 1 << 17, "");
     v4i xw[4];
     auto load_x = [&](int q0) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int q = max(min(q0 + 4 * i + g, q_end - 1), 0), ch = q / mp, row = q - ch * mp;
+        const int q = max(min(q0 + 4 * i + g, q_end - 1), 0), ch = (int)(q * inv >> 17), row = q - ch * mp;
         xw[i] = *(const v4i*)(a.x + (int64_t)s_token[m0 + row] * K + ch * 128 + 8 * l16);
       }
     };
@@ -371,7 +378,8 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
         const uint32_t byte = e8m0_from_absbits(quad_max(max(top[0], top[1])));
         const v2i c = quantize8(xw[i], byte, ((byte + 8u) << 7 | 0x60u) * 0x10001u);
         if (q < q_end) {
-          *(v2i*)(smem + q * kCodes + piece(q % mp, l16 >> 1) + 8 * (l16 & 1)) =
+          const int row = q - (int)(q * inv >> 17) * mp;
+          *(v2i*)(smem + q * kCodes + piece(row, l16 >> 1) + 8 * (l16 & 1)) =
               byte == 0xFFu ? (v2i){0x7F7F7F7F, 0x7F7F7F7F} : c;
           if ((l16 & 3) == 0) ((uint8_t*)(rsc + q))[l16 >> 2] = (uint8_t)byte;
         }
@@ -430,22 +438,34 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
 
     Weight wq[D][4];
     uint32_t ws[D][U];
-    int lb = begin / lines, lu = begin - lb * lines;      // block and line of the next load
+    // The next line to load: its place in the block, the first gate row there, how
+    // far the block's rows reach from it; the scales of this lane's row, gate row l
+    // or up row l - 32.
+    int lu = u, reach = kMoeRows * ldw - u * 128;
+    const int64_t to_up = N * ldw;
+    const uint8_t* wp = a.q13 + (int64_t)e * 2 * to_up + (int64_t)(b0 + b) * (kMoeRows * ldw) + u * 128;
+    const int64_t chunk = 2 * N * 4;      // bytes of a chunk's scales
+    const uint8_t* sblock = a.s13 + e * (chunk * nch) + ((int64_t)(b0 + b) * kMoeRows + (lane < 32 ? lane : N + lane - 32)) * 4;
+    const uint8_t* sp = sblock + u * U * chunk;
+    const int row0 = l16 * ldw, row1 = row0 + 16 * ldw;
     auto load_w = [&](auto slot_c, bool live) __attribute__((always_inline)) {
       constexpr int S = decltype(slot_c)::value;
-      const int b = min(lb, nb - 1);
-      const uint8_t* wb = wbase + (int64_t)b * kMoeRows * ldw;
-      const __amdgpu_buffer_rsrc_t rg = rsrc(wb, (int64_t)kMoeRows * ldw);
-      const __amdgpu_buffer_rsrc_t ru = rsrc(wb + N * ldw, (int64_t)kMoeRows * ldw);
+      const __amdgpu_buffer_rsrc_t rg = rsrc(wp, live ? reach : 0), ru = rsrc(wp + to_up, live ? reach : 0);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        wq[S][r] = load_weight(r < 2 ? rg : ru, (16 * (r & 1) + l16) * ldw, lu, g, live);
+      for (int r = 0; r < 4; ++r) wq[S][r] = load_weight(r < 2 ? rg : ru, r & 1 ? row1 : row0, g);
+      if (!live) return;
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        ws[S][i] = *(const uint32_t*)(sbase + ((int64_t)min(lu * U + i, nch - 1) * 2 * N + b * kMoeRows) * 4);
+      for (int i = 0; i < U; ++i)      // an odd last chunk has no second one
+        ws[S][i] = *(const uint32_t*)(sp + (i > 0 && lu * U + i < nch ? chunk : 0));
+      wp += 128;
+      reach -= 128;
+      sp += U * chunk;
       if (++lu == lines) {
         lu = 0;
-        ++lb;
+        wp += kMoeRows * ldw - lines * 128;
+        reach = kMoeRows * ldw;
+        sblock += kMoeRows * 4;
+        sp = sblock;
       }
     };
     load_x(q_begin);       // ahead of the weights, which then load while it is quantized
@@ -456,7 +476,6 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
       store_x(q0);
     }
     lds_barrier();
-    int b = begin / lines, u = begin - b * lines;
     bool whole = u == 0;       // this wave has the block's first line
     for (int u0 = begin; u0 < end; u0 += D) {
       static_for<0, D>([&](auto sc) __attribute__((always_inline)) {
@@ -582,16 +601,11 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
     for (int base = 0; base < hit; base += 64) {
       const int meta = base + lane < hit ? s_meta[1 + base + lane] : 0, m = meta >> 16;
       const int p = (m + kCols - 1) / kCols;
-      int incl = p | m << 16;        // both running sums at once (at most 1280 entries, 4096 tokens)
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(incl, d);
-        if (lane >= d) incl += v;
-      }
+      const int incl = scan(p | m << 16);        // both running sums at once (at most 1280 entries, 4096 tokens)
       const int at = carry + (incl & 0xFFFF) - p, first = off + (incl >> 16) - m;
       for (int i = 0; i < p; ++i)
         s_work[at + i] = make_int2((meta & 0xFFFF) | min(m - i * kCols, kCols) << 16, first + i * kCols);
-      const int last = __shfl(incl, 63);
+      const int last = __builtin_amdgcn_readlane(incl, 63);
       carry += last & 0xFFFF;
       off += last >> 16;
     }
@@ -638,9 +652,9 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
     auto load = [&](auto slot_c, int u) __attribute__((always_inline)) {
       constexpr int S = decltype(slot_c)::value;
       const bool live = u < end;
-      const __amdgpu_buffer_rsrc_t rw = rsrc(wbase, (int64_t)16 * RT * ldw);
+      const __amdgpu_buffer_rsrc_t rw = rsrc(wbase + lu * 128, live ? (int64_t)16 * RT * ldw - lu * 128 : 0);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) wq[S][r] = load_weight(rw, (16 * r + l16) * ldw, lu, g, live);
+      for (int r = 0; r < RT; ++r) wq[S][r] = load_weight(rw, (16 * r + l16) * ldw, g);
       ws[S] = *(const uint32_t*)(sbase + (int64_t)min(lu * U + (U > 1 ? lane >> 5 : 0), nch - 1) * K * 4);
 #pragma unroll
       for (int c = 0; c < CT; ++c)
