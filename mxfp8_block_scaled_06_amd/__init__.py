@@ -154,7 +154,9 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(device) -> int:
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    # the raw handle alone where torch offers it: 0.1 us against 1.9 for a Stream object
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _require(t, dtype, name):

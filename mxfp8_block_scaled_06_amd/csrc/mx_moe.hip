@@ -646,7 +646,7 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
         item[c] = t.x < 0 ? -1 : t.x & 0xFFFF;
       }
       wbase = a.q2 + (e * K + k0) * ldw;
-      // scales: lane l's row is l % 32, of the line's second chunk for l >= 32
+      // scales: lane l's row is l % (16 RT), of the line's second chunk for l >= 32
       sbase = a.s2 + (e * K * (N / 128) + k0 + lane % (16 * RT)) * 4;
     };
     auto load = [&](auto slot_c, int u) __attribute__((always_inline)) {
