@@ -224,6 +224,17 @@ __device__ __forceinline__ v2i quantize8(v4i w, uint32_t byte, uint32_t most) {
   return q;
 }
 
+// x / (1 + 2^(-x log2 e)): the power by the hardware, with what the product
+// -x log2 e rounds away put back (2^-22 of it otherwise lost at x = -40), and a
+// reciprocal of one ulp; some 2^-22 of the value in all.  Below -88 it is -0.
+__device__ __forceinline__ float silu(float x) {
+  const float t = fminf(-x * 1.442695041f, 127.9f);
+  const float lo = fmaf(-x, 1.925963033e-8f, fmaf(-x, 1.442695041f, -t));
+  float p = __builtin_amdgcn_exp2f(t);
+  p = fmaf(p * (t < 127.9f ? lo : 0.f), 0.6931471806f, p);
+  return x * __builtin_amdgcn_rcpf(1.0f + p);
+}
+
 // Largest |bf16| bits of eight values, as a packed pair still to be combined.
 __device__ __forceinline__ us2 absmax8x2(v4i w) {
   us2 m = __builtin_bit_cast(us2, (uint32_t)w[0] & 0x7FFF7FFFu);
@@ -332,19 +343,15 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
       s_total = (int)total;
       if (wg == 0) a.meta[0] = hit;
     }
-    const uint32_t at = (uint64_t)total * wg >> 8;
-    if (at < (uint32_t)((uint64_t)total * (wg + 1) >> 8)) enter(at / all, at % all == 0);
   }
   __syncthreads();
   const uint32_t total = (uint32_t)uni(s_total);
   const int start = (int)((uint64_t)total * wg >> 8), stop = (int)((uint64_t)total * (wg + 1) >> 8);
   for (int at = start; at < stop;) {
     const int entry = at / all, b0 = at - entry * all, nb = min(all - b0, stop - at);
-    if (at > start) {
-      __syncthreads();      // the lists and x of the entry before
-      if (wv == 0) enter(entry, true);
-      __syncthreads();
-    }
+    if (at > start) __syncthreads();      // the lists and x of the entry before
+    if (wv == 0) enter(entry, b0 == 0);
+    __syncthreads();
     at += nb;
     const int e = uni(s_expert);
     // an expert's entries share its tokens evenly: a second column tile only
@@ -401,7 +408,7 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
       if (r == 0) am = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        h[4 * r + i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
+        h[4 * r + i] = silu(gs[i]) * us[i];
         am = max(am, __float_as_uint(h[4 * r + i]) & 0x7FFFFFFFu);
       }
     };
