@@ -467,12 +467,14 @@ mx_status mx_grouped_mm_dgrad_fp4(const uint16_t* dOut, const uint8_t* qWt, cons
  * scales in the GEMM layout; out bf16 [T, K].
  * A slot whose id lies outside [0, E) adds nothing (a token with no other
  * slot gets a row of zeros); status, if not NULL, is set to 1 when there is
- * one, else to 0 (T = 0 enqueues nothing and leaves it).  An expert named twice by a token counts with the sum of
- * the two combine weights.
+ * one, else to 0 (T = 0 enqueues nothing and leaves it).  An expert named
+ * twice by a token counts with the sum of the two combine weights.  Weights of
+ * the gate and up projection past the bf16 range (which the quantizers never
+ * make of bf16 values) count as infinite.
  * Requires 0 <= T <= MX_MOE_MAX_TOKENS, 1 <= topk <= MX_MOE_MAX_TOPK, K and N
- * multiples of 128, 128 <= K <= 2^16 and 128 <= N <= 2^20, T*topk*N <= 2^30, 1 <= E <= 1024; x, codes, out 16-byte and
- * the rest 4-byte aligned.  Larger batches go through mx_route and the
- * grouped GEMMs.  ws: mx_moe_few_tokens_workspace_bytes, 256-byte aligned,
+ * multiples of 128, 128 <= K <= 2^16 and 128 <= N <= 2^20, T*topk*N <= 2^30,
+ * 1 <= E <= 1024; x, codes, out 16-byte and the rest 4-byte aligned.  Larger
+ * batches go through mx_route and the grouped GEMMs.  ws: mx_moe_few_tokens_workspace_bytes, 256-byte aligned,
  * the caller's, one per call in flight; needs no initialisation. */
 #define MX_MOE_MAX_TOKENS 128
 #define MX_MOE_MAX_TOPK 32
