@@ -399,7 +399,7 @@ mx_status mx_grouped_mm_fwd_q_noalloc(const uint16_t* A, const uint8_t* qW, cons
  * -> q [batch, rows, cols/2], s row-major [batch, rows, cols/32]
  * (scale_layout MX_SCALES_ROWMAJOR; requires cols % 32 == 0) or in the GEMM
  * layout [batch, cols/128, rows, 4] (MX_SCALES_GEMM; requires cols % 128 ==
- * 0).  Fewer than 2^32 blocks. */
+ * 0 and cols <= 2^30).  Fewer than 2^32 blocks. */
 mx_status mx_quantize_rowwise_fp4(const uint16_t* x, int64_t batch, int64_t rows, int64_t cols, uint8_t* q,
                                   uint8_t* s, int scale_layout, void* stream);
 
@@ -433,7 +433,8 @@ mx_status mx_quantize_weights_fp4(const uint16_t* w, int64_t E, int64_t N, int64
  * is dropped otherwise, and C rows that no entry names are left as they were.
  * C is bf16 (rounded to nearest even), or float with out_f32 != 0.  Rows past
  * offs[E-1] are not written.  Requires Kc % 128 == 0, Kc >= 128 (or I or J
- * zero), Kc <= 2^23, J % 8 == 0, 1 <= E <= 1024. */
+ * zero), Kc <= 2^23, J % 8 == 0, 1 <= E <= 1024, and fewer than 2^23 output
+ * tiles of 256 x 256 (partial ones of every group included). */
 mx_status mx_grouped_gemm_mxfp4(const uint8_t* X, const uint8_t* sX, int x_format, const uint8_t* Y,
                                 const uint8_t* sY, int scale_layout, const int32_t* offs, int64_t I, int64_t J,
                                 int64_t Kc, int64_t E, const int32_t* row_map, int64_t c_rows, void* C, int out_f32,

@@ -555,6 +555,8 @@ mx_status check_fp4(const char* fn, const void* x, int64_t batch, int64_t rows, 
                 scale_layout, (int)MX_SCALES_ROWMAJOR, (int)MX_SCALES_GEMM);
   mx_status st = check_quant(fn, x, batch, rows, cols, q, s, 1, scale_layout == MX_SCALES_GEMM ? 128 : 32);
   if (st != MX_OK || rows == 0 || cols == 0) return st;
+  if (scale_layout == MX_SCALES_GEMM && cols > ((int64_t)1 << 30))
+    return fail(MX_ERR_SHAPE, "%s: cols=%lld exceeds 2^30 (scales in the GEMM layout)", fn, (long long)cols);
   // batch * rows * (cols/32) < 2^32, without overflow on the way
   const int64_t most = ((int64_t)1 << 32) - 1;
   if (batch > most || rows > most || cols / 32 > most || batch * rows > most || batch * rows > most / (cols / 32))
@@ -628,8 +630,9 @@ mx_status mx_grouped_gemm_mxfp4(const uint8_t* X, const uint8_t* sX, int x_forma
   if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(C, 16) || !aligned(sX, 4) || !aligned(sY, 4) ||
       !aligned(offs, 4) || !aligned(row_map, 4))
     return fail(MX_ERR_ALIGN, "%s: X, Y, C must be 16-byte and scales, offsets and row_map 4-byte aligned", fn);
-  // one workgroup per tile: at most 2^31 - 1 of them
-  if ((I / 64 + E + 1) * (J / 32 + 1) >= ((int64_t)1 << 30))
+  // a workgroup of 512 threads per 256 x 256 tile, and fewer than 2^32 threads (the
+  // small tiles cover at most 2.5 times the CUs)
+  if ((I < E ? I : I / 256 + E + 1) * (J / 256 + 1) >= ((int64_t)1 << 23) - 256)
     return fail(MX_ERR_SHAPE, "%s: too many output tiles for one launch", fn);
   mxk::Fp4GemmArgs a{};
   a.X = X;

@@ -64,8 +64,15 @@ inline int t4_steps(int64_t batch, int64_t rows, int64_t cols) {
              : 1;
 }
 
+// `n` workgroups: a launch takes fewer than 2^32 threads along an axis.
+inline dim3 wide_grid(int64_t n) {
+  const int64_t x = n < ((int64_t)1 << 22) ? n : (int64_t)1 << 22;
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+__device__ __forceinline__ int64_t wide_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 inline dim3 t4_grid(int64_t batch, int64_t rows, int64_t cols, int steps) {
-  return dim3((unsigned)(batch * ((rows + kT4Rows * steps - 1) / (kT4Rows * steps)) * ((cols + kT4Cols - 1) / kT4Cols)));
+  return wide_grid(batch * ((rows + kT4Rows * steps - 1) / (kT4Rows * steps)) * ((cols + kT4Cols - 1) / kT4Cols));
 }
 
 // A workgroup's tile: batch entry, first row and first column, column tiles
@@ -78,9 +85,9 @@ template <int NC>
 __device__ __forceinline__ Tile4 tile4(int64_t rows, int cols) {
   const uint32_t kt = (uint32_t)(cols + kT4Cols - 1) / kT4Cols;
   const uint32_t rt = (uint32_t)((rows + kT4Rows * NC - 1) / (kT4Rows * NC));
-  const uint32_t t = blockIdx.x / kt;
+  const uint32_t id = (uint32_t)wide_block(), t = id / kt;      // at most 2^32 / 4 tiles of a block or more
   Tile4 o;
-  o.k0 = (int)(blockIdx.x - t * kt) * kT4Cols;
+  o.k0 = (int)(id - t * kt) * kT4Cols;
   o.b = t / rt;
   o.r0 = (int64_t)(t - (uint32_t)o.b * rt) * (kT4Rows * NC);
   return o;
@@ -92,7 +99,7 @@ __device__ __forceinline__ Tile4 tile4(int64_t rows, int cols) {
 __global__ __launch_bounds__(kF4Threads) void quant_rowwise_fp4_kernel(const uint16_t* __restrict__ x,
                                                                        int64_t nchunks, uint8_t* __restrict__ q,
                                                                        uint8_t* __restrict__ s) {
-  const int64_t idx = (int64_t)blockIdx.x * kF4Threads + threadIdx.x;
+  const int64_t idx = wide_block() * kF4Threads + threadIdx.x;
   v4i w = (v4i){0, 0, 0, 0};
   if (idx < nchunks) w = __builtin_nontemporal_load((const v4i*)(x + idx * 8));
   // nchunks is a multiple of 4: a quad is wholly in range or wholly out
@@ -104,11 +111,12 @@ __global__ __launch_bounds__(kF4Threads) void quant_rowwise_fp4_kernel(const uin
 }
 
 template <int NC>
-__global__ __launch_bounds__(kF4Threads) void quant_tiles_fp4_kernel(const uint16_t* __restrict__ x, int64_t rows,
-                                                                     int cols, uint8_t* __restrict__ q,
+__global__ __launch_bounds__(kF4Threads) void quant_tiles_fp4_kernel(const uint16_t* __restrict__ x, int64_t batch,
+                                                                     int64_t rows, int cols, uint8_t* __restrict__ q,
                                                                      uint8_t* __restrict__ s) {
   __shared__ uint8_t sc[2][kT4Rows * NC][4];     // [chunk of 128][row][block]
   const Tile4 t = tile4<NC>(rows, cols);
+  if (t.b >= batch) return;
   const int pc = threadIdx.x & 31, r = threadIdx.x >> 5;
   const bool k_in = t.k0 + 8 * pc < cols;
   v4i w[NC];
@@ -140,7 +148,7 @@ hipError_t launch_quant_rowwise_fp4(const uint16_t* x, int64_t rows_total, int64
   const int64_t nchunks = rows_total * (cols / 8);
   if (nchunks == 0) return hipSuccess;
   if (gemm_rows_per_batch == 0) {
-    hipLaunchKernelGGL(quant_rowwise_fp4_kernel, dim3((unsigned)((nchunks + kF4Threads - 1) / kF4Threads)),
+    hipLaunchKernelGGL(quant_rowwise_fp4_kernel, wide_grid((nchunks + kF4Threads - 1) / kF4Threads),
                        dim3(kF4Threads), 0, st, x, nchunks, q, s);
     return hipGetLastError();
   }
@@ -148,9 +156,11 @@ hipError_t launch_quant_rowwise_fp4(const uint16_t* x, int64_t rows_total, int64
   const int steps = t4_steps(batch, rows, cols);
   const dim3 grid = t4_grid(batch, rows, cols, steps);
   if (steps == kT4Steps)
-    hipLaunchKernelGGL(quant_tiles_fp4_kernel<kT4Steps>, grid, dim3(kF4Threads), 0, st, x, rows, (int)cols, q, s);
+    hipLaunchKernelGGL(quant_tiles_fp4_kernel<kT4Steps>, grid, dim3(kF4Threads), 0, st, x, batch, rows, (int)cols,
+                       q, s);
   else
-    hipLaunchKernelGGL(quant_tiles_fp4_kernel<1>, grid, dim3(kF4Threads), 0, st, x, rows, (int)cols, q, s);
+    hipLaunchKernelGGL(quant_tiles_fp4_kernel<1>, grid, dim3(kF4Threads), 0, st, x, batch, rows, (int)cols,
+                       q, s);
   return hipGetLastError();
 }
 
@@ -186,7 +196,7 @@ __device__ __forceinline__ v4i dequant8(uint32_t codes, uint32_t byte) {
 __global__ __launch_bounds__(kF4Threads) void dequant_fp4_kernel(const uint8_t* __restrict__ q,
                                                                  const uint8_t* __restrict__ s, int64_t nchunks,
                                                                  uint16_t* __restrict__ out) {
-  const int64_t idx = (int64_t)blockIdx.x * kF4Threads + threadIdx.x;
+  const int64_t idx = wide_block() * kF4Threads + threadIdx.x;
   if (idx >= nchunks) return;
   const uint32_t c = *(const uint32_t*)(q + idx * 4);
   __builtin_nontemporal_store(dequant8(c, s[idx >> 2]), (v4i*)(out + idx * 8));
@@ -194,9 +204,11 @@ __global__ __launch_bounds__(kF4Threads) void dequant_fp4_kernel(const uint8_t* 
 
 template <int NC>
 __global__ __launch_bounds__(kF4Threads) void dequant_tiles_fp4_kernel(const uint8_t* __restrict__ q,
-                                                                       const uint8_t* __restrict__ s, int64_t rows,
-                                                                       int cols, uint16_t* __restrict__ out) {
+                                                                       const uint8_t* __restrict__ s, int64_t batch,
+                                                                       int64_t rows, int cols,
+                                                                       uint16_t* __restrict__ out) {
   const Tile4 t = tile4<NC>(rows, cols);
+  if (t.b >= batch) return;
   const int pc = threadIdx.x & 31, r = threadIdx.x >> 5;
   if (t.k0 + 8 * pc >= cols) return;
   const uint8_t* sb = s + (t.b * (cols / 128) + t.k0 / 128 + (pc >> 4)) * rows * 4 + ((pc >> 2) & 3);
@@ -223,7 +235,7 @@ hipError_t launch_dequant_fp4(const uint8_t* q, const uint8_t* s, int64_t rows_t
   const int64_t nchunks = rows_total * (cols / 8);
   if (nchunks == 0) return hipSuccess;
   if (gemm_rows_per_batch == 0) {
-    hipLaunchKernelGGL(dequant_fp4_kernel, dim3((unsigned)((nchunks + kF4Threads - 1) / kF4Threads)), dim3(kF4Threads),
+    hipLaunchKernelGGL(dequant_fp4_kernel, wide_grid((nchunks + kF4Threads - 1) / kF4Threads), dim3(kF4Threads),
                        0, st, q, s, nchunks, out);
     return hipGetLastError();
   }
@@ -231,9 +243,11 @@ hipError_t launch_dequant_fp4(const uint8_t* q, const uint8_t* s, int64_t rows_t
   const int steps = t4_steps(batch, rows, cols);
   const dim3 grid = t4_grid(batch, rows, cols, steps);
   if (steps == kT4Steps)
-    hipLaunchKernelGGL(dequant_tiles_fp4_kernel<kT4Steps>, grid, dim3(kF4Threads), 0, st, q, s, rows, (int)cols, out);
+    hipLaunchKernelGGL(dequant_tiles_fp4_kernel<kT4Steps>, grid, dim3(kF4Threads), 0, st, q, s, batch, rows,
+                       (int)cols, out);
   else
-    hipLaunchKernelGGL(dequant_tiles_fp4_kernel<1>, grid, dim3(kF4Threads), 0, st, q, s, rows, (int)cols, out);
+    hipLaunchKernelGGL(dequant_tiles_fp4_kernel<1>, grid, dim3(kF4Threads), 0, st, q, s, batch, rows,
+                       (int)cols, out);
   return hipGetLastError();
 }
 

@@ -270,3 +270,25 @@ def test_training_then_decoding():
     ref, tol = moe.moe_layer(bf16_host_bits(x[:T].contiguous()), ids, c, v[0], v[1], oracle.compare.U_MFMA)
     err = np.abs(oracle.bf16_to_f64(bf16_host_bits(out)) - ref)
     assert (err <= tol).all(), float((err / tol).max())
+
+
+def test_more_values_than_one_grid_axis_holds():
+    """Past 2^35 values the quantizer's and dequantizer's threads exceed 2^32
+    (the limit of a grid axis): the last rows come out like rows of their own."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    rows, cols = (1 << 22) + 8, 8192
+    if torch.cuda.mem_get_info()[0] < 200 << 30:
+        pytest.skip("needs 200 GiB of free GPU memory")
+    log("fp4 quantize and restore 2^35 + 2^16 values")
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda:0")
+    tail = to_dev_bf16(inp.random_bf16((8, cols), seed=77))
+    x[-8:] = tail
+    q, s = mx.mx_quantize_rowwise_fp4(x)
+    del x
+    tq, ts = mx.mx_quantize_rowwise_fp4(tail)
+    assert torch.equal(q[-8:], tq) and torch.equal(s[-8:], ts) and not q[:-8:4099].any()
+    v = mx.mx_dequantize_fp4(q, s)
+    assert torch.equal(v[-8:], mx.mx_dequantize_fp4(tq, ts)) and not v[:-8:4099].any()
+    del q, s, v
+    torch.cuda.empty_cache()

@@ -166,3 +166,17 @@ def test_moe_refuses_hidden_layers_past_its_offsets():
     assert lib.mx_moe_few_tokens_workspace_bytes(128, 32, (1 << 18) + 128) == 0
     assert lib.mx_moe_few_tokens(*[FAKE] * 7, 1, 128, 32, 256, (1 << 18) + 128, 4, FAKE, None, FAKE, 1 << 40, None) == 2
     assert "2^30" in _err(lib)
+
+
+def test_sizes_past_one_launch_are_refused():
+    lib = _lib()
+    G = mx.SCALES_GEMM
+    for f in (lib.mx_quantize_rowwise_fp4,
+              lambda x, b, r, c, q, s, lay, st: lib.mx_dequantize_fp4(q, s, b, r, c, lay, x, st)):
+        assert f(FAKE, 1, 1, (1 << 30) + 128, FAKE, FAKE, G, None) == 2
+        assert "2^30" in _err(lib)
+    g = lib.mx_grouped_gemm_mxfp4
+    # one row, 2^23 column tiles: 2^32 threads
+    assert g(FAKE, FAKE, 0, FAKE, FAKE, G, FAKE, 1, (1 << 31) - 8, 128, 1, None, 0, FAKE, 0, None) == 2
+    assert "tiles" in _err(lib)
+    assert g(FAKE, FAKE, 0, FAKE, FAKE, G, FAKE, 1 << 21, 1 << 20, 128, 1024, None, 0, FAKE, 0, None) == 2
