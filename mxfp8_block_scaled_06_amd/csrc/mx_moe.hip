@@ -275,13 +275,17 @@ __device__ __forceinline__ int piece(int token, int p) { return 16 * (p ^ (token
 // ---------------------------------------------------------------------------
 constexpr int kMoeGrid = 256;      // workgroups of the gate kernel, one per CU
 static_assert(kMoeGrid == 1 << 8, "shares are taken by shifts");
+// Row tiles (gate and up) whose sums meet in LDS at a time: with two column tiles
+// one, as LDS is x's (20 tokens of K = 7168 and not 18: 128 tokens, top 4, 8-bit:
+// 323 us against 336), else two, with half the barriers.
+template <int CT>
+constexpr int kParts = CT == 1 ? 2 : 1;
 
 template <int WF, int CT, int D>
 __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))) void moe_gate_up_kernel(MoeArgs a,
                                                                                                           int rows) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ v4f part[kMoeWaves][2][64];
-  __shared__ int s_count[kMaxExperts], s_upto[kMaxExperts];
+  __shared__ v4f part[kMoeWaves][kParts<CT>][64];
   __shared__ int s_item[kMoeMaxTokens], s_token[kMoeMaxTokens], s_expert, s_pass, s_total;
   constexpr int U = kUnit<WF>;
   constexpr bool F4 = WF == kFmtE2M1;
@@ -292,6 +296,7 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
   // x in LDS, [chunk][token]: codes, scales
   uint32_t* rsc = (uint32_t*)(smem + nch * rows * kCodes);
   int* s_ids = (int*)(smem + nch * rows * kRec);
+  int *s_count = s_ids + a.T * a.topk, *s_upto = s_count + a.E;
   load_ids(a, s_ids, s_count);
   // Work entry `entry` for the workgroup, by wave 0: its expert, pass and tokens;
   // by the one that has the entry's first block, what the down kernel needs.
@@ -557,17 +562,20 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
         if (c > 0 && !wide) continue;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          lds_barrier();
-          part[wv][0][lane] = head[c][r];
-          part[wv][1][lane] = head[c][2 + r];
-          lds_barrier();
+          v4f gu[2] = {acc[c][r], acc[c][2 + r]};
+#pragma unroll
+          for (int i = 0; i < 2; i += kParts<CT>) {
+            lds_barrier();
+#pragma unroll
+            for (int k = 0; k < kParts<CT>; ++k) part[wv][k][lane] = head[c][2 * (i + k) + r];
+            lds_barrier();
+            if (shared && whole)
+              for (int v = wv + 1; v < kMoeWaves && share(nb * lines, v) < (b + 1) * lines; ++v)
+#pragma unroll
+                for (int k = 0; k < kParts<CT>; ++k) gu[i + k] += part[v][k][lane];
+          }
           if (shared && whole) {
-            v4f gs = acc[c][r], us = acc[c][2 + r];
-            for (int v = wv + 1; v < kMoeWaves && share(nb * lines, v) < (b + 1) * lines; ++v) {
-              gs += part[v][0][lane];
-              us += part[v][1][lane];
-            }
-            swiglu(r, gs, us);
+            swiglu(r, gu[0], gu[1]);
             if (r == 1) store_h(b, c);
           }
         }
@@ -752,10 +760,10 @@ static hipError_t launch_moe(const MoeArgs& a, size_t down, hipStream_t st) {
   constexpr int DU = 2, DD = 2;
   const int64_t n = (int64_t)a.T * a.topk, slots = std::min<int64_t>(a.E, n);
   // x of as many tokens as LDS holds beside the partial sums and the lists
-  const int64_t per_row = a.K / 128 * kRec;
-  const int64_t fit = (kLds - 16384 - kMaxExperts * 8 - kMoeMaxTokens * 8 - 256 - n * 4) / per_row;
+  const int64_t per_row = a.K / 128 * kRec, lists = (n + 2 * a.E) * 4;
+  const int64_t fit = (kLds - kMoeWaves * kParts<CT> * 1024 - kMoeMaxTokens * 8 - 256 - lists) / per_row;
   const int rows = (int)std::min<int64_t>(std::min(a.T, CT * kMoeCols), fit);
-  const size_t up = (size_t)(rows * per_row + n * 4);
+  const size_t up = (size_t)(rows * per_row + lists);
   hipError_t e = hipFuncSetAttribute((const void*)moe_gate_up_kernel<WF, CT, DU>,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)up);
   if (e != hipSuccess) return e;
