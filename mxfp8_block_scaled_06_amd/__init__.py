@@ -175,9 +175,9 @@ def _out(t, shape, dtype, device, name):
     """An output buffer: allocated when None, else checked to be exactly what
     the kernel writes (the C ABI sees only a pointer and cannot)."""
     import torch
-    shape = tuple(map(int, shape))
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    shape = tuple(map(int, shape))
     if isinstance(t, torch.Tensor) and tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     _require(t, dtype, name)
@@ -187,10 +187,11 @@ def _out(t, shape, dtype, device, name):
 
 
 def _as3d(x):
-    if x.dim() == 2:
-        return 1, x.shape[0], x.shape[1]
-    if x.dim() == 3:
-        return x.shape[0], x.shape[1], x.shape[2]
+    shape = tuple(x.shape)
+    if len(shape) == 2:
+        return 1, *shape
+    if len(shape) == 3:
+        return shape
     raise ValueError("expected a 2-D or 3-D tensor")
 
 
@@ -735,9 +736,10 @@ def _on(device):
 
 def _same_device(first, *rest):
     """Every tensor on the device of the first one (the kernels run there)."""
+    dev = first.device
     for t in rest:
-        if t.device != first.device:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+        if t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
 
 
 def mx_quantize_rowwise_fp4(x, q=None, s=None, scale_layout: str = "rowmajor"):
@@ -749,12 +751,13 @@ def mx_quantize_rowwise_fp4(x, q=None, s=None, scale_layout: str = "rowmajor"):
     lib = load_library()
     _require(x, torch.bfloat16, "x")
     B, R, C = _as3d(x)
-    s_shape, layout = _scale_shape(scale_layout, x.shape[:-2], R, C)
-    q = _out(q, (*x.shape[:-1], C // 2), torch.uint8, x.device, "q")
-    s = _out(s, s_shape, torch.uint8, x.device, "s")
-    with _on(x.device):
+    lead, dev = (B,) if x.dim() == 3 else (), x.device
+    s_shape, layout = _scale_shape(scale_layout, lead, R, C)
+    q = _out(q, (*lead, R, C // 2), torch.uint8, dev, "q")
+    s = _out(s, s_shape, torch.uint8, dev, "s")
+    with _on(dev):
         _check("mx_quantize_rowwise_fp4",
-               lib.mx_quantize_rowwise_fp4(_ptr(x), B, R, C, _ptr(q), _ptr(s), layout, _stream(x.device)))
+               lib.mx_quantize_rowwise_fp4(_ptr(x), B, R, C, _ptr(q), _ptr(s), layout, _stream(dev)))
     return q, s
 
 
@@ -768,14 +771,15 @@ def mx_dequantize_fp4(q, s, scale_layout: str = "rowmajor", out=None):
     _require(s, torch.uint8, "s")
     B, R, C = _as3d(q)
     C *= 2
-    s_shape, layout = _scale_shape(scale_layout, q.shape[:-2], R, C)
+    lead, dev = (B,) if q.dim() == 3 else (), q.device
+    s_shape, layout = _scale_shape(scale_layout, lead, R, C)
     if tuple(s.shape) != s_shape:
         raise ValueError(f"s must have shape {s_shape} for codes {tuple(q.shape)}, got {tuple(s.shape)}")
     _same_device(q, s)
-    out = _out(out, (*q.shape[:-1], C), torch.bfloat16, q.device, "out")
-    with _on(q.device):
+    out = _out(out, (*lead, R, C), torch.bfloat16, dev, "out")
+    with _on(dev):
         _check("mx_dequantize_fp4",
-               lib.mx_dequantize_fp4(_ptr(q), _ptr(s), B, R, C, layout, _ptr(out), _stream(q.device)))
+               lib.mx_dequantize_fp4(_ptr(q), _ptr(s), B, R, C, layout, _ptr(out), _stream(dev)))
     return out
 
 
