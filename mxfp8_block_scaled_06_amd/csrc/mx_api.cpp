@@ -603,10 +603,15 @@ mx_status mx_quantize_weights_fp4(const uint16_t* w, int64_t E, int64_t N, int64
   return hip_status(mxk::launch_quant_weights_fp4(w, E, N, K, q, s, q_t, s_t, (hipStream_t)stream), fn);
 }
 
-mx_status mx_grouped_gemm_mxfp4(const uint8_t* X, const uint8_t* sX, int x_format, const uint8_t* Y,
-                                const uint8_t* sY, int scale_layout, const int32_t* offs, int64_t I, int64_t J,
-                                int64_t Kc, int64_t E, const int32_t* row_map, int64_t c_rows, void* C, int out_f32,
-                                void* stream) {
+}  // extern "C"
+
+namespace {
+
+// The rows-grouped product with MXFP4 weights, of MX rows (X, sX) or of bf16 rows
+// A that the kernel quantizes itself.
+mx_status gemm_fp4(const uint16_t* A, const uint8_t* X, const uint8_t* sX, int x_format, const uint8_t* Y,
+                   const uint8_t* sY, int scale_layout, const int32_t* offs, int64_t I, int64_t J, int64_t Kc,
+                   int64_t E, const int32_t* row_map, int64_t c_rows, void* C, int out_f32, void* stream) {
   const char* fn = "mx_grouped_gemm_mxfp4";
   if (scale_layout != MX_SCALES_GEMM)
     return fail(MX_ERR_LAYOUT, "%s: scales must be in the GEMM layout [K/128][rows][4] (MX_SCALES_GEMM = %d, got %d)",
@@ -626,8 +631,8 @@ mx_status mx_grouped_gemm_mxfp4(const uint8_t* X, const uint8_t* sX, int x_forma
     return fail(MX_ERR_SHAPE, "%s: c_rows=%lld outside [0, 2^31)", fn, (long long)c_rows);
   if (I == 0 || J == 0 || (row_map && c_rows == 0)) return MX_OK;
   if (Kc == 0) return fail(MX_ERR_SHAPE, "%s: no contraction (Kc=0)", fn);
-  if (!X || !sX || !Y || !sY || !offs || !C) return fail(MX_ERR_NULL, "%s: null pointer", fn);
-  if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(C, 16) || !aligned(sX, 4) || !aligned(sY, 4) ||
+  if ((!A && (!X || !sX)) || !Y || !sY || !offs || !C) return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(A, 16) || !aligned(X, 16) || !aligned(Y, 16) || !aligned(C, 16) || !aligned(sX, 4) || !aligned(sY, 4) ||
       !aligned(offs, 4) || !aligned(row_map, 4))
     return fail(MX_ERR_ALIGN, "%s: X, Y, C must be 16-byte and scales, offsets and row_map 4-byte aligned", fn);
   // a workgroup of 512 threads per 256 x 256 tile, and fewer than 2^32 threads (the
@@ -635,6 +640,7 @@ mx_status mx_grouped_gemm_mxfp4(const uint8_t* X, const uint8_t* sX, int x_forma
   if ((I < E ? I : I / 256 + E + 1) * (J / 256 + 1) >= ((int64_t)1 << 23) - 256)
     return fail(MX_ERR_SHAPE, "%s: too many output tiles for one launch", fn);
   mxk::Fp4GemmArgs a{};
+  a.A = A;
   a.X = X;
   a.sX = sX;
   a.Y = Y;
@@ -652,6 +658,18 @@ mx_status mx_grouped_gemm_mxfp4(const uint8_t* X, const uint8_t* sX, int x_forma
   return hip_status(mxk::launch_fp4_gemm(a, (hipStream_t)stream), fn);
 }
 
+}  // namespace
+
+extern "C" {
+
+mx_status mx_grouped_gemm_mxfp4(const uint8_t* X, const uint8_t* sX, int x_format, const uint8_t* Y,
+                                const uint8_t* sY, int scale_layout, const int32_t* offs, int64_t I, int64_t J,
+                                int64_t Kc, int64_t E, const int32_t* row_map, int64_t c_rows, void* C, int out_f32,
+                                void* stream) {
+  return gemm_fp4(nullptr, X, sX, x_format, Y, sY, scale_layout, offs, I, J, Kc, E, row_map, c_rows, C, out_f32,
+                  stream);
+}
+
 size_t mx_grouped_mm_fp4_workspace_bytes(int64_t M, int64_t C, int act_format) {
   if (M < 0 || C < 0 || C % 128 != 0 || (act_format != MX_FMT_FP8 && act_format != MX_FMT_FP4)) return 0;
   if (C > ((int64_t)1 << 23) || M >= ((int64_t)1 << 31)) return 0;
@@ -667,9 +685,11 @@ namespace {
 mx_status mm_fp4(const char* fn, const char* c_name, const char* j_name, const uint16_t* a, const uint8_t* q,
                  const uint8_t* s, const int32_t* offs, int64_t M, int64_t J, int64_t C, int64_t E, int act_format,
                  uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
-  mx_status st = check_mm(fn, a, q, offs, out, M, J, C, E);
+  // without rows or columns nothing is read, and the tensors may have no memory
+  const bool none = (M == 0 || J == 0) && M >= 0 && J >= 0 && C >= 0 && E >= 1 && E <= mxk::kMaxExperts;
+  mx_status st = none ? MX_OK : check_mm(fn, a, q, offs, out, M, J, C, E);
   if (st != MX_OK) return st;
-  if (!s) return fail(MX_ERR_NULL, "%s: null weight scales", fn);
+  if (!none && !s) return fail(MX_ERR_NULL, "%s: null weight scales", fn);
   if (act_format != MX_FMT_FP8 && act_format != MX_FMT_FP4)
     return fail(MX_ERR_SHAPE, "%s: act_format must be MX_FMT_FP8 = %d or MX_FMT_FP4 = %d (got %d)", fn, MX_FMT_FP8,
                 MX_FMT_FP4, act_format);
@@ -677,19 +697,21 @@ mx_status mm_fp4(const char* fn, const char* c_name, const char* j_name, const u
   if (J % 8 != 0) return fail(MX_ERR_SHAPE, "%s: %s=%lld is not a multiple of 8", fn, j_name, (long long)J);
   if (C > ((int64_t)1 << 23) || M >= ((int64_t)1 << 31) || !rowwise_blocks_fit(M, C))
     return fail(MX_ERR_SHAPE, "%s: too large (M=%lld %s=%lld)", fn, (long long)M, c_name, (long long)C);
+  if (none) return MX_OK;
   const size_t need = mx_grouped_mm_fp4_workspace_bytes(M, C, act_format);
   if (!ws || ws_bytes < need)
     return fail(MX_ERR_WORKSPACE, "%s: workspace of %zu bytes at %p, need %zu", fn, ws_bytes, ws, need);
   if (!aligned(ws, 256)) return fail(MX_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
-  if (M == 0 || J == 0) return MX_OK;
   if (C == 0) return fail(MX_ERR_SHAPE, "%s: no contraction (%s=0)", fn, c_name);
+  if (mxk::fp4_gemm_takes_bf16(M, J, C, E))
+    return gemm_fp4(a, nullptr, nullptr, act_format, q, s, MX_SCALES_GEMM, offs, M, J, C, E, nullptr, 0, out, 0, stream);
   uint8_t* qa = (uint8_t*)ws;
   uint8_t* sa = qa + align_up((size_t)M * (size_t)(act_format == MX_FMT_FP4 ? C / 2 : C), 256);
   const hipStream_t hs = (hipStream_t)stream;
   st = hip_status(act_format == MX_FMT_FP4 ? mxk::launch_quant_rowwise_fp4(a, M, C, qa, sa, M, hs)
                                            : mxk::launch_quant_rowwise(a, M, C, qa, sa, M, hs), fn);
   if (st != MX_OK) return st;
-  return mx_grouped_gemm_mxfp4(qa, sa, act_format, q, s, MX_SCALES_GEMM, offs, M, J, C, E, nullptr, 0, out, 0, stream);
+  return gemm_fp4(nullptr, qa, sa, act_format, q, s, MX_SCALES_GEMM, offs, M, J, C, E, nullptr, 0, out, 0, stream);
 }
 
 }  // namespace

@@ -17,33 +17,9 @@
 // rounds to nearest even and saturates two values in one instruction.
 #include "mx_device.h"
 #include "mx_kernels.h"
+#include "mx_quantize.h"
 
 namespace mxk {
-
-// E8M0 byte of an MXFP4 block from the bits of its largest |bf16|.
-__device__ __forceinline__ uint32_t e8m0_fp4_from_absbits(uint32_t amax_bits) {
-  if (amax_bits >= 0x7F80u) return 0xFFu;
-  const int e = (int)(amax_bits >> 7) - 2;
-  return (uint32_t)(e > 0 ? e : 0);
-}
-
-// Two bf16 values -> two E2M1 codes in byte SEL of `old`; the convert divides
-// by `scale` = 2^(byte - 127), given as the float whose exponent field is the
-// byte.
-template <int SEL>
-__device__ __forceinline__ uint32_t cvt2_e2m1(uint32_t old, uint32_t pair, float scale) {
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2_t, pair), scale, SEL);
-}
-
-// 8 bf16 values (4 dwords) of one block -> 8 codes in a dword.
-__device__ __forceinline__ uint32_t quant8_fp4(v4i w, uint32_t byte) {
-  const float scale = __uint_as_float(byte << 23);
-  uint32_t c = cvt2_e2m1<0>(0u, (uint32_t)w[0], scale);
-  c = cvt2_e2m1<1>(c, (uint32_t)w[1], scale);
-  c = cvt2_e2m1<2>(c, (uint32_t)w[2], scale);
-  c = cvt2_e2m1<3>(c, (uint32_t)w[3], scale);
-  return byte == 0xFFu ? 0u : c;
-}
 
 constexpr int kF4Threads = 256;
 

@@ -19,6 +19,7 @@
 
 #include "mx_device.h"
 #include "mx_kernels.h"
+#include "mx_quantize.h"
 #include "mx_rows_tiles.h"
 
 namespace mxk {
@@ -37,7 +38,40 @@ constexpr int kFmtE4M3 = 0, kFmtE2M1 = 4;      // the instruction's operand form
 constexpr int kSmBM = 64, kSmBN = 32, kSmWaves = 8;
 constexpr int kSmCT = kSmBM / 16, kSmRT = kSmBN / 16;
 
-template <int XF, bool OUT_F32>
+// 16 bytes of codes of four 16-byte pieces of bf16 values, in the lane's operand
+// layout, and its scale byte: the codes and bytes of the row quantizers.  E2M1:
+// the pieces are block g.  E4M3: two pieces of block g/2 and two of 2 + g/2, each
+// shared with the lanes of group g ^ 1.
+template <int XF>
+__device__ __forceinline__ void quantize_operand(const v4i w[4], int g, v4i x[2], int& scale) {
+  us2 m[2] = {__builtin_elementwise_max(absmax8x2(w[0]), absmax8x2(w[1])),
+              __builtin_elementwise_max(absmax8x2(w[2]), absmax8x2(w[3]))};
+  if (XF == kFmtE4M3) {
+    uint32_t byte[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t v = max(m[i][0], m[i][1]);
+      const auto o = __builtin_amdgcn_permlane16_swap(v, v, false, false);      // groups 0 0 2 2 and 1 1 3 3
+      byte[i] = e8m0_from_absbits(max(o[0], o[1]));
+      const uint32_t most = ((byte[i] + 8u) << 7 | 0x60u) * 0x10001u;
+      const v2i lo = quantize8(w[2 * i], byte[i], most), hi = quantize8(w[2 * i + 1], byte[i], most);
+      const bool nan = byte[i] == 0xFFu;
+      x[i] = nan ? (v4i){0x7F7F7F7F, 0x7F7F7F7F, 0x7F7F7F7F, 0x7F7F7F7F} : (v4i){lo[0], lo[1], hi[0], hi[1]};
+    }
+    // block g's byte: blocks 0 0 2 2 of the four groups, and 1 1 3 3
+    const auto o = __builtin_amdgcn_permlane32_swap(byte[0], byte[1], false, false);
+    scale = (int)(g & 1 ? o[1] : o[0]);
+  } else {
+    const us2 all = __builtin_elementwise_max(m[0], m[1]);
+    const uint32_t byte = e8m0_fp4_from_absbits(max(all[0], all[1]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[0][i] = (int)quant8_fp4(w[i], byte);
+    scale = (int)byte;
+  }
+}
+
+// BF16: the rows are a.A, quantized to XF here.
+template <int XF, bool OUT_F32, bool BF16>
 __global__ __launch_bounds__(kSmWaves * 64) void fp4_rows_small_kernel(Fp4GemmArgs a) {
   __shared__ int s_offs[kMaxExperts], s_pref[kMaxExperts], s_total;
   __shared__ v4f part[kSmWaves][kSmRT * kSmCT][64];
@@ -51,7 +85,7 @@ __global__ __launch_bounds__(kSmWaves * 64) void fp4_rows_small_kernel(Fp4GemmAr
   const int nx = (int)min((int64_t)kSmBM, i_end - i0);
   const int ny = (int)min((int64_t)kSmBN, a.J - j0);
   const int64_t ldx = XF == kFmtE4M3 ? a.Kc : a.Kc / 2, ldy = a.Kc / 2;
-  const __amdgpu_buffer_rsrc_t rx = rows::rsrc(a.X + i0 * ldx, nx * ldx);
+  const __amdgpu_buffer_rsrc_t rx = BF16 ? rows::rsrc(a.A + i0 * a.Kc, nx * a.Kc * 2) : rows::rsrc(a.X + i0 * ldx, nx * ldx);
   const __amdgpu_buffer_rsrc_t ry = rows::rsrc(a.Y + ((int64_t)e * a.J + j0) * ldy, ny * ldy);
   const uint8_t* sx = a.sX + i0 * 4 + g;
   const uint8_t* sy = a.sY + (int64_t)e * a.J * (a.Kc / 32) + j0 * 4 + g;
@@ -64,7 +98,7 @@ __global__ __launch_bounds__(kSmWaves * 64) void fp4_rows_small_kernel(Fp4GemmAr
     for (int c = 0; c < kSmCT; ++c) acc[r][c] = (v4f){0.f, 0.f, 0.f, 0.f};
   const int end = units * (wv + 1) / kSmWaves;
   for (int u = units * wv / kSmWaves; u < end; ++u) {
-    v4i y[kSmRT][2], x[kSmCT][2][XF == kFmtE4M3 ? 2 : 1];
+    v4i y[kSmRT][2], x[kSmCT][2][BF16 ? 4 : XF == kFmtE4M3 ? 2 : 1];
     int ys[kSmRT][2], xs[kSmCT][2];
     // a line's second chunk past the end is not multiplied
     const int ch[2] = {2 * u, min(2 * u + 1, nch - 1)};
@@ -83,7 +117,14 @@ __global__ __launch_bounds__(kSmWaves * 64) void fp4_rows_small_kernel(Fp4GemmAr
       const int row = 16 * c + l16;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (XF == kFmtE4M3) {
+        if constexpr (BF16) {
+          const int o = (int)(row * a.Kc + ch[i] * 128) * 2;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[c][i][k] = __builtin_amdgcn_raw_buffer_load_b128(
+                rx, o + (XF == kFmtE4M3 ? 32 * g + 16 * (k & 1) + 128 * (k >> 1) : 64 * g + 16 * k), 0, 0);
+          continue;
+        } else if constexpr (XF == kFmtE4M3) {
           x[c][i][0] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(row * ldx) + ch[i] * 128 + 16 * g, 0, 0);
           x[c][i][XF == kFmtE4M3] =
               __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(row * ldx) + ch[i] * 128 + 64 + 16 * g, 0, 0);
@@ -99,6 +140,12 @@ __global__ __launch_bounds__(kSmWaves * 64) void fp4_rows_small_kernel(Fp4GemmAr
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (2 * u + i >= nch) continue;
+        if constexpr (BF16) {
+          v4i codes[2];
+          quantize_operand<XF>(x[c][i], g, codes, xs[c][i]);
+          x[c][i][0] = codes[0];
+          x[c][i][1] = codes[1];
+        }
         v8i xv;
         if (XF == kFmtE4M3) xv = __builtin_shufflevector(x[c][i][0], x[c][i][XF == kFmtE4M3], 0, 1, 2, 3, 4, 5, 6, 7);
         else xv = __builtin_shufflevector(x[c][i][0], x[c][i][0], 0, 1, 2, 3, -1, -1, -1, -1);
@@ -458,13 +505,47 @@ __global__ __launch_bounds__(kThreads, 1) void fp4_rows_kernel(Fp4GemmArgs a) {
   }
 }
 
+// Number of groups that can hold rows.
+static int64_t live_groups(int64_t I, int64_t E) { return std::min(E, I); }
+
+// Small workgroups that cover the output, from the row count alone: each group
+// may add a partial tile.
+static int64_t small_count(int64_t I, int64_t J, int64_t E) {
+  return (I / kSmBM + live_groups(I, E)) * ((J + kSmBN - 1) / kSmBN);
+}
+
+// Small workgroups while there are about 2.5 of them per CU, the large tiles past
+// that.  Measured, E4M3 rows, small / large, us:
+//   E  1 4096 x 4096:   1 row 7 / 23    256 rows (640) 30 / 38   384 (896) 44 / 38
+//   E  2 4096 x 5120:   1 row 8 / 27    64 rows (512) 19 / 31    256 (1280) 68 / 47
+//   E  8 2048 x 7168:   1 row 18 / 36   16 rows (640) 24 / 36    64 (1024) 48 / 41
+//   E 16 8192 x 5120:   1 row (4352) 124 / 94, 256 rows 1097 / 151
+static bool small_tiles(int64_t I, int64_t J, int64_t E) { return small_count(I, J, E) <= 640; }
+
+// Every small workgroup quantizes its own rows where that is less than a launch:
+// one workgroup per CU, and up to 65536 values of 16-row tiles each.  Measured in
+// a graph, quantizer and product / one kernel, us (a call from the host saves 2.5
+// more):
+//   E 2  512 x  256:  1 row 6.6 / 5.2    64 rows (16384 values) 7.9 / 7.9
+//   E 4 1024 x  512:  1 row 6.7 / 5.6    64 rows (32768) 8.5 / 9.7
+//   E 1 4096 x 4096:  1 row 8.9 / 7.6    16 rows (65536) 10.7 / 10.3   32 13.1 / 16.4
+//   E 8 2048 x 7168:  1 row (114688, two workgroups per CU) 20.8 / 22.5
+bool fp4_gemm_takes_bf16(int64_t I, int64_t J, int64_t Kc, int64_t E) {
+  if (I == 0 || small_count(I, J, E) > 256) return false;
+  const int64_t rows = (I + live_groups(I, E) - 1) / live_groups(I, E);
+  return std::min<int64_t>(kSmBM, (rows + 15) / 16 * 16) * Kc <= 65536;
+}
+
+template <int XF, bool OUT_F32, bool BF16>
+static hipError_t launch_small(const Fp4GemmArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((fp4_rows_small_kernel<XF, OUT_F32, BF16>),
+                     dim3((unsigned)rows::grid<kSmBM, kSmBN>(a.I, a.J, a.E)), dim3(kSmWaves * 64), 0, st, a);
+  return hipGetLastError();
+}
+
 template <int XF, bool OUT_F32>
-static hipError_t launch_rows(const Fp4GemmArgs& a, bool small, hipStream_t st) {
-  if (small) {
-    hipLaunchKernelGGL((fp4_rows_small_kernel<XF, OUT_F32>), dim3((unsigned)rows::grid<kSmBM, kSmBN>(a.I, a.J, a.E)),
-                       dim3(kSmWaves * 64), 0, st, a);
-    return hipGetLastError();
-  }
+static hipError_t launch_rows(const Fp4GemmArgs& a, hipStream_t st) {
+  if (small_tiles(a.I, a.J, a.E)) return launch_small<XF, OUT_F32, false>(a, st);
   const size_t lds = (size_t)Stage<XF>::kBytes * Stage<XF>::kBufs;
   const hipError_t e = hipFuncSetAttribute((const void*)fp4_rows_kernel<XF, OUT_F32>,
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -476,17 +557,9 @@ static hipError_t launch_rows(const Fp4GemmArgs& a, bool small, hipStream_t st) 
 
 hipError_t launch_fp4_gemm(const Fp4GemmArgs& a, hipStream_t st) {
   if (a.I == 0 || a.J == 0) return hipSuccess;
-  // The small workgroups while about 2.5 of them per CU cover the output (their
-  // number from the row count alone: each group may add a partial tile), the
-  // large tiles past that.  Measured, E4M3 rows, small / large, us:
-  //   E  1 4096 x 4096:   1 row 7 / 23    256 rows (640) 30 / 38   384 (896) 44 / 38
-  //   E  2 4096 x 5120:   1 row 8 / 27    64 rows (512) 19 / 31    256 (1280) 68 / 47
-  //   E  8 2048 x 7168:   1 row 18 / 36   16 rows (640) 24 / 36    64 (1024) 48 / 41
-  //   E 16 8192 x 5120:   1 row (4352) 124 / 94, 256 rows 1097 / 151
-  const int64_t groups = std::min<int64_t>(a.E, a.I);
-  const bool small = (a.I / kSmBM + groups) * ((a.J + kSmBN - 1) / kSmBN) <= 640;
-  if (a.x_fp4) return a.out_f32 ? launch_rows<kFmtE2M1, true>(a, small, st) : launch_rows<kFmtE2M1, false>(a, small, st);
-  return a.out_f32 ? launch_rows<kFmtE4M3, true>(a, small, st) : launch_rows<kFmtE4M3, false>(a, small, st);
+  if (a.A) return a.x_fp4 ? launch_small<kFmtE2M1, false, true>(a, st) : launch_small<kFmtE4M3, false, true>(a, st);
+  if (a.x_fp4) return a.out_f32 ? launch_rows<kFmtE2M1, true>(a, st) : launch_rows<kFmtE2M1, false>(a, st);
+  return a.out_f32 ? launch_rows<kFmtE4M3, true>(a, st) : launch_rows<kFmtE4M3, false>(a, st);
 }
 
 }  // namespace mxk

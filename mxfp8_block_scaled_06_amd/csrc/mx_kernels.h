@@ -76,6 +76,7 @@ hipError_t launch_dequant_fp4(const uint8_t* q, const uint8_t* s, int64_t rows_t
                               int64_t gemm_rows_per_batch, hipStream_t st);
 // Rows-grouped product with MXFP4 weights (see mx_fp4_gemm.hip).
 struct Fp4GemmArgs {
+  const uint16_t* A;          // bf16 rows [I, Kc] instead of X and sX (see fp4_gemm_takes_bf16), or null
   const uint8_t* X;           // [I, Kc] E4M3, or [I, Kc/2] E2M1 with x_fp4
   const uint8_t* sX;          // [Kc/128, I, 4]
   const uint8_t* Y;           // [E, J, Kc/2] E2M1
@@ -87,6 +88,8 @@ struct Fp4GemmArgs {
   int E, x_fp4, out_f32;
 };
 hipError_t launch_fp4_gemm(const Fp4GemmArgs& a, hipStream_t st);
+// Whether a product of these sizes had better quantize its bf16 rows itself.
+bool fp4_gemm_takes_bf16(int64_t I, int64_t J, int64_t Kc, int64_t E);
 hipError_t launch_quant_weights_fp4(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* q, uint8_t* s,
                                     uint8_t* q_t, uint8_t* s_t, hipStream_t st);
 

@@ -33,11 +33,11 @@
 
 #include "mx_device.h"
 #include "mx_kernels.h"
+#include "mx_quantize.h"
 
 namespace mxk {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kMoeWaves = 8, kMoeThreads = kMoeWaves * 64;
@@ -201,29 +201,6 @@ __device__ __forceinline__ Spread spread_rows(uint32_t v) {
   return {{l[0], l[1]}, {u[0], u[1]}};
 }
 
-// Four packed bf16 pairs of a block with scale byte `byte` -> eight E4M3
-// codes.  The convert divides by the scale and rounds to nearest even but does
-// not saturate, so magnitudes are clamped to 448 * 2^(byte - 127) first, as
-// bf16 bits (1.75 * 2^(byte + 8 - 127): mantissa bits 0x60).
-__device__ __forceinline__ v2i quantize8(v4i w, uint32_t byte, uint32_t most) {
-  const float scale = __uint_as_float(byte << 23);
-  v2i q;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    s16x2 r = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t u = (uint32_t)w[2 * i + j];
-      const us2 m = __builtin_elementwise_min(__builtin_bit_cast(us2, u & 0x7FFF7FFFu), __builtin_bit_cast(us2, most));
-      const uint32_t v = __builtin_bit_cast(uint32_t, m) | (u & 0x80008000u);
-      if (j == 0) r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, v), scale, 0);
-      else r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, v), scale, 1);
-    }
-    q[i] = __builtin_bit_cast(int, r);
-  }
-  return q;
-}
-
 // x / (1 + 2^(-x log2 e)): the power by the hardware, with what the product
 // -x log2 e rounds away put back (2^-22 of it otherwise lost at x = -40), and a
 // reciprocal of one ulp; some 2^-22 of the value in all.  Below -88 it is -0.
@@ -233,14 +210,6 @@ __device__ __forceinline__ float silu(float x) {
   float p = __builtin_amdgcn_exp2f(t);
   p = fmaf(p * (t < 127.9f ? lo : 0.f), 0.6931471806f, p);
   return x * __builtin_amdgcn_rcpf(1.0f + p);
-}
-
-// Largest |bf16| bits of eight values, as a packed pair still to be combined.
-__device__ __forceinline__ us2 absmax8x2(v4i w) {
-  us2 m = __builtin_bit_cast(us2, (uint32_t)w[0] & 0x7FFF7FFFu);
-#pragma unroll
-  for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(us2, (uint32_t)w[i] & 0x7FFF7FFFu));
-  return m;
 }
 
 // x in LDS: 128 codes (eight 16-byte pieces) per token and chunk, and the four

@@ -34,7 +34,7 @@ def _resources(src, out):
     return res
 
 
-@pytest.mark.parametrize("src,kernels,matrix", [("mx_fp4.hip", 8, False), ("mx_fp4_gemm.hip", 8, True),
+@pytest.mark.parametrize("src,kernels,matrix", [("mx_fp4.hip", 8, False), ("mx_fp4_gemm.hip", 10, True),
                                                 ("mx_moe.hip", 12, True)])
 def test_no_scratch_and_two_waves_per_simd(tmp_path, src, kernels, matrix):
     res = _resources(src, tmp_path / "k.s")

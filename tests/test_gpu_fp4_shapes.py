@@ -292,3 +292,45 @@ def test_more_values_than_one_grid_axis_holds():
     assert torch.equal(v[-8:], mx.mx_dequantize_fp4(tq, ts)) and not v[:-8:4099].any()
     del q, s, v
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("counts,N,K", [([1], 8, 128), ([5, 0, 40, 19], 72, 384), ([16], 4096, 4096),
+                                        ([3, 61, 2], 512, 896), ([0, 0], 64, 128)])
+def test_rows_quantized_in_the_product_give_the_same_bits(counts, N, K, fmt):
+    """Small products quantize their bf16 rows themselves: the same codes and
+    scales as the quantizers', NaN blocks, zeros, subnormals and the largest
+    values included, so the same bits as the two calls."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    M, E = sum(counts), len(counts)
+    x = inp.random_bf16((M, K), seed=K, outliers=True)
+    if M > 3:
+        x[0, 5], x[1, 40], x[2, 100] = 0x7FC0, 0xFF80, 0x7F7F        # NaN, -Inf, the largest
+        x[3, :64] = 0
+        x[3, 64:96] = np.arange(32, dtype=np.uint16) | 0x8000        # subnormal, negative
+    W = to_dev_bf16(inp.random_bf16((E, -(-N // 128) * 128, K), seed=9, std=0.02))
+    qw, sw, _, _ = mx.mx_quantize_weights_fp4(W)
+    qw, sw = qw[:, :N].contiguous(), sw[:, :, :N].contiguous()
+    offs, xd = to_dev_i32(inp.offsets_from_counts(counts)), to_dev_bf16(x)
+    if fmt == "mxfp8":
+        q, s = mx.mx_quantize_rowwise(xd)
+        s = mx.mx_scales_to_gemm_layout(s) if M else s.view(K // 128, 0, 4)
+    else:
+        q, s = mx.mx_quantize_rowwise_fp4(xd, scale_layout="gemm")
+    want = mx.mx_grouped_gemm_mxfp4(q, s, qw, sw, offs, x_format=fmt)
+    got = mx.mx_grouped_mm_fwd_fp4(xd, qw, sw, offs, act_format=fmt)
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    if M > 3:
+        assert torch.isnan(got[:2]).all() and not torch.isnan(got[2:]).any()
+    # on another stream, twice in a graph, rows behind the last group left alone
+    buf = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    ws = torch.empty(max(1, mx.mx_grouped_mm_fp4_workspace_bytes(M, K, fmt)), dtype=torch.uint8, device="cuda:0")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mx.mx_grouped_mm_fwd_fp4(xd, qw, sw, offs, act_format=fmt, out=buf[:M], ws=ws)
+    for _ in range(3):
+        buf.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(buf[:M].view(torch.int16), want.view(torch.int16)) and (buf[M:] == 7).all()
