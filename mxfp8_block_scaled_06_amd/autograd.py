@@ -67,6 +67,7 @@ class WeightCache:
     def get(self, W, as_experts=None, weight_format="mxfp8"):
         """The 4-tuple of W (or of `as_experts`, a 3-D view of W such as a
         dense weight's unsqueeze(0), while the entry stays keyed on W)."""
+        _format(weight_format, "weight_format")
         key = (id(W), weight_format)
         ent = self._entries.get(key)
         if ent is not None and ent[0]() is W and ent[1] == self._key(W):

@@ -180,3 +180,11 @@ def test_sizes_past_one_launch_are_refused():
     assert g(FAKE, FAKE, 0, FAKE, FAKE, G, FAKE, 1, (1 << 31) - 8, 128, 1, None, 0, FAKE, 0, None) == 2
     assert "tiles" in _err(lib)
     assert g(FAKE, FAKE, 0, FAKE, FAKE, G, FAKE, 1 << 21, 1 << 20, 128, 1024, None, 0, FAKE, 0, None) == 2
+
+
+def test_caches_refuse_unknown_formats():
+    import torch
+    from mxfp8_block_scaled_06_amd.autograd import WeightCache
+    _lib()
+    with pytest.raises(ValueError, match="weight_format"):
+        WeightCache().get(torch.zeros((1, 128, 128), dtype=torch.bfloat16), weight_format="fp4")
