@@ -555,10 +555,11 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
 
 // ---------------------------------------------------------------------------
 // Down projection and the weighted sum over a token's experts.  A work entry
-// is one hit expert with up to 16 CT of its tokens (columns of matrix tiles); the wave's share is a run of (entry, line) units, of which D are in
-// registers or on their way, across the border between entries.  At the end
-// of an entry its sums, times the combine weights, are added to the wave's own
-// sums of those tokens in LDS.
+// is one hit expert with up to 16 CT of its tokens (columns of matrix tiles); the
+// wave's share is a run of (entry, line) units, of which D are in registers or on
+// their way, across the border between entries.  At the end of an entry its sums,
+// times the combine weights, are added to the wave's own sums of those tokens in
+// LDS.
 // ---------------------------------------------------------------------------
 template <int WF, int RT, int CT, int D>
 __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))) void moe_down_kernel(MoeArgs a,
