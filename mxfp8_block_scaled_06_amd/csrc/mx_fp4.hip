@@ -10,11 +10,12 @@
 // NaN in the matrix cores).  Two codes to a byte, the even element of the
 // contraction axis in the low four bits.
 //
-// All of it is HBM-bound streaming (65600 x 5120: quantized in 139 us, 6.1 TB/s,
-// restored in 162, 5.2 TB/s; the weights of 16 x 8192 x 5120 in both orientations
-// in 356 us, 5.8 TB/s, restored from one in 300 to 340): the amax is an integer max over |bf16|
-// bits, the scale its exponent field, and v_cvt_scalef32_pk_fp4_bf16 scales,
-// rounds to nearest even and saturates two values in one instruction.
+// All of it is HBM-bound streaming (65600 x 5120: quantized in 140 us, 6.1 TB/s,
+// restored in 151, 5.6 TB/s; the weights of 16 x 8192 x 5120 in both orientations
+// in 356 us, 5.8 TB/s, restored from one in 300 to 340): the amax is an integer
+// max over |bf16| bits, the scale its exponent field, and
+// v_cvt_scalef32_pk_fp4_bf16 scales, rounds to nearest even and saturates two
+// values in one instruction.
 #include "mx_device.h"
 #include "mx_kernels.h"
 #include "mx_quantize.h"
@@ -31,7 +32,9 @@ constexpr int kF4Threads = 256;
 // 64-bit divisions and a wave's 16 scales lay in four far lines.
 constexpr int kT4Cols = 256, kT4Rows = kF4Threads / 32;   // rows of one step
 // Steps per workgroup: 8 keep enough loads in flight for the bandwidth, 1 spreads
-// a small input over the CUs.
+// an input of fewer than 1024 such tiles over the CUs.  Restoring 16 x 8192 x 5120:
+// 8 steps 338 us, 4 352, 2 372; 4 x 1024 x 512 (128 tiles): 1 step 4.3, 8 steps 7.5
+// (quantizing it 3.7 and 4.3 to 5.2).
 constexpr int kT4Steps = 8;
 
 inline int t4_steps(int64_t batch, int64_t rows, int64_t cols) {
