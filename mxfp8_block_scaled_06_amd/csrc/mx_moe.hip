@@ -250,7 +250,10 @@ static_assert(kMoeGrid == 1 << 8, "shares are taken by shifts");
 template <int CT>
 constexpr int kParts = CT == 1 ? 2 : 1;
 
-template <int WF, int CT, int D>
+// ONE: a single token, whose experts every wave finds in registers, without the
+// lists in LDS and their barriers (by the cycle counter 5000 cycles of the
+// kernel's 34000).
+template <int WF, int CT, bool ONE, int D>
 __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))) void moe_gate_up_kernel(MoeArgs a,
                                                                                                           int rows) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -266,7 +269,7 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
   uint32_t* rsc = (uint32_t*)(smem + nch * rows * kCodes);
   int* s_ids = (int*)(smem + nch * rows * kRec);
   int *s_count = s_ids + a.T * a.topk, *s_upto = s_count + a.E;
-  load_ids(a, s_ids, s_count);
+  if constexpr (!ONE) load_ids(a, s_ids, s_count);
   // Work entry `entry` for the workgroup, by wave 0: its expert, pass and tokens;
   // by the one that has the entry's first block, what the down kernel needs.
   auto enter = [&](int entry, bool first_block) __attribute__((always_inline)) {
@@ -301,37 +304,73 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
     }
   };
   const uint32_t wg = blockIdx.x;
-  if (wv == 0) {
-    // entries (low half) and tokens (high half) of the experts up to each one:
-    // at most 4096 of both
-    int before = 0, hit = 0;
-    for (int base = 0; base < a.E; base += 64) {
-      const int c = base + lane < a.E ? s_count[base + lane] : 0;
-      const int v = before + scan((c + rows - 1) / rows | c << 16);
-      if (base + lane < a.E) s_upto[base + lane] = v;
-      before = __builtin_amdgcn_readlane(v, 63);
-      hit += __builtin_popcountll(__ballot(c > 0));
+  uint32_t total;
+  int id = -1, rank = 0;      // ONE: slot `lane`'s expert, and its place among the hit ones
+  bool first = false;         // the slot is the first that names it
+  if constexpr (ONE) {
+    id = lane < a.topk ? a.ids[lane] : -1;
+    first = id >= 0 && id < a.E;
+    for (int j = 0; j < a.topk; ++j) {
+      const int other = __builtin_amdgcn_readlane(id, j);
+      first &= j >= lane || other != id;
     }
-    const uint32_t total = (uint32_t)(before & 0xFFFF) * all;
-    if (lane == 0) {
-      s_total = (int)total;
-      if (wg == 0) a.meta[0] = hit;
+    const uint64_t firsts = __ballot(first);
+    for (int j = 0; j < a.topk; ++j) {
+      const int other = __builtin_amdgcn_readlane(id, j);
+      rank += (firsts >> j & 1) != 0 && other < id;
     }
+    const int hit = __builtin_popcountll(firsts);
+    total = (uint32_t)hit * all;
+    if (wg == 0 && wv == 0) {
+      // for the down kernel, as in `enter`
+      if (first) {
+        float c = 0.f;
+        for (int k = 0; k < a.topk; ++k)
+          if (a.ids[k] == id) c += a.combine[k];
+        a.list[rank] = make_int2(lane, __float_as_int(c));
+        a.meta[1 + rank] = id | 1 << 16;
+      }
+      if (lane == 0) a.meta[0] = hit;
+    }
+  } else {
+    if (wv == 0) {
+      // entries (low half) and tokens (high half) of the experts up to each one:
+      // at most 4096 of both
+      int before = 0, hit = 0;
+      for (int base = 0; base < a.E; base += 64) {
+        const int c = base + lane < a.E ? s_count[base + lane] : 0;
+        const int v = before + scan((c + rows - 1) / rows | c << 16);
+        if (base + lane < a.E) s_upto[base + lane] = v;
+        before = __builtin_amdgcn_readlane(v, 63);
+        hit += __builtin_popcountll(__ballot(c > 0));
+      }
+      if (lane == 0) {
+        s_total = (before & 0xFFFF) * all;
+        if (wg == 0) a.meta[0] = hit;
+      }
+    }
+    __syncthreads();
+    total = (uint32_t)uni(s_total);
   }
-  __syncthreads();
-  const uint32_t total = (uint32_t)uni(s_total);
   const int start = (int)((uint64_t)total * wg >> 8), stop = (int)((uint64_t)total * (wg + 1) >> 8);
   for (int at = start; at < stop;) {
     const int entry = at / all, b0 = at - entry * all, nb = min(all - b0, stop - at);
     if (at > start) __syncthreads();      // the lists and x of the entry before
-    if (wv == 0) enter(entry, b0 == 0);
-    __syncthreads();
+    int e, m0 = 0, mp = 1, item_of_one = 0;
+    if constexpr (ONE) {
+      item_of_one = __builtin_ctzll(__ballot(first && rank == entry));
+      e = __builtin_amdgcn_readlane(id, item_of_one);
+    } else {
+      if (wv == 0) enter(entry, b0 == 0);
+      __syncthreads();
+      e = uni(s_expert);
+      // an expert's entries share its tokens evenly: a second column tile only
+      // where the first one is full
+      const int me = uni(s_count[e]), passes = (me + rows - 1) / rows, per = (me + passes - 1) / passes;
+      m0 = uni(s_pass) * per;
+      mp = min(me - m0, per);
+    }
     at += nb;
-    const int e = uni(s_expert);
-    // an expert's entries share its tokens evenly: a second column tile only
-    // where the first one is full
-    const int me = uni(s_count[e]), passes = (me + rows - 1) / rows, per = (me + passes - 1) / passes;
-    const int m0 = uni(s_pass) * per, mp = min(me - m0, per);
     const bool wide = CT > 1 && mp > kMoeCols;        // a second column tile has tokens
     // the wave's lines, and the first one's block and place in it
     const int begin = share(nb * lines, wv), end = share(nb * lines, wv + 1);
@@ -348,7 +387,7 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int q = max(min(q0 + 4 * i + g, q_end - 1), 0), ch = (int)(q * inv >> 17), row = q - ch * mp;
-        xw[i] = *(const v4i*)(a.x + (int64_t)s_token[m0 + row] * K + ch * 128 + 8 * l16);
+        xw[i] = *(const v4i*)(a.x + (int64_t)(ONE ? 0 : s_token[m0 + row]) * K + ch * 128 + 8 * l16);
       }
     };
     auto store_x = [&](int q0) __attribute__((always_inline)) {
@@ -395,7 +434,7 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
       const float mul = inv_scale_from_e8m0(nan ? 127u : byte);
       const int token = kMoeCols * c + l16;
       if (token < mp) {
-        const int64_t item = s_item[m0 + token];
+        const int64_t item = ONE ? item_of_one : s_item[m0 + token];
         const int n0 = (b0 + b) * kMoeRows;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -725,7 +764,7 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
   }
 }
 
-template <int WF, int RT, int CT>
+template <int WF, int RT, int CT, bool ONE = false>
 static hipError_t launch_moe(const MoeArgs& a, size_t down, hipStream_t st) {
   constexpr int DU = 2, DD = 2;
   const int64_t n = (int64_t)a.T * a.topk, slots = std::min<int64_t>(a.E, n);
@@ -734,13 +773,13 @@ static hipError_t launch_moe(const MoeArgs& a, size_t down, hipStream_t st) {
   const int64_t fit = (kLds - kMoeWaves * kParts<CT> * 1024 - kMoeMaxTokens * 8 - 256 - lists) / per_row;
   const int rows = (int)std::min<int64_t>(std::min(a.T, CT * kMoeCols), fit);
   const size_t up = (size_t)(rows * per_row + lists);
-  hipError_t e = hipFuncSetAttribute((const void*)moe_gate_up_kernel<WF, CT, DU>,
+  hipError_t e = hipFuncSetAttribute((const void*)moe_gate_up_kernel<WF, CT, ONE, DU>,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)up);
   if (e != hipSuccess) return e;
   e = hipFuncSetAttribute((const void*)moe_down_kernel<WF, RT, CT, DD>, hipFuncAttributeMaxDynamicSharedMemorySize,
                           (int)down);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_gate_up_kernel<WF, CT, DU>), dim3(kMoeGrid), dim3(kMoeThreads), up, st, a, rows);
+  hipLaunchKernelGGL((moe_gate_up_kernel<WF, CT, ONE, DU>), dim3(kMoeGrid), dim3(kMoeThreads), up, st, a, rows);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((moe_down_kernel<WF, RT, CT, DD>), dim3((unsigned)(a.K / (16 * RT))), dim3(kMoeThreads), down, st, a,
@@ -763,6 +802,7 @@ static size_t down_lds(const MoeArgs& a, int rt) {
 hipError_t launch_moe_few_tokens(const MoeArgs& a, hipStream_t st) {
   const size_t two = down_lds(a, 2), one = down_lds(a, 1);
   const bool wide = (int64_t)a.T * a.topk > 8 * (int64_t)a.E;
+  if (a.T == 1) return a.w_fp4 ? launch_moe<kFmtE2M1, 2, 1, true>(a, two, st) : launch_moe<kFmtE4M3, 2, 1, true>(a, two, st);
   if (two + 64 <= kLds) {
     if (a.w_fp4) return wide ? launch_moe<kFmtE2M1, 2, 2>(a, two, st) : launch_moe<kFmtE2M1, 2, 1>(a, two, st);
     return wide ? launch_moe<kFmtE4M3, 2, 2>(a, two, st) : launch_moe<kFmtE4M3, 2, 1>(a, two, st);

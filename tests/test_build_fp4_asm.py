@@ -35,7 +35,7 @@ def _resources(src, out):
 
 
 @pytest.mark.parametrize("src,kernels,matrix", [("mx_fp4.hip", 8, False), ("mx_fp4_gemm.hip", 10, True),
-                                                ("mx_moe.hip", 12, True)])
+                                                ("mx_moe.hip", 14, True)])
 def test_no_scratch_and_two_waves_per_simd(tmp_path, src, kernels, matrix):
     res = _resources(src, tmp_path / "k.s")
     assert len(res) == kernels, sorted(res)

@@ -5,6 +5,8 @@ random shapes, and all of them in one program (train, quantize, decode).
 
 Tolerances are the oracle's (oracle/compare.py, oracle/moe.py)."""
 
+import contextlib
+
 import numpy as np
 import pytest
 
@@ -334,3 +336,31 @@ def test_rows_quantized_in_the_product_give_the_same_bits(counts, N, K, fmt):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(buf[:M].view(torch.int16), want.view(torch.int16)) and (buf[M:] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("ids,E,K,N", [
+    ([3], 5, 128, 128), ([4, 1, 4, 0, 1], 6, 384, 640), ([-1, 7, 2, 9, 2], 8, 256, 256), ([-1], 2, 128, 128),
+    (list(range(31, -1, -1)), 40, 128, 256), ([1023, 0, 512, 1 << 30], 1024, 128, 128), ([5, 3, 0, 2, 7, 6, 1, 4], 8, 256, 4096),
+])
+def test_one_token_finds_the_experts_that_a_batch_finds(ids, E, K, N, fmt):
+    """A single token's experts are found in registers: the same bits as with a
+    second token that names none, repeated and invalid ids included."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    log(f"moe one token {ids} E={E} K={K} N={N} {fmt}")
+    x = to_dev_bf16(inp.random_bf16((2, K), seed=E + N, outliers=True))
+    q = mx.mx_quantize_weights_fp4 if fmt == "mxfp4" else mx.mx_quantize_weights
+    w13 = q(to_dev_bf16(inp.random_bf16((E, 2 * N, K), seed=1, std=0.05)))[:2]
+    w2 = q(to_dev_bf16(inp.random_bf16((E, K, N), seed=2, std=0.05)))[:2]
+    i = torch.full((2, len(ids)), -1, dtype=torch.int32, device="cuda:0")
+    i[0] = torch.tensor(ids, dtype=torch.int32)
+    c = torch.rand((2, len(ids)), device="cuda:0")
+    two = mx.mx_moe_few_tokens(x, i, c, w13, w2, weight_format=fmt, check=False)
+    one = mx.mx_moe_few_tokens(x[:1].contiguous(), i[:1].contiguous(), c[:1].contiguous(), w13, w2, weight_format=fmt,
+                               check=False)
+    assert torch.equal(one[0], two[0]) and not two[1].any()
+    if any(0 <= e < E for e in ids):
+        assert one.any()
+    with pytest.raises(ValueError, match="outside") if any(not 0 <= e < E for e in ids) else contextlib.nullcontext():
+        mx.mx_moe_few_tokens(x[:1].contiguous(), i[:1].contiguous(), c[:1].contiguous(), w13, w2, weight_format=fmt)
