@@ -203,13 +203,18 @@ __device__ __forceinline__ Spread spread_rows(uint32_t v) {
 
 // x / (1 + 2^(-x log2 e)): the power by the hardware, with what the product
 // -x log2 e rounds away put back (2^-22 of it otherwise lost at x = -40), and a
-// reciprocal of one ulp; some 2^-22 of the value in all.  Below -88 it is -0.
+// reciprocal of one ulp; some 2^-22 of the value in all, over the whole range of
+// x.  From 2^100 on the one is lost beside the power, which is taken with 2^-160:
+// its reciprocal would be subnormal past 2^126, which the hardware makes zero, and
+// silu(-88) is -5.3e-37.  Where the product itself overflows (x past 2.36e38) the
+// power is 0 or so large that the result is, with nothing to put back.
 __device__ __forceinline__ float silu(float x) {
-  const float t = fminf(-x * 1.442695041f, 127.9f);
+  const float y = -x * 1.442695041f, t = fminf(y, 280.f);
   const float lo = fmaf(-x, 1.925963033e-8f, fmaf(-x, 1.442695041f, -t));
-  float p = __builtin_amdgcn_exp2f(t);
-  p = fmaf(p * (t < 127.9f ? lo : 0.f), 0.6931471806f, p);
-  return x * __builtin_amdgcn_rcpf(1.0f + p);
+  const bool far = t > 100.f;
+  float p = __builtin_amdgcn_exp2f(far ? t - 160.f : t);
+  p = fmaf(p * (fabsf(y) < 280.f ? lo : 0.f), 0.6931471806f, p);
+  return __builtin_ldexpf(x * __builtin_amdgcn_rcpf((far ? 0.f : 1.f) + p), far ? -160 : 0);
 }
 
 // x in LDS: 128 codes (eight 16-byte pieces) per token and chunk, and the four
