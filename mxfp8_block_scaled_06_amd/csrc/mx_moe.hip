@@ -769,20 +769,26 @@ __global__ __launch_bounds__(kMoeThreads) __attribute__((amdgpu_waves_per_eu(2))
   }
 }
 
+// The most dynamic LDS a launch of the kernels may ask for, beside their static
+// arrays: a kernel's limit is the process's, so it is the same in every call.
+template <int CT>
+constexpr int kGateLds = kLds - kMoeWaves * kParts<CT> * 1024 - kMoeMaxTokens * 8 - 256;
+constexpr int kDownLds = kLds - 64;
+
 template <int WF, int RT, int CT, bool ONE = false>
 static hipError_t launch_moe(const MoeArgs& a, size_t down, hipStream_t st) {
   constexpr int DU = 2, DD = 2;
   const int64_t n = (int64_t)a.T * a.topk, slots = std::min<int64_t>(a.E, n);
   // x of as many tokens as LDS holds beside the partial sums and the lists
   const int64_t per_row = a.K / 128 * kRec, lists = (n + 2 * a.E) * 4;
-  const int64_t fit = (kLds - kMoeWaves * kParts<CT> * 1024 - kMoeMaxTokens * 8 - 256 - lists) / per_row;
+  const int64_t fit = (kGateLds<CT> - lists) / per_row;
   const int rows = (int)std::min<int64_t>(std::min(a.T, CT * kMoeCols), fit);
   const size_t up = (size_t)(rows * per_row + lists);
   hipError_t e = hipFuncSetAttribute((const void*)moe_gate_up_kernel<WF, CT, ONE, DU>,
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)up);
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, kGateLds<CT>);
   if (e != hipSuccess) return e;
   e = hipFuncSetAttribute((const void*)moe_down_kernel<WF, RT, CT, DD>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                          (int)down);
+                          kDownLds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((moe_gate_up_kernel<WF, CT, ONE, DU>), dim3(kMoeGrid), dim3(kMoeThreads), up, st, a, rows);
   e = hipGetLastError();
@@ -808,7 +814,7 @@ hipError_t launch_moe_few_tokens(const MoeArgs& a, hipStream_t st) {
   const size_t two = down_lds(a, 2), one = down_lds(a, 1);
   const bool wide = (int64_t)a.T * a.topk > 8 * (int64_t)a.E;
   if (a.T == 1) return a.w_fp4 ? launch_moe<kFmtE2M1, 2, 1, true>(a, two, st) : launch_moe<kFmtE4M3, 2, 1, true>(a, two, st);
-  if (two + 64 <= kLds) {
+  if (two <= kDownLds) {
     if (a.w_fp4) return wide ? launch_moe<kFmtE2M1, 2, 2>(a, two, st) : launch_moe<kFmtE2M1, 2, 1>(a, two, st);
     return wide ? launch_moe<kFmtE4M3, 2, 2>(a, two, st) : launch_moe<kFmtE4M3, 2, 1>(a, two, st);
   }
