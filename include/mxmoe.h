@@ -443,8 +443,9 @@ mx_status mx_grouped_gemm_mxfp4(const uint8_t* X, const uint8_t* sX, int x_forma
 /* mx_grouped_mm_fwd_q / _dgrad_q with MXFP4 weights, (q, s) respectively
  * (q_t, s_t) of mx_quantize_weights_fp4; the activations are quantized to
  * act_format in the workspace, or by a small product itself (with the same
- * result).  M or the output's columns 0: nothing is read.  fwd requires K % 128 == 0 and N % 8 == 0,
- * dgrad N % 128 == 0 and K % 8 == 0.  ws: mx_grouped_mm_fp4_workspace_bytes
+ * result).  M or the output's columns 0: nothing is read.  fwd requires
+ * K % 128 == 0 and N % 8 == 0, dgrad N % 128 == 0 and K % 8 == 0; M < 2^31 and
+ * fewer than 2^32 blocks of activations.  ws: mx_grouped_mm_fp4_workspace_bytes
  * of M rows and C contraction elements (K for fwd, N for dgrad), 256-byte
  * aligned; 0 for sizes or a format that the call refuses. */
 size_t mx_grouped_mm_fp4_workspace_bytes(int64_t M, int64_t C, int act_format);

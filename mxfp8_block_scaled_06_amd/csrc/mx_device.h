@@ -90,6 +90,14 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   return v;
 }
 
+// `n` workgroups of up to 1023 threads, on a second axis past 2^22 of them: a
+// launch takes fewer than 2^32 threads along an axis.
+inline dim3 wide_grid(int64_t n) {
+  const int64_t x = n < ((int64_t)1 << 22) ? n : (int64_t)1 << 22;
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+__device__ __forceinline__ int64_t wide_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 __device__ __forceinline__ void wait_vmcnt0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 }  // namespace mxk

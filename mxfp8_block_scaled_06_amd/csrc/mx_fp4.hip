@@ -43,13 +43,6 @@ inline int t4_steps(int64_t batch, int64_t rows, int64_t cols) {
              : 1;
 }
 
-// `n` workgroups: a launch takes fewer than 2^32 threads along an axis.
-inline dim3 wide_grid(int64_t n) {
-  const int64_t x = n < ((int64_t)1 << 22) ? n : (int64_t)1 << 22;
-  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
-}
-__device__ __forceinline__ int64_t wide_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
-
 inline dim3 t4_grid(int64_t batch, int64_t rows, int64_t cols, int steps) {
   return wide_grid(batch * ((rows + kT4Rows * steps - 1) / (kT4Rows * steps)) * ((cols + kT4Cols - 1) / kT4Cols));
 }

@@ -51,7 +51,7 @@ __global__ __launch_bounds__(kRowThreads) void quant_rowwise_kernel(const uint16
                                                                     uint8_t* __restrict__ s,
                                                                     uint32_t kb_per_row,
                                                                     uint32_t rows_per_batch) {
-  const int64_t base = (int64_t)blockIdx.x * (kRowThreads * kRowU) + threadIdx.x;
+  const int64_t base = wide_block() * (kRowThreads * kRowU) + threadIdx.x;
   v4i w[kRowU];
 #pragma unroll
   for (int u = 0; u < kRowU; ++u) {
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(kRowThreads) void quant_rowwise_gather_kernel(const
                                                                            uint8_t* __restrict__ s,
                                                                            uint32_t chunks_per_row,
                                                                            uint32_t out_rows) {
-  const int64_t base = (int64_t)blockIdx.x * (kRowThreads * kRowU) + threadIdx.x;
+  const int64_t base = wide_block() * (kRowThreads * kRowU) + threadIdx.x;
   auto row_of = [&](int64_t idx) -> uint32_t {
     return NARROW ? (uint32_t)idx / chunks_per_row : (uint32_t)(idx / chunks_per_row);
   };
@@ -635,7 +635,7 @@ hipError_t launch_quant_rowwise(const uint16_t* x, int64_t rows_total, int64_t c
   if (nchunks == 0) return hipSuccess;
   const int64_t per_block = (int64_t)kRowThreads * kRowU;
   const int64_t grid = (nchunks + per_block - 1) / per_block;
-  hipLaunchKernelGGL(quant_rowwise_kernel, dim3((unsigned)grid), dim3(kRowThreads), 0, st, x, nchunks, q, s,
+  hipLaunchKernelGGL(quant_rowwise_kernel, wide_grid(grid), dim3(kRowThreads), 0, st, x, nchunks, q, s,
                      (uint32_t)(cols / 32), (uint32_t)gemm_rows_per_batch);
   return hipGetLastError();
 }
@@ -663,10 +663,10 @@ hipError_t launch_quant_rowwise_gather(const uint16_t* x, int64_t src_rows, cons
   const int64_t per_block = (int64_t)kRowThreads * kRowU;
   const int64_t grid = (nchunks + per_block - 1) / per_block;
   if (nchunks <= (int64_t)UINT32_MAX)
-    hipLaunchKernelGGL(quant_rowwise_gather_kernel<true>, dim3((unsigned)grid), dim3(kRowThreads), 0, st, x, src_rows,
+    hipLaunchKernelGGL(quant_rowwise_gather_kernel<true>, wide_grid(grid), dim3(kRowThreads), 0, st, x, src_rows,
                        rows, nchunks, cols, q, s, (uint32_t)(cols / 8), (uint32_t)M);
   else
-    hipLaunchKernelGGL(quant_rowwise_gather_kernel<false>, dim3((unsigned)grid), dim3(kRowThreads), 0, st, x, src_rows,
+    hipLaunchKernelGGL(quant_rowwise_gather_kernel<false>, wide_grid(grid), dim3(kRowThreads), 0, st, x, src_rows,
                        rows, nchunks, cols, q, s, (uint32_t)(cols / 8), (uint32_t)M);
   return hipGetLastError();
 }

@@ -41,3 +41,31 @@ def test_layers_of_all_shapes_share_one_lds_limit_per_kernel():
         for launch in call.launches:
             assert launch.lds <= min(limits[launch.kernel]) and max(limits[launch.kernel]) <= CU_LDS
     assert all(len(v) == 1 for v in limits.values()), limits
+
+
+def test_threads_of_a_launch_stay_below_the_limit_of_an_axis():
+    """A launch takes fewer than 2^32 threads along an axis.  Up to the documented
+    2^32 - 1 blocks of 32 the row quantizers, alone or in a product, need more."""
+    rows, cols, tiny = (1 << 24) - 1, 1 << 13, 64      # 2^32 - 2^8 blocks
+    need = 1 << 60
+    calls = record([
+        ("mx_quantize_rowwise", (P, 1, rows, cols, P, P, None)),
+        ("mx_quantize_rowwise_gather", (P, 100, P, rows, cols, P, P, None)),
+        ("mx_quantize_rowwise_fp4", (P, 1, rows, cols, P, P, mx.SCALES_ROWMAJOR, None)),
+        ("mx_quantize_rowwise_fp4", (P, 1, rows, cols, P, P, mx.SCALES_GEMM, None)),
+        ("mx_dequantize_fp4", (P, P, 1, rows, cols, mx.SCALES_ROWMAJOR, P, None)),
+        ("mx_dequantize_fp4", (P, P, 1, rows, cols, mx.SCALES_GEMM, P, None)),
+        ("mx_grouped_mm_fwd_q", (P, P, P, P, rows, tiny, cols, 1, P, P, need, None)),
+        ("mx_grouped_mm_dgrad_q", (P, P, P, P, rows, cols, tiny, 1, P, P, need, None)),
+        ("mx_grouped_mm_fwd_fp4", (P, P, P, P, rows, tiny, cols, 1, 0, P, P, need, None)),
+        ("mx_grouped_mm_fwd_fp4", (P, P, P, P, rows, tiny, cols, 1, 1, P, P, need, None)),
+        ("mx_grouped_mm_dgrad_fp4", (P, P, P, P, rows, cols, tiny, 1, 0, P, P, need, None)),
+    ])
+    for i, call in enumerate(calls):
+        assert call.status == 0, (i, call.text)
+        assert call.launches
+        for launch in call.launches:
+            assert max(launch.threads) < 1 << 32, (launch.kernel, launch.grid)
+            assert launch.grid[1] <= 65535 and launch.grid[2] <= 65535, (launch.kernel, launch.grid)
+    quantizer = calls[0].launches[0]
+    assert quantizer.grid[0] * quantizer.grid[1] * quantizer.block[0] * 16 >= rows * cols      # 16 values a thread
