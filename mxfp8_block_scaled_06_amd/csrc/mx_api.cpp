@@ -607,6 +607,14 @@ mx_status mx_quantize_weights_fp4(const uint16_t* w, int64_t E, int64_t N, int64
 
 namespace {
 
+// A launch's workgroups: 512 threads per 256 x 256 tile, and fewer than 2^32
+// threads (the small tiles cover at most 2.5 times the CUs).
+mx_status check_fp4_tiles(const char* fn, int64_t I, int64_t J, int64_t E) {
+  if ((I < E ? I : I / 256 + E + 1) * (J / 256 + 1) >= ((int64_t)1 << 23) - 256)
+    return fail(MX_ERR_SHAPE, "%s: too many output tiles for one launch", fn);
+  return MX_OK;
+}
+
 // The rows-grouped product with MXFP4 weights, of MX rows (X, sX) or of bf16 rows
 // A that the kernel quantizes itself.
 mx_status gemm_fp4(const uint16_t* A, const uint8_t* X, const uint8_t* sX, int x_format, const uint8_t* Y,
@@ -635,10 +643,8 @@ mx_status gemm_fp4(const uint16_t* A, const uint8_t* X, const uint8_t* sX, int x
   if (!aligned(A, 16) || !aligned(X, 16) || !aligned(Y, 16) || !aligned(C, 16) || !aligned(sX, 4) || !aligned(sY, 4) ||
       !aligned(offs, 4) || !aligned(row_map, 4))
     return fail(MX_ERR_ALIGN, "%s: X, Y, C must be 16-byte and scales, offsets and row_map 4-byte aligned", fn);
-  // a workgroup of 512 threads per 256 x 256 tile, and fewer than 2^32 threads (the
-  // small tiles cover at most 2.5 times the CUs)
-  if ((I < E ? I : I / 256 + E + 1) * (J / 256 + 1) >= ((int64_t)1 << 23) - 256)
-    return fail(MX_ERR_SHAPE, "%s: too many output tiles for one launch", fn);
+  const mx_status st = check_fp4_tiles(fn, I, J, E);
+  if (st != MX_OK) return st;
   mxk::Fp4GemmArgs a{};
   a.A = A;
   a.X = X;
@@ -698,6 +704,9 @@ mx_status mm_fp4(const char* fn, const char* c_name, const char* j_name, const u
   if (C > ((int64_t)1 << 23) || M >= ((int64_t)1 << 31) || !rowwise_blocks_fit(M, C))
     return fail(MX_ERR_SHAPE, "%s: too large (M=%lld %s=%lld)", fn, (long long)M, c_name, (long long)C);
   if (none) return MX_OK;
+  // what the product would refuse, before the rows are quantized
+  if ((st = check_fp4_tiles(fn, M, J, E)) != MX_OK) return st;
+  if (!aligned(s, 4)) return fail(MX_ERR_ALIGN, "%s: weight scales must be 4-byte aligned", fn);
   const size_t need = mx_grouped_mm_fp4_workspace_bytes(M, C, act_format);
   if (!ws || ws_bytes < need)
     return fail(MX_ERR_WORKSPACE, "%s: workspace of %zu bytes at %p, need %zu", fn, ws_bytes, ws, need);

@@ -69,3 +69,18 @@ def test_threads_of_a_launch_stay_below_the_limit_of_an_axis():
             assert launch.grid[1] <= 65535 and launch.grid[2] <= 65535, (launch.kernel, launch.grid)
     quantizer = calls[0].launches[0]
     assert quantizer.grid[0] * quantizer.grid[1] * quantizer.block[0] * 16 >= rows * cols      # 16 values a thread
+
+
+def test_products_refuse_before_anything_is_launched():
+    """A product that the multiplication would refuse does not quantize its rows
+    first."""
+    rows, need = (1 << 31) - 1, 1 << 60
+    calls = record([("mx_grouped_mm_fwd_fp4", (P, P, P, P, rows, 256, 128, 1, fmt, P, P, need, None)) for fmt in (0, 1)]
+                   + [("mx_grouped_mm_dgrad_fp4", (P, P, P, P, rows, 128, 256, 1, fmt, P, P, need, None)) for fmt in (0, 1)]
+                   + [("mx_grouped_mm_fwd_fp4", (P, P, P, P, 1 << 20, 1 << 31, 128, 1, fmt, P, P, need, None)) for fmt in (0, 1)])
+    calls += record([(f"mx_grouped_mm_{op}_fp4", (P, P, P + 2, P, 4096, 4096, 4096, 1, fmt, P, P, need, None))
+                     for op in ("fwd", "dgrad") for fmt in (0, 1)])
+    for i, call in enumerate(calls):
+        assert call.status == (2 if i < 6 else 3), call.text
+        assert not call.launches, call.launches[0].kernel
+        assert "mx_grouped_mm" in call.text, call.text
