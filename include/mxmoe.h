@@ -399,7 +399,7 @@ mx_status mx_grouped_mm_fwd_q_noalloc(const uint16_t* A, const uint8_t* qW, cons
  * -> q [batch, rows, cols/2], s row-major [batch, rows, cols/32]
  * (scale_layout MX_SCALES_ROWMAJOR; requires cols % 32 == 0) or in the GEMM
  * layout [batch, cols/128, rows, 4] (MX_SCALES_GEMM; requires cols % 128 ==
- * 0 and cols <= 2^30).  Fewer than 2^32 blocks. */
+ * 0, cols <= 2^30 and s 4-byte aligned).  Fewer than 2^32 blocks. */
 mx_status mx_quantize_rowwise_fp4(const uint16_t* x, int64_t batch, int64_t rows, int64_t cols, uint8_t* q,
                                   uint8_t* s, int scale_layout, void* stream);
 

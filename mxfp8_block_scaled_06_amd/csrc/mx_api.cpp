@@ -573,6 +573,8 @@ mx_status mx_quantize_rowwise_fp4(const uint16_t* x, int64_t batch, int64_t rows
   const char* fn = "mx_quantize_rowwise_fp4";
   const mx_status st = check_fp4(fn, x, batch, rows, cols, q, s, scale_layout);
   if (st != MX_OK || rows == 0 || cols == 0) return st;
+  if (scale_layout == MX_SCALES_GEMM && !aligned(s, 4))
+    return fail(MX_ERR_ALIGN, "%s: scales in the GEMM layout must be 4-byte aligned", fn);
   return hip_status(mxk::launch_quant_rowwise_fp4(x, batch * rows, cols, q, s,
                                                   scale_layout == MX_SCALES_GEMM ? rows : 0, (hipStream_t)stream),
                     fn);

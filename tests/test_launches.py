@@ -84,3 +84,11 @@ def test_products_refuse_before_anything_is_launched():
         assert call.status == (2 if i < 6 else 3), call.text
         assert not call.launches, call.launches[0].kernel
         assert "mx_grouped_mm" in call.text, call.text
+
+
+def test_row_quantizer_refuses_misaligned_scale_dwords():
+    """Scales in the GEMM layout are stored as dwords, row-major ones as bytes."""
+    args = lambda s, layout: ("mx_quantize_rowwise_fp4", (P, 1, 64, 256, P, s, layout, None))  # noqa: E731
+    bad, good, rowmajor = record([args(P + 2, mx.SCALES_GEMM), args(P + 4, mx.SCALES_GEMM), args(P + 1, mx.SCALES_ROWMAJOR)])
+    assert bad.status == 3 and "4-byte" in bad.text and not bad.launches
+    assert good.status == rowmajor.status == 0 and len(good.launches) == len(rowmajor.launches) == 1
