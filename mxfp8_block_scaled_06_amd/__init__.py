@@ -729,9 +729,12 @@ _CURRENT = contextlib.nullcontext()
 
 
 def _on(device):
-    """Makes `device` the current one for a launch; no cost where it is."""
+    """Makes `device` the current one for a launch; no cost where it is (nothing
+    to do for the CPU, whose tensors the calls refuse)."""
     import torch
-    return _CURRENT if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return _CURRENT
+    return torch.cuda.device(device)
 
 
 def _same_device(first, *rest):

@@ -37,7 +37,7 @@ from __future__ import annotations
 
 import weakref
 
-from . import (_format, mx_grouped_gemm_mx, mx_grouped_gemm_mx_rows, mx_grouped_gemm_mxfp4, mx_grouped_mm_dgrad_fp4,
+from . import (_format, _on, mx_grouped_gemm_mx, mx_grouped_gemm_mx_rows, mx_grouped_gemm_mxfp4, mx_grouped_mm_dgrad_fp4,
                mx_grouped_mm_dgrad_q, mx_grouped_mm_fwd_fp4, mx_grouped_mm_fwd_q, mx_quantize_dual,
                mx_quantize_dual_gather, mx_quantize_rowwise_gather, mx_quantize_weights, mx_quantize_weights_fp4,
                mx_route, mx_topk_sum_rows)
@@ -222,10 +222,12 @@ def mx_grouped_mm(A, W, offs, check_offsets: bool = True, weights=None, cache: W
     reuses the result across micro-batches until W changes.  With
     weight_format="mxfp4" the 4-tuple is that of mx_quantize_weights_fp4, and
     without `weights` or `cache` every call quantizes W."""
-    _check(A, W, offs, check_offsets)
-    W = W.contiguous()
-    mx4 = _weights_for(W, weights, cache, weight_format)
-    return _MXGroupedMM.get().apply(A.contiguous(), W, offs, mx4, weight_format)
+    # on the tensors' device, current or not (the backward runs on it by itself)
+    with _on(A.device):
+        _check(A, W, offs, check_offsets)
+        W = W.contiguous()
+        mx4 = _weights_for(W, weights, cache, weight_format)
+        return _MXGroupedMM.get().apply(A.contiguous(), W, offs, mx4, weight_format)
 
 
 def mx_linear(x, weight, weight_format: str = "mxfp8"):
@@ -243,7 +245,8 @@ def mx_linear(x, weight, weight_format: str = "mxfp8"):
     w3 = weight.unsqueeze(0)
     if _format(weight_format, "weight_format"):
         return mx_grouped_mm(x, w3, offs, weight_format=weight_format)
-    return mx_grouped_mm(x, w3, offs, weights=_DEFAULT_CACHE.get(weight, as_experts=w3))
+    with _on(x.device):
+        return mx_grouped_mm(x, w3, offs, weights=_DEFAULT_CACHE.get(weight, as_experts=w3))
 
 
 class _MXRouted:
@@ -346,11 +349,12 @@ def mx_routed_experts(x, expert_idx, W, check: bool = True, weights=None, cache:
     E, N, K = W.shape
     if K % 128 or N % 128:
         raise ValueError(f"mx_routed_experts: N={N} and K={K} must be multiples of 128")
-    offs, rows, _pos, status = mx_route(expert_idx.contiguous().reshape(-1), E)
-    if check:
-        if int(status.item()):
-            raise ValueError(f"mx_routed_experts: an expert id lies outside [0, {E})")
-    W = W.contiguous()
-    mx4 = _weights_for(W, weights, cache, weight_format)
-    out = _MXRouted.get().apply(x.contiguous(), W, offs, rows, mx4, not check, topk, weight_format)
-    return out if expert_idx.dim() == 1 else out.view(T, topk, N)
+    with _on(x.device):
+        offs, rows, _pos, status = mx_route(expert_idx.contiguous().reshape(-1), E)
+        if check:
+            if int(status.item()):
+                raise ValueError(f"mx_routed_experts: an expert id lies outside [0, {E})")
+        W = W.contiguous()
+        mx4 = _weights_for(W, weights, cache, weight_format)
+        out = _MXRouted.get().apply(x.contiguous(), W, offs, rows, mx4, not check, topk, weight_format)
+        return out if expert_idx.dim() == 1 else out.view(T, topk, N)
