@@ -37,9 +37,9 @@ from __future__ import annotations
 
 import weakref
 
-from . import (_format, _on, mx_grouped_gemm_mx, mx_grouped_gemm_mx_rows, mx_grouped_gemm_mxfp4, mx_grouped_mm_dgrad_fp4,
-               mx_grouped_mm_dgrad_q, mx_grouped_mm_fwd_fp4, mx_grouped_mm_fwd_q, mx_quantize_dual,
-               mx_quantize_dual_gather, mx_quantize_rowwise_gather, mx_quantize_weights, mx_quantize_weights_fp4,
+from . import (_format, _on, mx_grouped_gemm_mx, mx_grouped_gemm_mx_rows, mx_grouped_gemm_mxfp4,
+               mx_grouped_mm_dgrad_fp4, mx_grouped_mm_dgrad_q, mx_grouped_mm_fwd_fp4, mx_grouped_mm_fwd_q,
+               mx_quantize_dual, mx_quantize_dual_gather, mx_quantize_rowwise_gather, mx_quantize_weights, mx_quantize_weights_fp4,
                mx_route, mx_topk_sum_rows)
 
 
@@ -110,7 +110,9 @@ def _weights_for(W, weights, cache, weight_format):
         return tuple(weights)
     if cache is None and weight_format == "mxfp4":
         return _quantize_weights(W.detach(), weight_format)
-    return (cache if cache is not None else _DEFAULT_CACHE).get(W, weight_format=weight_format)
+    cache = cache if cache is not None else _DEFAULT_CACHE
+    # a caller's own cache of MXFP8 weights need not know of formats
+    return cache.get(W) if weight_format == "mxfp8" else cache.get(W, weight_format=weight_format)
 
 
 _DEFAULT_CACHE = WeightCache()
