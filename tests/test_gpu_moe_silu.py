@@ -78,3 +78,68 @@ def test_ends_of_the_range_of_silu(gates, gate_exp, up_exp, T, fmt):
         assert (want != 0).all()
     got = _hidden(inp.f32_to_bf16_bits(x), w13, N, fmt)
     assert np.array_equal(got, want), (got[0, :8], want[0, :8])
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_gate_and_up_sums_are_fp32_ones(fmt):
+    """The codes of h of tokens with outliers, against 64 bits: fp32 sums move
+    hardly one, sums through the block-scaled instruction (the grouped product of
+    the same operands) many.
+
+    The partial sums of an fp32 sum over the contraction are sums over runs of it,
+    at most P = the greatest less the least prefix sum in magnitude.  K additions,
+    each off by at most half a step of such a sum and independent, have a root
+    mean square of 2^-24 sqrt(K/3) P at most: the codes that noise of that size
+    moves are the limit.  (With the sum S of the absolute products for P, eleven
+    times as large here, the limit would be above what block-scaled sums move.)"""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    K = N = 1024
+    T = 64
+    log(f"moe gate and up sums {fmt}")
+    x = inp.random_bf16((T, K), seed=11, outliers=True)
+    values, w13 = _quantized(inp.random_bf16((1, 2 * N, K), seed=12, std=0.05), fmt)
+    xq, xs = oracle.quantize_rowwise(x)
+    xv = oracle.dequant_rowwise(xq, xs)
+    sums = xv @ values[0].T
+    run, low, high = np.zeros((3, T, 2 * N))
+    for k in range(K):
+        run += xv[:, k:k + 1] * values[0][None, :, k]
+        np.minimum(low, run, out=low)
+        np.maximum(high, run, out=high)
+
+    def codes(gu):
+        h = moe._silu(gu[:, :N]) * gu[:, N:]
+        return moe._quantize_h(h, np.zeros_like(h))[0]
+
+    want = codes(sums)
+    noise = 2.0 ** -24 * (K / 3) ** 0.5 * (high - low) * np.random.default_rng(13).standard_normal(sums.shape)
+    limit = (codes(sums + noise) != want).sum()
+    batch = (_hidden(x, w13, N, fmt) != want).sum()
+    single = sum((_hidden(x[t:t + 1], w13, N, fmt) != want[t:t + 1]).sum() for t in range(T))
+    product = mx.mx_grouped_gemm_mxfp4 if fmt == "mxfp4" else mx.mx_grouped_gemm_mx
+    scaled = product(to_dev_u8(xq), to_dev_u8(mxfp4.to_gemm_layout(xs)), *w13, to_dev_i32(np.array([T])),
+                     **({} if fmt == "mxfp4" else {"mode": 0}), out_dtype=torch.float32)
+    instead = (codes(scaled.cpu().numpy().astype(np.float64)) != want).sum()
+    log(f"codes of {T * N} moved: {batch} in a batch, {single} one by one; limit {limit}; block-scaled sums {instead}")
+    assert batch <= limit and single <= limit
+    assert instead > 2 * limit
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_tokens_of_subnormal_values(fmt):
+    """Tokens around 2^-128, subnormal in bf16, against weights of about 2^120."""
+    require_gpu()
+    K = N = 128
+    rng = np.random.default_rng(21)
+    x = rng.integers(-64, 65, size=(5, K)).astype(np.float64) * 2.0 ** -133       # multiples of the least bf16
+    W = rng.choice([-1.0, -0.5, 0.5, 1.0], size=(1, 2 * N, K)) * 2.0 ** 120
+    bits = inp.f32_to_bf16_bits(x.astype(np.float32))
+    values, w13 = _quantized(inp.f32_to_bf16_bits(W.astype(np.float32)), fmt)
+    xv = oracle.dequant_rowwise(*oracle.quantize_rowwise(bits))
+    assert xv.any()
+    gu = xv @ values[0].T
+    h = moe._silu(gu[:, :N]) * gu[:, N:]
+    want, far = moe._quantize_h(h, 2.0 ** -20 * np.abs(h))
+    got = _hidden(bits, w13, N, fmt)
+    assert want.any() and (np.abs(got - want) <= far).all()
