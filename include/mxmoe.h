@@ -34,6 +34,15 @@
  *            +-448, subnormals kept, sign kept on values that round to zero;
  *            every element of a NaN/Inf block is 0x7F.
  *   value    decode(q) * 2^(byte - 127).
+ *
+ * Sums
+ * ----
+ * Matrix sums are accumulated in fp32 by the block-scaled matrix instruction.
+ * It aligns the products that it adds to the largest of them and drops what
+ * lies far below: with an E4M3 operand a sum was off by up to 1.6e-4 of the sum
+ * of the magnitudes of its products (tests allow 2^-11); with two E2M1 operands
+ * every sum tried was exact.  "fp32" below means these sums, unrounded, unless it says more.
+ *
  * bf16 is passed as uint16_t bit patterns, E4M3 and E8M0 as uint8_t.  All
  * tensors are dense and row-major unless a leading dimension says otherwise.
  *
@@ -462,9 +471,10 @@ mx_status mx_grouped_mm_dgrad_fp4(const uint16_t* dOut, const uint8_t* qWt, cons
  *   h      = MX8(silu(g) * u)
  *   out[t] = bf16(sum_j combine[t, j] * (h W2[e]^T)),   e = expert_idx[t, j]
  * MX8 is the MXFP8 quantization in 1x32 blocks along the contraction
- * (mx_quantize_rowwise), of h taken from its fp32 values; sums are fp32, the
- * sum over a token's slots is rounded once, and the order of additions is
- * fixed.  x bf16 [T, K], expert_idx int32 and combine float [T, topk], W13
+ * (mx_quantize_rowwise), of h taken from its fp32 values.  The gate and up sums
+ * are plain fp32 sums of the exact products, those over h go through the
+ * block-scaled instruction (see Sums above); the sum over a token's slots is
+ * fp32 and rounded once, and the order of additions is fixed.  x bf16 [T, K], expert_idx int32 and combine float [T, topk], W13
  * [E, 2N, K] as (q13, s13) and W2 [E, K, N] as (q2, s2): codes in w_format
  * (MX_FMT_FP8: mx_quantize_weights, or MX_FMT_FP4: mx_quantize_weights_fp4),
  * scales in the GEMM layout; out bf16 [T, K].

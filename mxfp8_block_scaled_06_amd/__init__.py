@@ -932,7 +932,10 @@ def mx_moe_few_tokens(x, expert_idx, combine, w13, w2, weight_format: str = "mxf
     first) and w2 = (q, s) of the down weights [E, K, N], the first two results
     of mx_quantize_weights_fp4 (weight_format "mxfp4") or mx_quantize_weights
     ("mxfp8").  K and N multiples of 128.  x and silu(g) * u are quantized to
-    MXFP8 in the kernels; sums are fp32, rounded once.  Returns bf16 [T, K].
+    MXFP8 in the kernels.  The gate and up sums are fp32, those of the down
+    projection as in the grouped products (fp32 with the low bits of small
+    products dropped, up to 1.6e-4 of the magnitudes' sum); the weighted sum is
+    fp32 and rounded once.  Returns bf16 [T, K].
 
     check=True reads the routing status (one synchronization) and raises on an
     expert id outside [0, E); with check=False such slots add nothing.  `ws`:

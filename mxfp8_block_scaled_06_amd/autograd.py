@@ -39,8 +39,8 @@ import weakref
 
 from . import (_format, _on, mx_grouped_gemm_mx, mx_grouped_gemm_mx_rows, mx_grouped_gemm_mxfp4,
                mx_grouped_mm_dgrad_fp4, mx_grouped_mm_dgrad_q, mx_grouped_mm_fwd_fp4, mx_grouped_mm_fwd_q,
-               mx_quantize_dual, mx_quantize_dual_gather, mx_quantize_rowwise_gather, mx_quantize_weights, mx_quantize_weights_fp4,
-               mx_route, mx_topk_sum_rows)
+               mx_quantize_dual, mx_quantize_dual_gather, mx_quantize_rowwise_gather, mx_quantize_weights,
+               mx_quantize_weights_fp4, mx_route, mx_topk_sum_rows)
 
 
 class WeightCache:

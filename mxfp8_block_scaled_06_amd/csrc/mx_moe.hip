@@ -18,7 +18,8 @@
 //   moe_down_kernel     32 or 16 output columns per workgroup, all hit experts, all
 //                       tokens; the sum over a token's experts stays in fp32
 //                       on the CU, so nothing is added through memory and the
-//                       order of additions is fixed.
+//                       order of additions is fixed.  K / 32 workgroups leave
+//                       CUs idle below K = 8192: 2.6 TB/s at K = 5120, one token.
 // Partial sums of several waves are added in wave order.  A wave keeps the next
 // lines of its weights in flight while it multiplies one.
 //
@@ -234,7 +235,7 @@ __device__ __forceinline__ int piece(int token, int p) { return 16 * (p ^ (token
 // at the end of the run.  (With every block split over the eight waves, 28 lines
 // of E2M1 made shares of 3 and 4, and all waves waited at every block: 128
 // tokens, top 8 of 32 experts, K 7168, N 2048: 393 us the layer, 351 with whole
-// blocks.)
+// blocks, in the same state of the rest.)
 //
 // Loads from memory are waited for in the order of their issue, so the wave's
 // stream of weights, D lines of each row ahead and across the blocks, has no
@@ -245,12 +246,14 @@ __device__ __forceinline__ int piece(int token, int p) { return 16 * (p ^ (token
 // instruction drops the low bits of small products beside large ones (1.5e-4 of
 // the sum of magnitudes on tokens with outliers), which moved values of h to a
 // neighbouring code, and with one or seven tokens the output's error from 0.0017
-// to 0.0042 and 0.0027.  It costs 21.9 -> 23.1 us (1 token) and 127 -> 130 (7).
+// to 0.0042 and 0.0027.  It cost 21.9 -> 23.1 us (1 token) and 127 -> 130 (7) when
+// it came in.  The down projection keeps the block-scaled instruction: with it the
+// output's error is that of its rounding to bf16 (those 0.0017).
 // ---------------------------------------------------------------------------
 constexpr int kMoeGrid = 256;      // workgroups of the gate kernel, one per CU
 static_assert(kMoeGrid == 1 << 8, "shares are taken by shifts");
 // Row tiles (gate and up) whose sums meet in LDS at a time: with two column tiles
-// one, as LDS is x's (20 tokens of K = 7168 and not 18: 128 tokens, top 4, 8-bit:
+// one, as LDS is x's (20 tokens of K = 7168 and not 18: 128 tokens, top 4, 8-bit,
 // 323 us against 336), else two, with half the barriers.
 template <int CT>
 constexpr int kParts = CT == 1 ? 2 : 1;
@@ -805,11 +808,18 @@ static size_t down_lds(const MoeArgs& a, int rt) {
 }
 
 // Row tiles of the down kernel: two (h is read half as often) where the waves'
-// sums of all tokens leave LDS for the lists, else one: 128 tokens, top 4 of 32
-// experts, 8-bit: 405 us with two, 453 with one; 7 tokens, top 8, 4-bit: 135, 151.
-// Column tiles: two where an expert has more than 8 tokens on average, so that
-// few experts' weights are read twice: 128 tokens, top 4, 8-bit: 340 us with
-// two, 413 with one; 32 tokens, top 8, 4-bit (8 on average): 168, 162.
+// sums of all tokens leave LDS for the lists, else one.  Column tiles: two where
+// an expert has more than 8 tokens on average, so that few experts' weights are
+// read twice.  Both kernels, us in a trace (16 experts, K 5120, N 8192 for one
+// token, else 32 experts, K 7168, N 2048):
+//                           as chosen   one row tile   the other column tiles
+//   1 token, top 1, 4-bit      23.5         25.8           -
+//   1 token, top 1, 8-bit      33.8         35.5           -
+//   7 tokens, top 8, 4-bit      147          162          156 (two)
+//   32, top 8, 4-bit (8 avg)    153          175          162 (two)
+//   128, top 4, 4-bit           212          256          227 (one)
+//   128, top 8, 4-bit           313          393          344 (one)
+//   128, top 4, 8-bit           314          359          387 (one)
 hipError_t launch_moe_few_tokens(const MoeArgs& a, hipStream_t st) {
   const size_t two = down_lds(a, 2), one = down_lds(a, 1);
   const bool wide = (int64_t)a.T * a.topk > 8 * (int64_t)a.E;
