@@ -497,6 +497,134 @@ mx_status mx_moe_few_tokens(const uint16_t* x, const int32_t* expert_idx, const 
                             int64_t topk, int64_t K, int64_t N, int64_t E, uint16_t* out, int32_t* status, void* ws,
                             size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Around the experts' products: the router, the activation between the products
+ * with its checkpoint in 8 bits, the weighted sum over a token's experts.
+ * ------------------------------------------------------------------------ */
+
+/* Types of the tensors that come in two. */
+#define MX_BF16 0
+#define MX_F32 1
+
+#define MX_SCORE_SOFTMAX 0
+#define MX_SCORE_SIGMOID 1
+#define MX_GROUP_MAX 0
+#define MX_GROUP_TOP2 1
+#define MX_ROUTER_MAX_GROUPS 64
+
+/* The experts of each token and their weights, from the router's logits [T, E]
+ * (logits_type MX_BF16 or MX_F32):
+ *   s       softmax of the token's logits, or their sigmoid
+ *   c       s + bias[e] (bias float [E], or NULL); c takes part in the choice alone
+ *   groups  E/groups consecutive experts each; a group's value is its largest c
+ *           (MX_GROUP_MAX) or the sum of its two largest (MX_GROUP_TOP2); the
+ *           experts of the topk_groups best groups stay
+ *   expert_idx [T, k]  the experts of the k largest c, largest first
+ *   combine [T, k]     scale * s[expert_idx], with renormalize != 0 over their sum
+ * Equal values go to the lowest index.  The choice is that of c in 64 bits;
+ * without a bias and without sums of two it is by the logits themselves, which
+ * order the experts as their scores do.  combine is computed in fp32.
+ * A masked expert (logit minus infinity, or the lowest finite value of its type)
+ * has the score 0, adds nothing to its group's value and comes behind every other
+ * expert of the chosen groups, a group with none but such behind every other group; so does an
+ * expert whose c is NaN.  A token whose experts are all masked gets weights 0.
+ * The ids of a token are distinct and lie in [0, E) whatever the logits hold.
+ * Requires 0 <= T < 2^31, 1 <= E <= 1024, 1 <= k <= MX_MOE_MAX_TOPK, 1 <= groups <=
+ * MX_ROUTER_MAX_GROUPS, groups dividing E, topk_groups * (E/groups) >= k, scale
+ * positive and finite.  logits 16-byte, the rest 4-byte aligned. */
+mx_status mx_topk_router_fwd(const void* logits, int logits_type, const float* bias, int64_t T, int64_t E, int64_t k,
+                             int score, int64_t groups, int64_t topk_groups, int group_score, int renormalize,
+                             float scale, int32_t* expert_idx, float* combine, void* stream);
+
+/* Gradient of the logits, dlogits [T, E] in their type, from that of the
+ * weights, dcombine float [T, k]; expert_idx and combine as the forward wrote them
+ * for these logits, score, renormalize and scale.  With p = combine / scale, g =
+ * dcombine and s the scores:
+ *   softmax             dl[e] = s[e] (scale g[e] - sum_j scale g[j] p[j])
+ *   ... renormalized    dl[e] = combine[e] (g[e] - sum_j g[j] p[j])
+ *   sigmoid             dl[e] = combine[e] (1 - s[e]) g[e]
+ *   ... renormalized    dl[e] = combine[e] (1 - s[e]) (g[e] - sum_j g[j] p[j])
+ * (e not chosen: g[e] and combine[e] 0).  The choice passes no gradient, nor
+ * does the bias get one.  Masked experts get 0.  An id outside [0, E) adds
+ * nothing. */
+mx_status mx_topk_router_bwd(const void* logits, int logits_type, const int32_t* expert_idx, const float* combine,
+                             const float* dcombine, int64_t T, int64_t E, int64_t k, int score, int renormalize,
+                             float scale, void* dlogits, void* stream);
+
+/* Values of MXFP8 codes: out bf16 [batch, rows, cols] of q [batch, rows, cols] and
+ * s in either layout, sizes as mx_dequantize_fp4.  code * 2^(byte - 127), rounded
+ * to nearest even where it lies below 2^-126, and infinite past the bf16 range;
+ * byte 255 gives NaN. */
+mx_status mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t batch, int64_t rows, int64_t cols, int scale_layout,
+                        uint16_t* out, void* stream);
+
+/* The gated activation h = silu(g) * u (bf16 [M, N]) of gu [M, 2N] bf16, gate
+ * columns 0..N-1, up columns N..2N-1; computed in fp32, rounded once.  With kept
+ * and kept_s it leaves a checkpoint of gu in 8 bits for the backward: kept [M, 2N]
+ * and kept_s [M, 2N/32], what mx_quantize_rowwise writes of gu (both NULL: none).
+ * Requires N % 32 == 0, fewer than 2^32 blocks of 32 columns of h; gu, h, kept 16-byte aligned. */
+mx_status mx_swiglu_fwd(const uint16_t* gu, int64_t M, int64_t N, uint16_t* h, uint8_t* kept, uint8_t* kept_s,
+                        void* stream);
+
+/* Its gradient at the values that the checkpoint stands for: with s = sigmoid(g),
+ *   dgu = [dh * u * s * (1 + g (1 - s)) | dh * g * s]
+ * dh [M, N] and dgu [M, 2N] bf16, computed in fp32, rounded once. */
+mx_status mx_swiglu_bwd(const uint16_t* dh, const uint8_t* kept, const uint8_t* kept_s, int64_t M, int64_t N,
+                        uint16_t* dgu, void* stream);
+
+/* The same between the two MXFP8 products of routed experts, on rows grouped by
+ * expert, with the quantization of the operands of the next products.  rows int32
+ * [M]: the item of each row (the `rows` of mx_route); a row whose entry lies
+ * outside [0, n_items) has none: it counts as zeros, whatever it holds.  rows
+ * NULL: row r is item r, n_items = M.  h is quantized from its fp32 values.
+ *
+ * mx_swiglu_quantize: q [M, N] and s [N/128, M, 4] alone (inference): h in 1x32
+ * blocks along N, an operand X of the rows-grouped GEMM.  Any M.
+ *
+ * mx_swiglu_quantize_fwd: also q_t [N, ldq] and s_t [ldq/128, N, 4], h times
+ * combine[rows[r]] (float [n_items], NULL: 1) in 32x1 blocks along the rows, an
+ * operand of the weight gradient's GEMM (columns M..ldq-1: zero codes); and the
+ * checkpoint of gu as mx_swiglu_fwd leaves it (rows without an item: of zeros).
+ * Requires M % 32 == 0, ldq % 128 == 0, ldq >= M.
+ *
+ * mx_swiglu_quantize_bwd: dh [M, N] bf16 is the gradient of h without the combine
+ * weight.  With dgu as in mx_swiglu_bwd of combine * dh: q [M, 2N] and s [2N/128,
+ * M, 4], q_t [2N, ldq] and s_t [ldq/128, 2N, 4], dgu in both orientations.
+ * dcombine (float [n_items], or NULL) is each item's sum_n dh[n] h[n], h from the
+ * checkpoint, in fp32 with a fixed order of additions; it needs pos (int32
+ * [n_items], the `pos` of mx_route, the inverse of rows; NULL without rows) and a workspace: items
+ * whose entry of pos is negative get 0.  ws: mx_swiglu_quantize_workspace_bytes(M, N),
+ * 256-byte aligned, needs no initialisation.
+ *
+ * All require N % 128 == 0, n_items < 2^31, fewer than 65535 * 256 rows; gu,
+ * dh, kept and codes 16-byte, the rest but kept_s 4-byte aligned. */
+mx_status mx_swiglu_quantize(const uint16_t* gu, const int32_t* rows, int64_t n_items, int64_t M, int64_t N, uint8_t* q,
+                             uint8_t* s, void* stream);
+mx_status mx_swiglu_quantize_fwd(const uint16_t* gu, const int32_t* rows, const float* combine, int64_t n_items,
+                                 int64_t M, int64_t N, int64_t ldq, uint8_t* q, uint8_t* s, uint8_t* q_t, uint8_t* s_t,
+                                 uint8_t* kept, uint8_t* kept_s, void* stream);
+size_t mx_swiglu_quantize_workspace_bytes(int64_t M, int64_t N);
+mx_status mx_swiglu_quantize_bwd(const uint16_t* dh, const uint8_t* kept, const uint8_t* kept_s, const int32_t* rows,
+                                 const int32_t* pos, const float* combine, int64_t n_items, int64_t M, int64_t N,
+                                 int64_t ldq, uint8_t* q, uint8_t* s, uint8_t* q_t, uint8_t* s_t, float* dcombine,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* The weighted sum over a token's experts: out[t] = bf16(sum_j combine[t, j] *
+ * y[t, j]) over the k items of token t, y [T, k, N] (y_type MX_BF16 or MX_F32),
+ * combine float [T, k]; in fp32 in slot order, rounded once.  pos int32 [T, k] (of
+ * mx_route) or NULL: an item whose entry is negative was not routed; its row of y is not
+ * read and adds nothing.  Requires 1 <= k <= 1024, N % 8 == 0, T and N below 2^31; y and out
+ * 16-byte, the rest 4-byte aligned. */
+mx_status mx_topk_combine_fwd(const void* y, int y_type, const float* combine, const int32_t* pos, int64_t T, int64_t k,
+                              int64_t N, uint16_t* out, void* stream);
+
+/* Its gradients from dout bf16 [T, N]: dy[t, j] = combine[t, j] * dout[t] in y's
+ * type, and dcombine[t, j] = sum_n dout[t, n] * y[t, j, n] in fp32 with a fixed
+ * order of additions; 0 for items that were not routed.  Either may be NULL (y
+ * too without dcombine). */
+mx_status mx_topk_combine_bwd(const void* y, int y_type, const float* combine, const int32_t* pos, const uint16_t* dout,
+                              int64_t T, int64_t k, int64_t N, void* dy, float* dcombine, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

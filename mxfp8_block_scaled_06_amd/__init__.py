@@ -29,12 +29,19 @@ __all__ = [
     "mx_quantize_rowwise_fp4", "mx_dequantize_fp4", "mx_quantize_weights_fp4",
     "mx_grouped_gemm_mxfp4", "mx_grouped_mm_fwd_fp4", "mx_grouped_mm_dgrad_fp4", "mx_grouped_mm_fp4_workspace_bytes",
     "mx_moe_few_tokens", "mx_moe_few_tokens_workspace_bytes", "MOE_MAX_TOKENS", "MOE_MAX_TOPK",
+    "mx_dequantize", "mx_topk_router", "mx_topk_router_fwd", "mx_topk_router_bwd", "ROUTER_MAX_GROUPS",
+    "mx_swiglu", "mx_swiglu_fwd", "mx_swiglu_bwd", "mx_swiglu_quantize", "mx_swiglu_quantize_fwd",
+    "mx_swiglu_quantize_bwd", "mx_swiglu_quantize_workspace_bytes",
+    "mx_topk_combine", "mx_topk_combine_fwd", "mx_topk_combine_bwd", "mx_moe_layer",
 ]
 
 OP_FWD, OP_DGRAD, OP_WGRAD, OP_FWD_Q, OP_DGRAD_Q = 0, 1, 2, 3, 4
 SCALES_ROWMAJOR, SCALES_GEMM = 0, 1
 MOE_MAX_TOKENS, MOE_MAX_TOPK = 128, 32     # MX_MOE_MAX_TOKENS, MX_MOE_MAX_TOPK
 FORMATS = {"mxfp8": 0, "mxfp4": 1}    # MX_FMT_FP8, MX_FMT_FP4
+SCORES = {"softmax": 0, "sigmoid": 1}     # MX_SCORE_SOFTMAX, MX_SCORE_SIGMOID
+GROUP_SCORES = {"max": 0, "top2": 1}      # MX_GROUP_MAX, MX_GROUP_TOP2
+ROUTER_MAX_GROUPS = 64                    # MX_ROUTER_MAX_GROUPS
 OFFS_DECREASING, OFFS_RANGE, OFFS_LAST, OFFS_ALIGN = 1, 2, 4, 8
 NOALLOC_SCRATCH_BYTES = 128 << 20     # MX_NOALLOC_SCRATCH_BYTES of include/mxmoe.h
 _STATUS = {0: "MX_OK", 1: "MX_ERR_NULL", 2: "MX_ERR_SHAPE", 3: "MX_ERR_ALIGN", 4: "MX_ERR_WORKSPACE",
@@ -135,6 +142,32 @@ def load_library():
     lib.mx_moe_few_tokens.restype = c_int
     lib.mx_moe_few_tokens.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_i64,
                                       c_i64, c_vp, c_vp, c_vp, c_sz, c_vp]
+    c_f = ctypes.c_float
+    lib.mx_dequantize.restype = c_int
+    lib.mx_dequantize.argtypes = lib.mx_dequantize_fp4.argtypes
+    lib.mx_topk_router_fwd.restype = c_int
+    lib.mx_topk_router_fwd.argtypes = [c_vp, c_int, c_vp, c_i64, c_i64, c_i64, c_int, c_i64, c_i64, c_int, c_int, c_f,
+                                       c_vp, c_vp, c_vp]
+    lib.mx_topk_router_bwd.restype = c_int
+    lib.mx_topk_router_bwd.argtypes = [c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_f, c_vp, c_vp]
+    lib.mx_swiglu_fwd.restype = c_int
+    lib.mx_swiglu_fwd.argtypes = [c_vp, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp]
+    lib.mx_swiglu_bwd.restype = c_int
+    lib.mx_swiglu_bwd.argtypes = [c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_vp]
+    lib.mx_swiglu_quantize.restype = c_int
+    lib.mx_swiglu_quantize.argtypes = [c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]
+    lib.mx_swiglu_quantize_fwd.restype = c_int
+    lib.mx_swiglu_quantize_fwd.argtypes = [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                           c_vp, c_vp]
+    lib.mx_swiglu_quantize_workspace_bytes.restype = c_sz
+    lib.mx_swiglu_quantize_workspace_bytes.argtypes = [c_i64, c_i64]
+    lib.mx_swiglu_quantize_bwd.restype = c_int
+    lib.mx_swiglu_quantize_bwd.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp,
+                                           c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]
+    lib.mx_topk_combine_fwd.restype = c_int
+    lib.mx_topk_combine_fwd.argtypes = [c_vp, c_int, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp]
+    lib.mx_topk_combine_bwd.restype = c_int
+    lib.mx_topk_combine_bwd.argtypes = [c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]
     _lib = lib
     return lib
 
@@ -985,3 +1018,368 @@ def mx_moe_few_tokens(x, expert_idx, combine, w13, w2, weight_format: str = "mxf
     if check and int(status.item()):
         raise ValueError(f"mx_moe_few_tokens: an expert id lies outside [0, {E})")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Around the experts' products: router, activation, weighted sum
+# ---------------------------------------------------------------------------
+def mx_dequantize(q, s, scale_layout: str = "rowmajor", out=None):
+    """The values of MXFP8 codes, bf16 [B?, R, C], from q uint8 [B?, R, C] and s
+    in either layout (as mx_dequantize_fp4).  Exact from 2^-126 on; a NaN/Inf
+    block's scale byte 255 gives NaN."""
+    import torch
+    lib = load_library()
+    _require(q, torch.uint8, "q")
+    _require(s, torch.uint8, "s")
+    B, R, C = _as3d(q)
+    lead, dev = (B,) if q.dim() == 3 else (), q.device
+    s_shape, layout = _scale_shape(scale_layout, lead, R, C)
+    if tuple(s.shape) != s_shape:
+        raise ValueError(f"s must have shape {s_shape} for codes {tuple(q.shape)}, got {tuple(s.shape)}")
+    _same_device(q, s)
+    out = _out(out, tuple(q.shape), torch.bfloat16, dev, "out")
+    with _on(dev):
+        _check("mx_dequantize", lib.mx_dequantize(_ptr(q), _ptr(s), B, R, C, layout, _ptr(out), _stream(dev)))
+    return out
+
+
+def _type(t, name):
+    """MX_BF16 or MX_F32 of a tensor that may be either (contiguous, on the GPU)."""
+    import torch
+    if isinstance(t, torch.Tensor) and t.dtype == torch.float32:
+        _require(t, torch.float32, name)
+        return 1
+    _require(t, torch.bfloat16, name)
+    return 0
+
+
+def _choice(value, of, name):
+    if value not in of:
+        raise ValueError(f"{name} must be one of {', '.join(map(repr, of))}, got {value!r}")
+    return of[value]
+
+
+def mx_topk_router_fwd(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+                       group_score: str = "max", renormalize: bool = True, scale: float = 1.0, expert_idx=None,
+                       combine=None):
+    """(expert_idx int32 [T, k], combine fp32 [T, k]) of the logits (see mx_topk_router), without a gradient."""
+    import torch
+    lib = load_library()
+    kind = _type(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    if bias is not None:
+        _require(bias, torch.float32, "bias")
+        if tuple(bias.shape) != (E,):
+            raise ValueError(f"bias must be [{E}] (one per expert), got {tuple(bias.shape)}")
+        _same_device(logits, bias)
+    sc, gs = _choice(score, SCORES, "score"), _choice(group_score, GROUP_SCORES, "group_score")
+    dev = logits.device
+    expert_idx = _out(expert_idx, (T, max(k, 0)), torch.int32, dev, "expert_idx")
+    combine = _out(combine, (T, max(k, 0)), torch.float32, dev, "combine")
+    with _on(dev):
+        _check("mx_topk_router_fwd",
+               lib.mx_topk_router_fwd(_ptr(logits), kind, _ptr(bias), T, E, k, sc, groups, topk_groups, gs,
+                                      int(bool(renormalize)), scale, _ptr(expert_idx), _ptr(combine), _stream(dev)))
+    return expert_idx, combine
+
+
+def mx_topk_router_bwd(logits, expert_idx, combine, dcombine, score: str = "softmax", renormalize: bool = True,
+                       scale: float = 1.0, dlogits=None):
+    """Gradient of the logits from that of the combine weights (dcombine fp32 [T, k]); expert_idx and combine
+    as mx_topk_router_fwd returned them with the same arguments."""
+    import torch
+    lib = load_library()
+    kind = _type(logits, "logits")
+    _require(expert_idx, torch.int32, "expert_idx")
+    _require(combine, torch.float32, "combine")
+    _require(dcombine, torch.float32, "dcombine")
+    if logits.dim() != 2 or expert_idx.dim() != 2 or expert_idx.shape[0] != logits.shape[0]:
+        raise ValueError("logits must be [T, E] and expert_idx [T, k]")
+    if expert_idx.shape != combine.shape or expert_idx.shape != dcombine.shape:
+        raise ValueError(f"expert_idx, combine and dcombine must have one shape, got {tuple(expert_idx.shape)}, "
+                         f"{tuple(combine.shape)} and {tuple(dcombine.shape)}")
+    _same_device(logits, expert_idx, combine, dcombine)
+    T, E = logits.shape
+    dev = logits.device
+    dlogits = _out(dlogits, (T, E), logits.dtype, dev, "dlogits")
+    with _on(dev):
+        _check("mx_topk_router_bwd",
+               lib.mx_topk_router_bwd(_ptr(logits), kind, _ptr(expert_idx), _ptr(combine), _ptr(dcombine), T, E,
+                                      expert_idx.shape[1], _choice(score, SCORES, "score"), int(bool(renormalize)),
+                                      scale, _ptr(dlogits), _stream(dev)))
+    return dlogits
+
+
+def mx_topk_router(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+                   group_score: str = "max", renormalize: bool = True, scale: float = 1.0):
+    """The router: logits fp32 or bf16 [T, E] -> (expert_idx int32 [T, k], combine fp32 [T, k]), what mx_route,
+    mx_moe_layer and mx_moe_few_tokens take.  Differentiable in the logits.
+
+        s = softmax(logits) or sigmoid(logits)     score="softmax" / "sigmoid"
+        c = s + bias                               bias fp32 [E], for balance: takes part in the choice alone
+        expert_idx = the k largest c, largest first, equal ones by index
+        combine = scale * s[expert_idx]            divided by their sum with renormalize=True
+
+    groups > 1: the choice is among the experts of the topk_groups best of that many groups of consecutive
+    experts; a group counts with its largest c (group_score="max") or the sum of its two largest ("top2").
+    The choice is that of 64-bit scores, the weights are fp32.  Experts whose logit is -inf (or the lowest
+    finite value of the type) are masked: score 0, chosen after all others; a token with no other expert gets
+    weights 0.  E up to 1024, k up to MOE_MAX_TOPK, groups up to ROUTER_MAX_GROUPS."""
+    from .autograd import mx_topk_router as _f
+    return _f(logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale)
+
+
+def _halves(gu):
+    if gu.dim() != 2 or gu.shape[1] % 2:
+        raise ValueError(f"gu must be [M, 2N] (gate columns, then up columns), got {tuple(gu.shape)}")
+    return gu.shape[0], gu.shape[1] // 2
+
+
+def _kept(kept, kept_s, M, N):
+    import torch
+    _require(kept, torch.uint8, "kept")
+    _require(kept_s, torch.uint8, "kept_s")
+    if tuple(kept.shape) != (M, 2 * N) or tuple(kept_s.shape) != (M, 2 * N // 32):
+        raise ValueError(f"the checkpoint must be codes {(M, 2 * N)} and scales {(M, 2 * N // 32)}, got "
+                         f"{tuple(kept.shape)} and {tuple(kept_s.shape)}")
+
+
+def mx_swiglu_fwd(gu, keep: bool = True, h=None, kept=None, kept_s=None):
+    """(h bf16 [M, N], kept uint8 [M, 2N], kept_s uint8 [M, 2N/32]) of gu bf16 [M, 2N]: silu(gate) * up and
+    the MXFP8 checkpoint of gu that mx_swiglu_bwd reads (None, None with keep=False).  N % 32 == 0."""
+    import torch
+    lib = load_library()
+    _require(gu, torch.bfloat16, "gu")
+    M, N = _halves(gu)
+    dev = gu.device
+    h = _out(h, (M, N), torch.bfloat16, dev, "h")
+    if keep:
+        kept = _out(kept, (M, 2 * N), torch.uint8, dev, "kept")
+        kept_s = _out(kept_s, (M, 2 * N // 32), torch.uint8, dev, "kept_s")
+    elif kept is not None or kept_s is not None:
+        raise ValueError("kept and kept_s go with keep=True")
+    with _on(dev):
+        _check("mx_swiglu_fwd", lib.mx_swiglu_fwd(_ptr(gu), M, N, _ptr(h), _ptr(kept), _ptr(kept_s), _stream(dev)))
+    return h, kept, kept_s
+
+
+def mx_swiglu_bwd(dh, kept, kept_s, dgu=None):
+    """Gradient of gu, bf16 [M, 2N], from that of h (bf16 [M, N]) at the values of the checkpoint."""
+    import torch
+    lib = load_library()
+    _require(dh, torch.bfloat16, "dh")
+    if dh.dim() != 2:
+        raise ValueError("dh must be [M, N]")
+    M, N = dh.shape
+    _kept(kept, kept_s, M, N)
+    _same_device(dh, kept, kept_s)
+    dev = dh.device
+    dgu = _out(dgu, (M, 2 * N), torch.bfloat16, dev, "dgu")
+    with _on(dev):
+        _check("mx_swiglu_bwd", lib.mx_swiglu_bwd(_ptr(dh), _ptr(kept), _ptr(kept_s), M, N, _ptr(dgu), _stream(dev)))
+    return dgu
+
+
+def mx_swiglu(gu):
+    """Differentiable h = silu(gate) * up of gu bf16 [M, 2N] (gate columns first): bf16 [M, N].  N % 32 == 0.
+
+    The backward keeps gu in MXFP8 (2.06 bytes per element of h instead of 4) and is the gradient at the
+    values kept: each gate and up value off by at most 1/16 of itself (or, in a block of 32 with a larger
+    one, 2^-18 of the largest's power of two; up to 1/8 for values from 7/8 of the next power of two on)."""
+    from .autograd import mx_swiglu as _f
+    return _f(gu)
+
+
+def _rows_of(gu, rows, combine, M):
+    """Checks of the items that rows stand for; their number."""
+    import torch
+    if combine is not None:
+        _require(combine, torch.float32, "combine")
+        _same_device(gu, combine)
+    if rows is None:
+        if combine is not None and combine.numel() != M:
+            raise ValueError(f"without rows combine must hold M={M} weights, got {combine.numel()}")
+        return M
+    _require(rows, torch.int32, "rows")
+    if tuple(rows.shape) != (M,):
+        raise ValueError(f"rows must be int32 [{M}] (the item of each row), got {tuple(rows.shape)}")
+    _same_device(gu, rows)
+    return combine.numel() if combine is not None else (1 << 31) - 1
+
+
+def mx_swiglu_quantize(gu, rows=None, q=None, s=None):
+    """MXFP8 of silu(gate) * up of gu bf16 [M, 2N], (q uint8 [M, N], s uint8 [N/128, M, 4]): X of the next
+    grouped product.  rows int32 [M] (of mx_route): rows with a negative entry count as zeros, whatever they
+    hold.  N % 128 == 0."""
+    import torch
+    lib = load_library()
+    _require(gu, torch.bfloat16, "gu")
+    M, N = _halves(gu)
+    n = _rows_of(gu, rows, None, M)
+    dev = gu.device
+    q = _out(q, (M, N), torch.uint8, dev, "q")
+    s = _out(s, (N // 128, M, 4), torch.uint8, dev, "s")
+    with _on(dev):
+        _check("mx_swiglu_quantize",
+               lib.mx_swiglu_quantize(_ptr(gu), _ptr(rows), n, M, N, _ptr(q), _ptr(s), _stream(dev)))
+    return q, s
+
+
+def mx_swiglu_quantize_fwd(gu, rows=None, combine=None, ldq: Optional[int] = None, q=None, s=None, q_t=None, s_t=None,
+                           kept=None, kept_s=None):
+    """The activation between the two products of routed experts, for training: (q, s, q_t, s_t, kept,
+    kept_s) of gu bf16 [M, 2N] with the rows of mx_route (None: row r is item r).
+
+      q [M, N], s [N/128, M, 4]         h = silu(gate) * up in 1x32 blocks along N, X of the down product
+      q_t [N, ldq], s_t [ldq/128, N, 4] combine[rows[r]] * h in 32x1 blocks along the rows, for the down
+                                        weights' gradient (combine fp32, one weight per item; None: 1)
+      kept [M, 2N], kept_s [M, 2N/32]   the checkpoint of gu in MXFP8, for mx_swiglu_quantize_bwd
+
+    Rows whose entry of `rows` is negative or past the items count as zeros.  M % 32 == 0, N % 128 == 0; ldq
+    defaults to M rounded up to 128."""
+    import torch
+    lib = load_library()
+    _require(gu, torch.bfloat16, "gu")
+    M, N = _halves(gu)
+    n = _rows_of(gu, rows, combine, M)
+    if ldq is None:
+        ldq = (M + 127) // 128 * 128
+    dev = gu.device
+    q = _out(q, (M, N), torch.uint8, dev, "q")
+    s = _out(s, (N // 128, M, 4), torch.uint8, dev, "s")
+    q_t = _out(q_t, (N, ldq), torch.uint8, dev, "q_t")
+    s_t = _out(s_t, (ldq // 128, N, 4), torch.uint8, dev, "s_t")
+    kept = _out(kept, (M, 2 * N), torch.uint8, dev, "kept")
+    kept_s = _out(kept_s, (M, 2 * N // 32), torch.uint8, dev, "kept_s")
+    with _on(dev):
+        _check("mx_swiglu_quantize_fwd",
+               lib.mx_swiglu_quantize_fwd(_ptr(gu), _ptr(rows), _ptr(combine), n, M, N, ldq, _ptr(q), _ptr(s), _ptr(q_t),
+                                          _ptr(s_t), _ptr(kept), _ptr(kept_s), _stream(dev)))
+    return q, s, q_t, s_t, kept, kept_s
+
+
+def mx_swiglu_quantize_workspace_bytes(M: int, N: int) -> int:
+    return int(load_library().mx_swiglu_quantize_workspace_bytes(int(M), int(N)))
+
+
+def mx_swiglu_quantize_bwd(dh, kept, kept_s, rows=None, pos=None, combine=None, ldq: Optional[int] = None, q=None, s=None,
+                           q_t=None, s_t=None, dcombine=None, ws=None):
+    """Its backward: (q [M, 2N], s [2N/128, M, 4], q_t [2N, ldq], s_t [ldq/128, 2N, 4], dcombine) from dh bf16
+    [M, N], the gradient of h without the combine weight.  q and q_t are the gradient of gu (combine * dh
+    through the activation at the checkpoint's values) in both orientations, dcombine fp32 (the shape of
+    combine; None without it) each item's sum over N of dh * h.  rows and pos as mx_route returned them; items
+    whose pos is negative get dcombine 0.  `ws`: uint8 scratch of mx_swiglu_quantize_workspace_bytes(M, N)."""
+    import torch
+    lib = load_library()
+    _require(dh, torch.bfloat16, "dh")
+    if dh.dim() != 2:
+        raise ValueError("dh must be [M, N]")
+    M, N = dh.shape
+    _kept(kept, kept_s, M, N)
+    n = _rows_of(dh, rows, combine, M)
+    _same_device(dh, kept, kept_s)
+    dev = dh.device
+    if combine is None:
+        if dcombine is not None:
+            raise ValueError("dcombine goes with combine")
+        pos = None
+    else:
+        dcombine = _out(dcombine, tuple(combine.shape), torch.float32, dev, "dcombine")
+        if (rows is None) != (pos is None):
+            raise ValueError("rows and pos go together (both of mx_route)")
+        if pos is not None:
+            _require(pos, torch.int32, "pos")
+            _same_device(dh, pos)
+            if pos.numel() != n:
+                raise ValueError(f"pos must hold one entry per item ({n}), got {pos.numel()}")
+        if ws is None:
+            ws = torch.empty(max(mx_swiglu_quantize_workspace_bytes(M, N), 1), dtype=torch.uint8, device=dev)
+        else:
+            _require(ws, torch.uint8, "ws")
+            _same_device(dh, ws)
+    if ldq is None:
+        ldq = (M + 127) // 128 * 128
+    q = _out(q, (M, 2 * N), torch.uint8, dev, "q")
+    s = _out(s, (2 * N // 128, M, 4), torch.uint8, dev, "s")
+    q_t = _out(q_t, (2 * N, ldq), torch.uint8, dev, "q_t")
+    s_t = _out(s_t, (ldq // 128, 2 * N, 4), torch.uint8, dev, "s_t")
+    with _on(dev):
+        _check("mx_swiglu_quantize_bwd",
+               lib.mx_swiglu_quantize_bwd(_ptr(dh), _ptr(kept), _ptr(kept_s), _ptr(rows), _ptr(pos), _ptr(combine), n, M,
+                                          N, ldq, _ptr(q), _ptr(s), _ptr(q_t), _ptr(s_t), _ptr(dcombine), _ptr(ws),
+                                          0 if ws is None else ws.numel(), _stream(dev)))
+    return q, s, q_t, s_t, dcombine
+
+
+def _combine_sizes(y, combine, pos):
+    """Checks of the weighted sum's operands: (type of y, T, k, N)."""
+    import torch
+    kind = _type(y, "y")
+    _require(combine, torch.float32, "combine")
+    if y.dim() != 3:
+        raise ValueError("y must be [T, k, N] (one row per item)")
+    T, k, N = y.shape
+    if tuple(combine.shape) != (T, k):
+        raise ValueError(f"combine must be [{T}, {k}], got {tuple(combine.shape)}")
+    _same_device(y, combine)
+    if pos is not None:
+        _require(pos, torch.int32, "pos")
+        _same_device(y, pos)
+        if pos.numel() != T * k:
+            raise ValueError(f"pos must hold one entry per item ({T * k}), got {pos.numel()}")
+    return kind, T, k, N
+
+
+def mx_topk_combine_fwd(y, combine, pos=None, out=None):
+    """out bf16 [T, N] = sum_j combine[t, j] * y[t, j] (see mx_topk_combine), without a gradient."""
+    import torch
+    lib = load_library()
+    kind, T, k, N = _combine_sizes(y, combine, pos)
+    dev = y.device
+    out = _out(out, (T, N), torch.bfloat16, dev, "out")
+    with _on(dev):
+        _check("mx_topk_combine_fwd",
+               lib.mx_topk_combine_fwd(_ptr(y), kind, _ptr(combine), _ptr(pos), T, k, N, _ptr(out), _stream(dev)))
+    return out
+
+
+def mx_topk_combine_bwd(dout, y, combine, pos=None, need_dy: bool = True, need_dcombine: bool = True, dy=None,
+                        dcombine=None):
+    """(dy [T, k, N] in y's type, dcombine fp32 [T, k]) of the weighted sum from dout bf16 [T, N]; None for one
+    that is not needed."""
+    import torch
+    lib = load_library()
+    kind, T, k, N = _combine_sizes(y, combine, pos)
+    _require(dout, torch.bfloat16, "dout")
+    if tuple(dout.shape) != (T, N):
+        raise ValueError(f"dout must be [{T}, {N}], got {tuple(dout.shape)}")
+    _same_device(y, dout)
+    dev = y.device
+    dy = _out(dy, (T, k, N), y.dtype, dev, "dy") if need_dy else None
+    dcombine = _out(dcombine, (T, k), torch.float32, dev, "dcombine") if need_dcombine else None
+    with _on(dev):
+        _check("mx_topk_combine_bwd",
+               lib.mx_topk_combine_bwd(_ptr(y), kind, _ptr(combine), _ptr(pos), _ptr(dout), T, k, N, _ptr(dy),
+                                       _ptr(dcombine), _stream(dev)))
+    return dy, dcombine
+
+
+def mx_topk_combine(y, combine, pos=None):
+    """Differentiable weighted sum over a token's experts: out[t] = sum_j combine[t, j] * y[t, j], bf16 [T, N], of
+    y bf16 or fp32 [T, k, N] (what mx_routed_experts returns for a top-k router) and combine fp32 [T, k].
+    Summed in fp32 in slot order and rounded once.  pos int32 [T * k] (of mx_route): items with a negative
+    entry were not routed; their rows are not read, add nothing and get zero gradients.  N % 8 == 0."""
+    from .autograd import mx_topk_combine as _f
+    return _f(y, combine, pos)
+
+
+def mx_moe_layer(x, expert_idx, combine, W13, W2, check: bool = True, weights=None, cache=None,
+                 weight_format: str = "mxfp8"):
+    """A differentiable gated MoE layer on the MXFP8 grouped products (the training form of
+    mx_moe_few_tokens):
+        out[t] = sum_j combine[t, j] * (silu(g) * u) @ W2[e]^T,
+        g, u = x[t] @ W13[e]^T split in halves,  e = expert_idx[t, j]."""
+    from .autograd import mx_moe_layer as _f
+    return _f(x, expert_idx, combine, W13, W2, check, weights, cache, weight_format)

@@ -40,7 +40,9 @@ import weakref
 from . import (_format, _on, mx_grouped_gemm_mx, mx_grouped_gemm_mx_rows, mx_grouped_gemm_mxfp4,
                mx_grouped_mm_dgrad_fp4, mx_grouped_mm_dgrad_q, mx_grouped_mm_fwd_fp4, mx_grouped_mm_fwd_q,
                mx_quantize_dual, mx_quantize_dual_gather, mx_quantize_rowwise_gather, mx_quantize_weights,
-               mx_quantize_weights_fp4, mx_route, mx_topk_sum_rows)
+               mx_quantize_weights_fp4, mx_route, mx_swiglu_bwd, mx_swiglu_fwd, mx_swiglu_quantize,
+               mx_swiglu_quantize_bwd, mx_swiglu_quantize_fwd, mx_topk_combine_bwd, mx_topk_combine_fwd,
+               mx_topk_router_bwd, mx_topk_router_fwd, mx_topk_sum_rows)
 
 
 class WeightCache:
@@ -360,3 +362,253 @@ def mx_routed_experts(x, expert_idx, W, check: bool = True, weights=None, cache:
         mx4 = _weights_for(W, weights, cache, weight_format)
         out = _MXRouted.get().apply(x.contiguous(), W, offs, rows, mx4, not check, topk, weight_format)
         return out if expert_idx.dim() == 1 else out.view(T, topk, N)
+
+
+def _wants_grad(*tensors):
+    import torch
+    return torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
+
+
+class _MXRouter:
+    """torch.autograd.Function of mx_topk_router (built lazily)."""
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            import torch
+
+            class Fn(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, logits, bias, k, score, groups, topk_groups, group_score, renormalize, scale):
+                    expert_idx, combine = mx_topk_router_fwd(logits, k, score, bias, groups, topk_groups, group_score,
+                                                             renormalize, scale)
+                    ctx.mark_non_differentiable(expert_idx)
+                    ctx.save_for_backward(logits, expert_idx, combine)
+                    ctx.score, ctx.renormalize, ctx.scale = score, renormalize, scale
+                    return expert_idx, combine
+
+                @staticmethod
+                @torch.autograd.function.once_differentiable
+                def backward(ctx, _, dcombine):
+                    logits, expert_idx, combine = ctx.saved_tensors
+                    dlogits = mx_topk_router_bwd(logits, expert_idx, combine, dcombine.contiguous(), ctx.score,
+                                                 ctx.renormalize, ctx.scale)
+                    return dlogits, None, None, None, None, None, None, None, None
+
+            cls.fn = Fn
+        return cls.fn
+
+
+def mx_topk_router(logits, k, score="softmax", bias=None, groups=1, topk_groups=1, group_score="max",
+                   renormalize=True, scale=1.0):
+    """(expert_idx int32 [T, k], combine fp32 [T, k]) of the router's logits [T, E], differentiable in the
+    logits (the package's mx_topk_router).  The bias takes part in the choice alone: it gets no gradient,
+    and one that requires it is refused."""
+    logits = logits.contiguous()
+    if bias is not None and _wants_grad(bias):
+        raise ValueError("mx_topk_router: the bias takes part in the choice of the experts alone and gets no "
+                         "gradient: pass bias.detach()")
+    if not _wants_grad(logits):
+        return mx_topk_router_fwd(logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale)
+    return _MXRouter.get().apply(logits, bias, k, score, groups, topk_groups, group_score, renormalize, scale)
+
+
+class _MXSwiglu:
+    """torch.autograd.Function of mx_swiglu (built lazily)."""
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            import torch
+
+            class Fn(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, gu):
+                    h, kept, kept_s = mx_swiglu_fwd(gu)
+                    ctx.save_for_backward(kept, kept_s)
+                    return h
+
+                @staticmethod
+                @torch.autograd.function.once_differentiable
+                def backward(ctx, dh):
+                    return mx_swiglu_bwd(dh.contiguous(), *ctx.saved_tensors)
+
+            cls.fn = Fn
+        return cls.fn
+
+
+def mx_swiglu(gu):
+    """silu(gate) * up with an MXFP8 checkpoint of gu for the backward (the package's mx_swiglu)."""
+    gu = gu.contiguous()
+    if not _wants_grad(gu):
+        return mx_swiglu_fwd(gu, keep=False)[0]
+    return _MXSwiglu.get().apply(gu)
+
+
+class _MXCombine:
+    """torch.autograd.Function of mx_topk_combine (built lazily)."""
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            import torch
+
+            class Fn(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, y, combine, pos):
+                    ctx.save_for_backward(y, combine, pos)
+                    return mx_topk_combine_fwd(y, combine, pos)
+
+                @staticmethod
+                @torch.autograd.function.once_differentiable
+                def backward(ctx, dout):
+                    y, combine, pos = ctx.saved_tensors
+                    dy, dcombine = mx_topk_combine_bwd(dout.contiguous(), y, combine, pos, ctx.needs_input_grad[0],
+                                                       ctx.needs_input_grad[1])
+                    return dy, dcombine, None
+
+            cls.fn = Fn
+        return cls.fn
+
+
+def mx_topk_combine(y, combine, pos=None):
+    """Weighted sum over a token's experts, differentiable in y and combine (the package's mx_topk_combine)."""
+    y, combine = y.contiguous(), combine.contiguous()
+    if not _wants_grad(y, combine):
+        return mx_topk_combine_fwd(y, combine, pos)
+    return _MXCombine.get().apply(y, combine, pos)
+
+
+class _MXLayer:
+    """torch.autograd.Function of mx_moe_layer (built lazily)."""
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            import torch
+
+            class Fn(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, x, combine, W13, W2, offs, rows, pos, mx13, mx2, zero_fill, weight_format):
+                    T, topk = combine.shape
+                    K, cap = x.shape[1], rows.shape[0]
+                    q13, s13, q13t, s13t = mx13
+                    q2, s2, q2t, s2t = mx2
+                    # tokens in both orientations; the columns feed the weight gradient
+                    qx, sx, qxt, sxt = mx_quantize_dual_gather(x, rows, topk=topk, ldq=cap)
+                    gu = _rows_gemm(qx, sx, q13, s13, offs, weight_format)
+                    del qx, sx
+                    qh, sh, qht, sht, kept, kept_s = mx_swiglu_quantize_fwd(gu, rows, combine, ldq=cap)
+                    del gu
+                    y = torch.empty((T, topk, K), dtype=torch.bfloat16, device=x.device)
+                    _rows_gemm_mapped(qh, sh, q2, s2, offs, rows, y.view(T * topk, K), weight_format)
+                    del qh, sh
+                    out = mx_topk_combine_fwd(y, combine, pos)
+                    if not ctx.needs_input_grad[2]:
+                        qxt = sxt = None
+                    if not ctx.needs_input_grad[3]:
+                        qht = sht = None
+                    ctx.zero_fill, ctx.weight_format = zero_fill, weight_format
+                    ctx.save_for_backward(combine, offs, rows, pos, q13t, s13t, q2t, s2t, qxt, sxt, qht, sht, kept, kept_s)
+                    return out
+
+                @staticmethod
+                @torch.autograd.function.once_differentiable
+                def backward(ctx, dout):
+                    (combine, offs, rows, pos, q13t, s13t, q2t, s2t, qxt, sxt, qht, sht, kept,
+                     kept_s) = ctx.saved_tensors
+                    T, topk = combine.shape
+                    cap = rows.shape[0]
+                    need_x, need_c, need_13, need_2 = ctx.needs_input_grad[:4]
+                    dx = dcombine = dW13 = dW2 = None
+                    # each item's gradient without its combine weight: the weight is in the columns of h
+                    # (down weights) and enters the gradient of gu in the activation's backward
+                    qg, sg, qgt, sgt = mx_quantize_dual_gather(dout.contiguous(), rows, topk=topk, ldq=cap)
+                    if need_2:
+                        dW2 = mx_grouped_gemm_mx(qgt, sgt, qht, sht, offs, 1)
+                    del qgt, sgt
+                    if need_x or need_c or need_13:
+                        dh = _rows_gemm(qg, sg, q2t, s2t, offs, ctx.weight_format)
+                        del qg, sg
+                        qd, sd, qdt, sdt, dcombine = mx_swiglu_quantize_bwd(dh, kept, kept_s, rows, pos, combine, ldq=cap)
+                        del dh
+                        if need_13:
+                            dW13 = mx_grouped_gemm_mx(qdt, sdt, qxt, sxt, offs, 1)
+                        del qdt, sdt
+                        if need_x:
+                            alloc = torch.zeros if ctx.zero_fill else torch.empty      # rows of items that were dropped
+                            items = alloc((T * topk, q13t.shape[1]), device=dout.device,
+                                          dtype=torch.bfloat16 if topk == 1 else torch.float32)
+                            _rows_gemm_mapped(qd, sd, q13t, s13t, offs, rows, items, ctx.weight_format)
+                            dx = items if topk == 1 else mx_topk_sum_rows(items, topk)
+                    return dx, dcombine if need_c else None, dW13, dW2, None, None, None, None, None, None, None
+
+            cls.fn = Fn
+        return cls.fn
+
+
+def mx_moe_layer(x, expert_idx, combine, W13, W2, check: bool = True, weights=None, cache: WeightCache | None = None,
+                 weight_format: str = "mxfp8"):
+    """Differentiable gated MoE layer:
+
+        out[t] = sum_j combine[t, j] * (silu(g) * u) @ W2[e]^T,
+        g, u = x[t] @ W13[e]^T split in halves,  e = expert_idx[t, j].
+
+    x bf16 [T, K]; expert_idx int32 and combine fp32, both [T] or [T, k] (what mx_topk_router returns); W13
+    bf16 [E, 2N, K] (gate rows first) and W2 bf16 [E, K, N], K and N multiples of 128.  Gradients of x,
+    combine, W13 and W2.  Every step runs in the library: mx_route groups the items by expert, the tokens
+    are gathered inside the quantizer, the activation between the products writes the down product's
+    operand, and mx_topk_combine_fwd sums a token's experts.  Between the steps: gate and up values, the
+    experts' rows and the gradient of h are bf16.  The backward keeps the tokens and combine * h in
+    32x1 blocks and the gate and up values in 1x32 blocks, all MXFP8: 1.03 (K + 3 N) bytes per item; the
+    gradient through the activation and that of combine are taken at the kept values.
+
+    Weights: `weights` = (4-tuple of W13, 4-tuple of W2) of mx_quantize_weights (or _fp4 with
+    weight_format="mxfp4"), else from `cache`, as for mx_grouped_mm.  check=True reads the routing status
+    (one synchronization) and raises on an expert id outside [0, E); with check=False such items add
+    nothing and get zero gradients.  Without a gradient to compute nothing is kept."""
+    import torch
+    if x.dtype != torch.bfloat16 or W13.dtype != torch.bfloat16 or W2.dtype != torch.bfloat16:
+        raise TypeError("mx_moe_layer: x, W13 and W2 must be bfloat16")
+    if x.dim() != 2 or W13.dim() != 3 or W2.dim() != 3:
+        raise ValueError("mx_moe_layer: x must be [T, K], W13 [E, 2N, K] and W2 [E, K, N]")
+    T, K = x.shape
+    E, N = W13.shape[0], W2.shape[2]
+    if tuple(W13.shape) != (E, 2 * N, K) or tuple(W2.shape) != (E, K, N):
+        raise ValueError(f"mx_moe_layer: W13 must be [E, 2N, K={K}] and W2 [E, K={K}, N], got {tuple(W13.shape)} and "
+                         f"{tuple(W2.shape)}")
+    if K % 128 or N % 128:
+        raise ValueError(f"mx_moe_layer: K={K} and N={N} must be multiples of 128")
+    if expert_idx.dtype != torch.int32 or combine.dtype != torch.float32:
+        raise TypeError("mx_moe_layer: expert_idx must be int32 and combine float32")
+    if expert_idx.dim() not in (1, 2) or expert_idx.shape[0] != T or expert_idx.shape != combine.shape:
+        raise ValueError(f"mx_moe_layer: expert_idx and combine must both be [T={T}] or [T={T}, k], got "
+                         f"{tuple(expert_idx.shape)} and {tuple(combine.shape)}")
+    topk = 1 if expert_idx.dim() == 1 else expert_idx.shape[1]
+    if topk < 1:
+        raise ValueError("mx_moe_layer: k must be at least 1")
+    if weights is not None and len(weights) != 2:
+        raise ValueError("mx_moe_layer: weights must be the 4-tuples of W13 and W2")
+    combine = combine.reshape(T, topk).contiguous()
+    if T == 0:
+        # no token, and zeros for the weights' gradients
+        return x * 1 + 0 * (W13.sum() + W2.sum() + combine.sum()).to(x.dtype) if _wants_grad(x, combine, W13, W2) else x.clone()
+    with _on(x.device):
+        offs, rows, pos, status = mx_route(expert_idx.contiguous().reshape(-1), E)
+        if check and int(status.item()):
+            raise ValueError(f"mx_moe_layer: an expert id lies outside [0, {E})")
+        x, W13, W2 = x.contiguous(), W13.contiguous(), W2.contiguous()
+        mx13, mx2 = (_weights_for(W, w, cache, weight_format) for W, w in zip((W13, W2), weights or (None, None)))
+        if _wants_grad(x, combine, W13, W2):
+            return _MXLayer.get().apply(x, combine, W13, W2, offs, rows, pos, mx13, mx2, not check, weight_format)
+        gathered = torch.div(rows, topk, rounding_mode="floor") if topk > 1 else rows
+        qx, sx = mx_quantize_rowwise_gather(x, gathered)
+        gu = _rows_gemm(qx, sx, *mx13[:2], offs, weight_format)
+        qh, sh = mx_swiglu_quantize(gu, rows)
+        y = torch.empty((T, topk, K), dtype=torch.bfloat16, device=x.device)
+        _rows_gemm_mapped(qh, sh, *mx2[:2], offs, rows, y.view(T * topk, K), weight_format)
+        return mx_topk_combine_fwd(y, combine, pos)

@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmxmoe.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
-SOURCES = ["mx_quant.hip", "mx_gemm.hip", "mx_route.hip", "mx_noalloc.hip", "mx_fp4.hip", "mx_fp4_gemm.hip", "mx_moe.hip", "mx_api.cpp"]
+SOURCES = ["mx_quant.hip", "mx_gemm.hip", "mx_route.hip", "mx_noalloc.hip", "mx_fp4.hip", "mx_fp4_gemm.hip", "mx_moe.hip",
+           "mx_router.hip", "mx_swiglu.hip", "mx_combine.hip", "mx_api.cpp"]
 
 # -packed-fp32-ops: never emit packed fp32 VALU instructions.
 HIP_FLAGS = [

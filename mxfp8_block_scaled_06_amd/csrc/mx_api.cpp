@@ -828,3 +828,310 @@ mx_status mx_moe_few_tokens(const uint16_t* x, const int32_t* expert_idx, const 
 }
 
 }  // extern "C"
+
+extern "C" {
+
+mx_status mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t batch, int64_t rows, int64_t cols, int scale_layout,
+                        uint16_t* out, void* stream) {
+  const char* fn = "mx_dequantize";
+  const mx_status st = check_fp4(fn, out, batch, rows, cols, q, s, scale_layout);
+  if (st != MX_OK || rows == 0 || cols == 0) return st;
+  return hip_status(mxk::launch_dequant(q, s, batch * rows, cols, out, scale_layout == MX_SCALES_GEMM ? rows : 0,
+                                        (hipStream_t)stream),
+                    fn);
+}
+
+}  // extern "C"
+
+namespace {
+
+mx_status check_router(const char* fn, int logits_type, int64_t T, int64_t E, int64_t k, int score, float scale) {
+  if (logits_type != MX_BF16 && logits_type != MX_F32)
+    return fail(MX_ERR_SHAPE, "%s: logits_type must be MX_BF16 = %d or MX_F32 = %d (got %d)", fn, MX_BF16, MX_F32,
+                logits_type);
+  if (score != MX_SCORE_SOFTMAX && score != MX_SCORE_SIGMOID)
+    return fail(MX_ERR_SHAPE, "%s: score must be MX_SCORE_SOFTMAX = %d or MX_SCORE_SIGMOID = %d (got %d)", fn,
+                MX_SCORE_SOFTMAX, MX_SCORE_SIGMOID, score);
+  if (T < 0 || T >= ((int64_t)1 << 31)) return fail(MX_ERR_SHAPE, "%s: T=%lld outside [0, 2^31)", fn, (long long)T);
+  if (E < 1 || E > mxk::kMaxExperts)
+    return fail(MX_ERR_SHAPE, "%s: number of experts E=%lld outside [1, %d]", fn, (long long)E, mxk::kMaxExperts);
+  if (k < 1 || k > MX_MOE_MAX_TOPK || k > E)
+    return fail(MX_ERR_SHAPE, "%s: k=%lld outside [1, %d], or more than the %lld experts", fn, (long long)k,
+                MX_MOE_MAX_TOPK, (long long)E);
+  if (!(scale > 0.f) || !(scale <= 3.402823466e38f))
+    return fail(MX_ERR_SHAPE, "%s: scale must be positive and finite (got %g)", fn, (double)scale);
+  return MX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_topk_router_fwd(const void* logits, int logits_type, const float* bias, int64_t T, int64_t E, int64_t k,
+                             int score, int64_t groups, int64_t topk_groups, int group_score, int renormalize,
+                             float scale, int32_t* expert_idx, float* combine, void* stream) {
+  const char* fn = "mx_topk_router_fwd";
+  const mx_status st = check_router(fn, logits_type, T, E, k, score, scale);
+  if (st != MX_OK) return st;
+  if (groups < 1 || groups > MX_ROUTER_MAX_GROUPS || E % groups != 0)
+    return fail(MX_ERR_SHAPE, "%s: groups=%lld must divide E=%lld and lie in [1, %d]", fn, (long long)groups,
+                (long long)E, MX_ROUTER_MAX_GROUPS);
+  if (topk_groups < 1 || topk_groups > groups || topk_groups * (E / groups) < k)
+    return fail(MX_ERR_SHAPE, "%s: topk_groups=%lld must lie in [1, groups=%lld] and hold k=%lld experts", fn,
+                (long long)topk_groups, (long long)groups, (long long)k);
+  if (group_score != MX_GROUP_MAX && group_score != MX_GROUP_TOP2)
+    return fail(MX_ERR_SHAPE, "%s: group_score must be MX_GROUP_MAX = %d or MX_GROUP_TOP2 = %d (got %d)", fn,
+                MX_GROUP_MAX, MX_GROUP_TOP2, group_score);
+  if (T == 0) return MX_OK;
+  if (!logits || !expert_idx || !combine) return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(expert_idx, 4) || !aligned(combine, 4))
+    return fail(MX_ERR_ALIGN, "%s: logits must be 16-byte, the other tensors 4-byte aligned", fn);
+  mxk::RouterArgs a{};
+  a.logits = logits;
+  a.bias = bias;
+  a.expert_idx = expert_idx;
+  a.combine = combine;
+  a.T = T;
+  a.E = (int)E;
+  a.k = (int)k;
+  a.score = score;
+  a.groups = (int)groups;
+  a.topk_groups = (int)topk_groups;
+  a.group_top2 = group_score == MX_GROUP_TOP2;
+  a.renormalize = renormalize != 0;
+  a.logits_f32 = logits_type == MX_F32;
+  a.scale = scale;
+  return hip_status(mxk::launch_router_fwd(a, (hipStream_t)stream), fn);
+}
+
+mx_status mx_topk_router_bwd(const void* logits, int logits_type, const int32_t* expert_idx, const float* combine,
+                             const float* dcombine, int64_t T, int64_t E, int64_t k, int score, int renormalize,
+                             float scale, void* dlogits, void* stream) {
+  const char* fn = "mx_topk_router_bwd";
+  const mx_status st = check_router(fn, logits_type, T, E, k, score, scale);
+  if (st != MX_OK) return st;
+  if (T == 0) return MX_OK;
+  if (!logits || !expert_idx || !combine || !dcombine || !dlogits) return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(logits, 16) || !aligned(dlogits, 16) || !aligned(expert_idx, 4) || !aligned(combine, 4) ||
+      !aligned(dcombine, 4))
+    return fail(MX_ERR_ALIGN, "%s: logits and dlogits must be 16-byte, the other tensors 4-byte aligned", fn);
+  mxk::RouterArgs a{};
+  a.logits = logits;
+  a.expert_idx = const_cast<int32_t*>(expert_idx);
+  a.combine = const_cast<float*>(combine);
+  a.T = T;
+  a.E = (int)E;
+  a.k = (int)k;
+  a.score = score;
+  a.renormalize = renormalize != 0;
+  a.logits_f32 = logits_type == MX_F32;
+  a.scale = scale;
+  return hip_status(mxk::launch_router_bwd(a, dcombine, dlogits, (hipStream_t)stream), fn);
+}
+
+}  // extern "C"
+
+namespace {
+
+mx_status check_swiglu(const char* fn, int64_t M, int64_t N, int64_t mult) {
+  if (M < 0 || N < 0) return fail(MX_ERR_SHAPE, "%s: negative size M=%lld N=%lld", fn, (long long)M, (long long)N);
+  if (N % mult != 0) return fail(MX_ERR_SHAPE, "%s: N=%lld is not a multiple of %lld", fn, (long long)N, (long long)mult);
+  // two blocks of gate and up values to one of h
+  const int64_t most = ((int64_t)1 << 32) - 1;
+  if (M > most || N / 32 > most || (N > 0 && M > most / (N / 32)))
+    return fail(MX_ERR_SHAPE, "%s: M*N/32 must be below 2^32 blocks", fn);
+  return MX_OK;
+}
+
+// Sizes of the activation between two products.  rows: those of the launch.
+mx_status check_swiglu_tiles(const char* fn, int64_t M, int64_t N, int64_t ldq, int64_t n_items, bool train) {
+  const mx_status st = check_swiglu(fn, M, N, 128);
+  if (st != MX_OK) return st;
+  if (n_items < 0 || n_items >= ((int64_t)1 << 31))
+    return fail(MX_ERR_SHAPE, "%s: n_items=%lld outside [0, 2^31)", fn, (long long)n_items);
+  if (train && (M % 32 != 0 || ldq % 128 != 0 || ldq < M))
+    return fail(MX_ERR_SHAPE, "%s: M=%lld must be a multiple of 32 and ldq=%lld one of 128, >= M", fn, (long long)M,
+                (long long)ldq);
+  if ((train ? ldq : M) / 256 >= 65535) return fail(MX_ERR_SHAPE, "%s: too many rows for one launch", fn);
+  return MX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_swiglu_fwd(const uint16_t* gu, int64_t M, int64_t N, uint16_t* h, uint8_t* kept, uint8_t* kept_s,
+                        void* stream) {
+  const char* fn = "mx_swiglu_fwd";
+  const mx_status st = check_swiglu(fn, M, N, 32);
+  if (st != MX_OK || M == 0 || N == 0) return st;
+  if (!gu || !h || (!kept != !kept_s)) return fail(MX_ERR_NULL, "%s: null pointer (kept and kept_s: both or none)", fn);
+  if (!aligned(gu, 16) || !aligned(h, 16) || !aligned(kept, 16))
+    return fail(MX_ERR_ALIGN, "%s: gu, h and kept must be 16-byte aligned", fn);
+  return hip_status(mxk::launch_swiglu_fwd(gu, M, N, h, kept, kept_s, (hipStream_t)stream), fn);
+}
+
+mx_status mx_swiglu_bwd(const uint16_t* dh, const uint8_t* kept, const uint8_t* kept_s, int64_t M, int64_t N,
+                        uint16_t* dgu, void* stream) {
+  const char* fn = "mx_swiglu_bwd";
+  const mx_status st = check_swiglu(fn, M, N, 32);
+  if (st != MX_OK || M == 0 || N == 0) return st;
+  if (!dh || !kept || !kept_s || !dgu) return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(dh, 16) || !aligned(kept, 16) || !aligned(dgu, 16))
+    return fail(MX_ERR_ALIGN, "%s: dh, kept and dgu must be 16-byte aligned", fn);
+  return hip_status(mxk::launch_swiglu_bwd(dh, kept, kept_s, M, N, dgu, (hipStream_t)stream), fn);
+}
+
+mx_status mx_swiglu_quantize(const uint16_t* gu, const int32_t* rows, int64_t n_items, int64_t M, int64_t N, uint8_t* q,
+                             uint8_t* s, void* stream) {
+  const char* fn = "mx_swiglu_quantize";
+  const mx_status st = check_swiglu_tiles(fn, M, N, 0, rows ? n_items : 0, false);
+  if (st != MX_OK || M == 0 || N == 0) return st;
+  if (!gu || !q || !s) return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(gu, 16) || !aligned(q, 16) || !aligned(s, 4) || !aligned(rows, 4))
+    return fail(MX_ERR_ALIGN, "%s: gu and q must be 16-byte, s and rows 4-byte aligned", fn);
+  mxk::SwigluArgs a{};
+  a.gu = gu;
+  a.rows = rows;
+  a.q = q;
+  a.s = s;
+  a.M = M;
+  a.N = N;
+  a.n_items = rows ? n_items : M;
+  return hip_status(mxk::launch_swiglu_quantize_fwd(a, (hipStream_t)stream), fn);
+}
+
+mx_status mx_swiglu_quantize_fwd(const uint16_t* gu, const int32_t* rows, const float* combine, int64_t n_items,
+                                 int64_t M, int64_t N, int64_t ldq, uint8_t* q, uint8_t* s, uint8_t* q_t, uint8_t* s_t,
+                                 uint8_t* kept, uint8_t* kept_s, void* stream) {
+  const char* fn = "mx_swiglu_quantize_fwd";
+  const mx_status st = check_swiglu_tiles(fn, M, N, ldq, n_items, true);
+  if (st != MX_OK) return st;
+  if (!rows && n_items != M)
+    return fail(MX_ERR_SHAPE, "%s: without rows n_items=%lld must be M=%lld", fn, (long long)n_items, (long long)M);
+  if (ldq == 0 || N == 0) return MX_OK;
+  if (!q_t || !s_t || (M > 0 && (!gu || !q || !s || !kept || !kept_s))) return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(gu, 16) || !aligned(q, 16) || !aligned(q_t, 16) || !aligned(kept, 16) || !aligned(s, 4) ||
+      !aligned(s_t, 4) || !aligned(rows, 4) || !aligned(combine, 4))
+    return fail(MX_ERR_ALIGN, "%s: gu, q, q_t and kept must be 16-byte, s, s_t, rows and combine 4-byte aligned", fn);
+  mxk::SwigluArgs a{};
+  a.gu = gu;
+  a.rows = rows;
+  a.combine = combine;
+  a.kept = kept;
+  a.kept_s = kept_s;
+  a.q = q;
+  a.s = s;
+  a.q_t = q_t;
+  a.s_t = s_t;
+  a.M = M;
+  a.N = N;
+  a.ldq = ldq;
+  a.n_items = n_items;
+  return hip_status(mxk::launch_swiglu_quantize_fwd(a, (hipStream_t)stream), fn);
+}
+
+size_t mx_swiglu_quantize_workspace_bytes(int64_t M, int64_t N) {
+  if (M < 0 || N < 0 || N % 128 != 0 || M >= ((int64_t)1 << 32) || N >= ((int64_t)1 << 32)) return 0;
+  return align_up((size_t)M * (size_t)mxk::swiglu_col_tiles(N) * sizeof(float), 256);
+}
+
+mx_status mx_swiglu_quantize_bwd(const uint16_t* dh, const uint8_t* kept, const uint8_t* kept_s, const int32_t* rows,
+                                 const int32_t* pos, const float* combine, int64_t n_items, int64_t M, int64_t N,
+                                 int64_t ldq, uint8_t* q, uint8_t* s, uint8_t* q_t, uint8_t* s_t, float* dcombine,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "mx_swiglu_quantize_bwd";
+  const mx_status st = check_swiglu_tiles(fn, M, N, ldq, n_items, true);
+  if (st != MX_OK) return st;
+  if (!rows && n_items != M)
+    return fail(MX_ERR_SHAPE, "%s: without rows n_items=%lld must be M=%lld", fn, (long long)n_items, (long long)M);
+  if (rows && dcombine && !pos)
+    return fail(MX_ERR_NULL, "%s: dcombine of routed rows needs pos (items without a row get 0)", fn);
+  if (ldq > 0 && N > 0 && (!q_t || !s_t || (M > 0 && (!dh || !kept || !kept_s || !q || !s))))
+    return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(dh, 16) || !aligned(kept, 16) || !aligned(q, 16) || !aligned(q_t, 16) || !aligned(s, 4) ||
+      !aligned(s_t, 4) || !aligned(rows, 4) || !aligned(pos, 4) || !aligned(combine, 4) || !aligned(dcombine, 4))
+    return fail(MX_ERR_ALIGN,
+                "%s: dh, kept, q and q_t must be 16-byte, the other tensors but kept_s 4-byte aligned", fn);
+  const size_t need = dcombine ? mx_swiglu_quantize_workspace_bytes(M, N) : 0;
+  if (need && (!ws || ws_bytes < need))
+    return fail(MX_ERR_WORKSPACE, "%s: workspace of %zu bytes at %p, need %zu", fn, ws_bytes, ws, need);
+  if (need && !aligned(ws, 256)) return fail(MX_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
+  mxk::SwigluArgs a{};
+  a.dh = dh;
+  a.rows = rows;
+  a.pos = pos;
+  a.combine = combine;
+  a.kept = const_cast<uint8_t*>(kept);
+  a.kept_s = const_cast<uint8_t*>(kept_s);
+  a.q = q;
+  a.s = s;
+  a.q_t = q_t;
+  a.s_t = s_t;
+  a.partial = dcombine ? (float*)ws : nullptr;
+  a.M = M;
+  a.N = N;
+  a.ldq = ldq;
+  a.n_items = n_items;
+  return hip_status(mxk::launch_swiglu_quantize_bwd(a, dcombine, (hipStream_t)stream), fn);
+}
+
+}  // extern "C"
+
+namespace {
+
+mx_status check_combine(const char* fn, int y_type, int64_t T, int64_t k, int64_t N) {
+  if (y_type != MX_BF16 && y_type != MX_F32)
+    return fail(MX_ERR_SHAPE, "%s: y_type must be MX_BF16 = %d or MX_F32 = %d (got %d)", fn, MX_BF16, MX_F32, y_type);
+  if (k < 1 || k > 1024) return fail(MX_ERR_SHAPE, "%s: k=%lld outside [1, 1024]", fn, (long long)k);
+  if (T < 0 || N < 0 || N % 8 != 0)
+    return fail(MX_ERR_SHAPE, "%s: T=%lld and N=%lld must not be negative, N a multiple of 8", fn, (long long)T,
+                (long long)N);
+  if (T >= ((int64_t)1 << 31) || N >= ((int64_t)1 << 31))
+    return fail(MX_ERR_SHAPE, "%s: T=%lld and N=%lld must be below 2^31", fn, (long long)T, (long long)N);
+  return MX_OK;
+}
+
+mxk::CombineArgs combine_args(const void* y, int y_type, const float* combine, const int32_t* pos, int64_t T, int64_t k,
+                              int64_t N) {
+  mxk::CombineArgs a{};
+  a.y = y;
+  a.combine = combine;
+  a.pos = pos;
+  a.T = T;
+  a.N = N;
+  a.k = (int)k;
+  a.y_f32 = y_type == MX_F32;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_topk_combine_fwd(const void* y, int y_type, const float* combine, const int32_t* pos, int64_t T, int64_t k,
+                              int64_t N, uint16_t* out, void* stream) {
+  const char* fn = "mx_topk_combine_fwd";
+  const mx_status st = check_combine(fn, y_type, T, k, N);
+  if (st != MX_OK || T == 0 || N == 0) return st;
+  if (!y || !combine || !out) return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(y, 16) || !aligned(out, 16) || !aligned(combine, 4) || !aligned(pos, 4))
+    return fail(MX_ERR_ALIGN, "%s: y and out must be 16-byte, combine and pos 4-byte aligned", fn);
+  return hip_status(mxk::launch_combine_fwd(combine_args(y, y_type, combine, pos, T, k, N), out, (hipStream_t)stream), fn);
+}
+
+mx_status mx_topk_combine_bwd(const void* y, int y_type, const float* combine, const int32_t* pos, const uint16_t* dout,
+                              int64_t T, int64_t k, int64_t N, void* dy, float* dcombine, void* stream) {
+  const char* fn = "mx_topk_combine_bwd";
+  const mx_status st = check_combine(fn, y_type, T, k, N);
+  if (st != MX_OK || T == 0 || (!dy && !dcombine)) return st;
+  if (!combine || (N > 0 && (!dout || (dcombine && !y)))) return fail(MX_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(y, 16) || !aligned(dout, 16) || !aligned(dy, 16) || !aligned(combine, 4) || !aligned(pos, 4) ||
+      !aligned(dcombine, 4))
+    return fail(MX_ERR_ALIGN, "%s: y, dout and dy must be 16-byte, combine, pos and dcombine 4-byte aligned", fn);
+  return hip_status(
+      mxk::launch_combine_bwd(combine_args(y, y_type, combine, pos, T, k, N), dout, dy, dcombine, (hipStream_t)stream),
+      fn);
+}
+
+}  // extern "C"

@@ -116,6 +116,57 @@ struct MoeArgs {
 };
 hipError_t launch_moe_few_tokens(const MoeArgs& a, hipStream_t st);
 
+// MXFP8 codes back to bf16 (mx_quant.hip); scales as launch_quant_rowwise_fp4.
+hipError_t launch_dequant(const uint8_t* q, const uint8_t* s, int64_t rows_total, int64_t cols, uint16_t* out,
+                          int64_t gemm_rows_per_batch, hipStream_t st);
+
+// The router (mx_router.hip).
+struct RouterArgs {
+  const void* logits;         // [T, E] bf16 or fp32
+  const float* bias;          // [E] or null
+  int32_t* expert_idx;        // [T, k]
+  float* combine;             // [T, k]
+  int64_t T;
+  int E, k, score, groups, topk_groups;
+  int group_top2, renormalize, logits_f32;
+  float scale;
+};
+hipError_t launch_router_fwd(const RouterArgs& a, hipStream_t st);
+hipError_t launch_router_bwd(const RouterArgs& a, const float* dcombine, void* dlogits, hipStream_t st);
+
+// The gated activation and its 8-bit checkpoint (mx_swiglu.hip).
+hipError_t launch_swiglu_fwd(const uint16_t* gu, int64_t M, int64_t N, uint16_t* h, uint8_t* kept, uint8_t* kept_s,
+                             hipStream_t st);
+hipError_t launch_swiglu_bwd(const uint16_t* dh, const uint8_t* kept, const uint8_t* kept_s, int64_t M, int64_t N,
+                             uint16_t* dgu, hipStream_t st);
+struct SwigluArgs {
+  const uint16_t* gu;         // [M, 2N] (forward)
+  const uint16_t* dh;         // [M, N] (backward)
+  const int32_t* rows;        // item of each row, or null: the row itself
+  const int32_t* pos;         // row of each item, or null
+  const float* combine;       // [n_items], or null: 1
+  uint8_t* kept;              // [M, 2N] codes
+  uint8_t* kept_s;            // [M, 2N/32]
+  uint8_t *q, *s;             // rowwise codes and scales (GEMM layout) of h, or of dgu
+  uint8_t *q_t, *s_t;         // colwise ones of w h (null: rowwise alone), or of dgu
+  float* partial;             // [N/128, M] (backward), or null
+  int64_t M, N, ldq, n_items;
+};
+int64_t swiglu_col_tiles(int64_t N);
+hipError_t launch_swiglu_quantize_fwd(const SwigluArgs& a, hipStream_t st);
+hipError_t launch_swiglu_quantize_bwd(const SwigluArgs& a, float* dcombine, hipStream_t st);
+
+// The weighted sum over a token's experts (mx_combine.hip).
+struct CombineArgs {
+  const void* y;              // [T, k, N] bf16 or fp32
+  const float* combine;       // [T, k]
+  const int32_t* pos;         // [T, k] or null: negative where the item was not routed
+  int64_t T, N;
+  int k, y_f32;
+};
+hipError_t launch_combine_fwd(const CombineArgs& a, uint16_t* out, hipStream_t st);
+hipError_t launch_combine_bwd(const CombineArgs& a, const uint16_t* dout, void* dy, float* dcombine, hipStream_t st);
+
 // Record `text` as the calling thread's mx_last_error() and return `st`.
 mx_status set_last_error(mx_status st, const char* text);
 

@@ -1,0 +1,93 @@
+// The sigmoid of the gated activation, and values of MXFP8 codes.
+#pragma once
+
+#include "mx_device.h"
+
+namespace mxk {
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+// sigmoid(x) = m, or m * 2^-160 where `far`, and 1 - sigmoid(x) = q, off by some
+// 2^-22 of the value over the whole fp32 range.  e^-x = 2^y of y = -x / ln 2 by the
+// hardware, with what the product rounds away put back.  From y = 120 on (the one
+// is lost beside the power) the power is taken with 2^-160: its reciprocal would be
+// subnormal past y = 126, which the hardware makes zero, while silu(-90) * u may be
+// any number.  Past |y| = 280 the result is 0 or 1, with nothing to put back.
+struct Sigmoid {
+  float m, q;
+  bool far;
+};
+
+__device__ __forceinline__ Sigmoid sigmoid_parts(float x) {
+  const float y = x * -1.442695041f;
+  const float lo = fmaf(x, -1.925963033e-8f, fmaf(x, -1.442695041f, -y));
+  Sigmoid s;
+  s.far = y > 120.f;
+  float p = __builtin_amdgcn_exp2f(s.far ? y - 160.f : y);
+  const float whole = fmaf(p * lo, 0.6931471806f, p);
+  p = fabsf(y) < 280.f ? whole : p;
+  s.m = __builtin_amdgcn_rcpf((s.far ? 0.f : 1.f) + p);
+  s.q = s.far ? 1.f : p * s.m;
+  return s;
+}
+
+// a * b where a was computed from s.m.  The 2^-160 is split so that neither factor
+// falls below fp32's range where the product does not.
+__device__ __forceinline__ float scaled(const Sigmoid& s, float a, float b) {
+  return __builtin_ldexpf(a, s.far ? -40 : 0) * __builtin_ldexpf(b, s.far ? -120 : 0);
+}
+
+// silu(x) * u
+__device__ __forceinline__ float silu_mul(float x, float u) {
+  const Sigmoid s = sigmoid_parts(x);
+  return scaled(s, x * s.m, u);
+}
+
+// The scale of an E8M0 byte as fp32: 2^(byte - 127), NaN for 255.
+__device__ __forceinline__ float scale_from_e8m0(uint32_t byte) {
+  const uint32_t bits = byte == 0u ? 0x00400000u : byte << 23;
+  return __uint_as_float(byte == 0xFFu ? 0x7FC00000u : bits);
+}
+
+// Four E4M3 codes of a dword -> their values times `scale`.
+__device__ __forceinline__ void values4(uint32_t codes, float scale, float* out) {
+  const v2f a = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false);
+  const v2f b = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true);
+  out[0] = a[0] * scale;
+  out[1] = a[1] * scale;
+  out[2] = b[0] * scale;
+  out[3] = b[1] * scale;
+}
+__device__ __forceinline__ void values8(v2i codes, float scale, float* out) {
+  values4((uint32_t)codes[0], scale, out);
+  values4((uint32_t)codes[1], scale, out + 4);
+}
+
+// E8M0 byte of a block from the bits of its largest |fp32|.
+__device__ __forceinline__ uint32_t e8m0_from_absbits32(uint32_t amax_bits) {
+  if (amax_bits >= 0x7F800000u) return 0xFFu;
+  const int e = (int)(amax_bits >> 23) - 8;
+  return (uint32_t)(e > 0 ? e : 0);
+}
+
+// Eight fp32 values of a block with scale byte `byte` -> E4M3 codes.
+__device__ __forceinline__ v2i quant8_f32(const float* x, uint32_t byte) {
+  if (byte == 0xFFu) return (v2i){0x7F7F7F7F, 0x7F7F7F7F};
+  const float m = inv_scale_from_e8m0(byte);
+  v2i r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int c = cvt2_e4m3<false>(x[4 * i] * m, x[4 * i + 1] * m, 0);
+    r[i] = cvt2_e4m3<true>(x[4 * i + 2] * m, x[4 * i + 3] * m, c);
+  }
+  return r;
+}
+
+__device__ __forceinline__ uint32_t absmax8_f32(const float* x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+}  // namespace mxk

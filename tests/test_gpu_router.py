@@ -1,0 +1,256 @@
+"""The router on the GPU against the fp64 oracle: every choice equal, weights and
+gradients within fp32's error; masks, ties, groups, NaN, odd expert counts,
+single tokens, graphs, and the ids as they reach the few-token layer."""
+
+import numpy as np
+import pytest
+
+from oracle import around, ulp_bf16
+from mxfp8_block_scaled_06_amd import inputs as inp
+from gpu_util import require_gpu, log
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = {"fp32": float(np.finfo(np.float32).min), "bf16": -2.0 ** 127 * (2 - 2.0 ** -7)}
+
+# Weights: two powers at 2^-22 each (the hardware's at 2^-23, its argument's
+# rounding put back), up to 16 + 6 additions of the sum, a division, a product
+# at 2^-24: below 2^-19.  Results below fp32's normal range may be 0.
+REL_W, TINY = 2.0 ** -19, 2.0 ** -126
+# Gradients: of the magnitudes they are added from, the weights' error, the sum
+# over the slots (five additions more) and three products: below 2^-18.
+REL_D = 2.0 ** -18
+
+
+def _logits(rng, T, E, dtype, std=1.5):
+    l = rng.normal(size=(T, E)).astype(np.float32) * np.float32(std)
+    return l if dtype == "fp32" else inp.bf16_bits_to_f32(inp.f32_to_bf16_bits(l))
+
+
+def _dev(l, dtype):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(l, dtype=np.float32)).to("cuda:0").to(
+        torch.float32 if dtype == "fp32" else torch.bfloat16)
+
+
+def _check(l, dtype, k, rng, bias=None, grad=True, **kw):
+    import torch
+    import mxfp8_block_scaled_06_amd as mx
+    T = l.shape[0]
+    rids, rw = around.router(l, LOWEST[dtype], k, bias=bias, **kw)
+    b = None if bias is None else torch.from_numpy(np.asarray(bias, dtype=np.float32)).to("cuda:0")
+    x = _dev(l, dtype).requires_grad_(grad)
+    ids, w = mx.mx_topk_router(x, k, bias=b, **kw)
+    assert np.array_equal(ids.cpu().numpy(), rids)
+    got = w.detach().cpu().double().numpy()
+    assert (np.abs(got - rw) <= REL_W * rw + TINY).all(), np.abs(got - rw).max()
+    if not grad:
+        return
+    dw = rng.normal(size=(T, k)).astype(np.float32)
+    dl, = torch.autograd.grad(w, x, torch.from_numpy(dw).to("cuda:0"))
+    assert dl.dtype == x.dtype
+    ref, mag = around.router_grad(l, LOWEST[dtype], rids, dw, kw.get("score", "softmax"), kw.get("renormalize", True),
+                                  kw.get("scale", 1.0))
+    tol = REL_D * mag + TINY
+    if dtype == "bf16":
+        tol = tol + 0.5 * ulp_bf16(np.abs(ref) + tol)
+    err = np.abs(dl.cpu().double().numpy() - ref)
+    assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 16, 1), (7, 5, 5), (33, 64, 8), (9, 65, 6), (130, 128, 32), (5, 200, 3),
+                                   (17, 256, 8), (4, 511, 7), (3, 1024, 32)])
+def test_router_matches_oracle(T, E, k, score, dtype):
+    require_gpu()
+    log(f"router T={T} E={E} k={k} {score} {dtype}")
+    rng = np.random.default_rng(T + E + k)
+    l = _logits(rng, T, E, dtype)
+    for renormalize in (True, False):
+        for bias in (None, rng.normal(size=E).astype(np.float32) * np.float32(0.05)):
+            _check(l, dtype, k, rng, bias, score=score, renormalize=renormalize, scale=2.5)
+
+
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("T,E,k,groups,kept", [(31, 256, 8, 8, 4), (6, 60, 4, 4, 1), (5, 66, 9, 3, 2), (3, 128, 8, 64, 7),
+                                               (2, 1024, 16, 16, 16), (4, 8, 2, 8, 2)])
+def test_groups(T, E, k, groups, kept, group_score):
+    require_gpu()
+    log(f"router groups T={T} E={E} k={k} groups={groups} kept={kept} {group_score}")
+    rng = np.random.default_rng(E + groups)
+    for score, bias in (("sigmoid", rng.normal(size=E).astype(np.float32) * np.float32(0.1)), ("softmax", None)):
+        _check(_logits(rng, T, E, "fp32"), "fp32", k, rng, bias, score=score, groups=groups, topk_groups=kept,
+               group_score=group_score)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_masked_experts(score, dtype):
+    """-inf and the lowest finite value mask alike; rows of nothing else give
+    weights and gradients of 0 and distinct ids."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    rng = np.random.default_rng(3)
+    l = _logits(rng, 40, 48, dtype)
+    l[rng.random(l.shape) < 0.3] = -np.inf
+    l[rng.random(l.shape) < 0.3] = LOWEST[dtype]
+    l[7] = -np.inf
+    l[8] = LOWEST[dtype]
+    l[9] = np.where(np.arange(48) % 2 == 0, -np.inf, LOWEST[dtype])
+    l[10] = -np.inf
+    l[10, 30] = -1e4                                         # one expert alone
+    bias = rng.normal(size=48).astype(np.float32)
+    for kw in ({}, {"groups": 6, "topk_groups": 2, "group_score": "top2"}, {"groups": 6, "topk_groups": 2}):
+        for b in (None, bias):
+            for renormalize in (True, False):
+                _check(l, dtype, 8, rng, b, score=score, renormalize=renormalize, **kw)
+    ids, w = mx.mx_topk_router(_dev(l, dtype), 8, score=score)
+    assert (w[7:10] == 0).all() and all(len(set(r)) == 8 for r in ids.cpu().numpy().tolist())
+    assert float(w[10, 0]) == 1
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_ties_go_to_the_lowest_index(bias):
+    """Few distinct logits: nearly every choice is one among equals."""
+    require_gpu()
+    rng = np.random.default_rng(4)
+    for E, k, groups in ((64, 8, 1), (200, 32, 1), (256, 8, 8), (96, 5, 4)):
+        l = rng.integers(-2, 3, size=(50, E)).astype(np.float32)
+        b = np.round(rng.normal(size=E)).astype(np.float32) if bias else None
+        for gs in ("max", "top2"):
+            _check(l, "bf16", k, rng, b, score="sigmoid", groups=groups, topk_groups=max(1, groups // 2), group_score=gs)
+
+
+def test_choice_beyond_fp32():
+    """Scores that fp32 holds equal and 64 bits do not: saturated sigmoids, small
+    scores beside a bias of the same value."""
+    require_gpu()
+    rng = np.random.default_rng(5)
+    l = 16 + np.arange(40, dtype=np.float32)[None, :] / 8 * rng.choice([-1, 1], size=(20, 40)).astype(np.float32)
+    _check(l, "fp32", 9, rng, np.zeros(40, np.float32), score="sigmoid", grad=False)
+    l = -rng.random((20, 300)).astype(np.float32) * 3 - 17
+    _check(l, "fp32", 9, rng, np.full(300, 0.75, np.float32), score="sigmoid")
+    # softmax scores 1e-9 apart
+    l = rng.normal(size=(64, 256)).astype(np.float32) * np.float32(1e-6)
+    _check(l, "fp32", 8, rng, np.full(256, -0.125, np.float32))
+
+
+def test_far_logits():
+    """Large logits, and weights whose scores lie below fp32's range."""
+    require_gpu()
+    rng = np.random.default_rng(6)
+    for score in ("softmax", "sigmoid"):
+        for shift in (-300.0, -95.0, 95.0, 3e4):
+            l = (_logits(rng, 12, 70, "fp32") + np.float32(shift)).astype(np.float32)
+            _check(l, "fp32", 6, rng, score=score, grad=shift > -300 or score == "softmax")
+
+
+def test_nan_and_infinity():
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    rng = np.random.default_rng(7)
+    l = _logits(rng, 6, 100, "fp32")
+    l[0, 3] = np.nan
+    l[1] = np.nan
+    l[2, 5] = np.inf
+    l[3, [5, 6]] = np.inf
+    for bias in (None, torch.full((100,), 0.5, device="cuda:0"), torch.full((100,), float("nan"), device="cuda:0")):
+        for score in ("softmax", "sigmoid"):
+            ids, w = mx.mx_topk_router(_dev(l, "fp32"), 8, score=score, bias=bias)
+            got = ids.cpu().numpy()
+            assert ((got >= 0) & (got < 100)).all() and all(len(set(r)) == 8 for r in got.tolist())
+            if score == "softmax":
+                assert torch.isnan(w[0:2]).all()
+            if bias is None:
+                assert got[2, 0] == 5 and got[3, :2].tolist() == [5, 6] and 3 not in got[0]
+            # the other tokens do not notice
+            clean, cw = mx.mx_topk_router(_dev(l[4:], "fp32"), 8, score=score, bias=bias)
+            assert torch.equal(ids[4:], clean) and torch.equal(w[4:], cw)
+
+
+def test_empty_and_given_outputs():
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    ids, w = mx.mx_topk_router(torch.zeros((0, 8), device="cuda:0"), 2)
+    assert tuple(ids.shape) == (0, 2) and tuple(w.shape) == (0, 2)
+    l = torch.randn((5, 24), device="cuda:0")
+    ids, w = torch.empty((5, 4), dtype=torch.int32, device="cuda:0"), torch.empty((5, 4), device="cuda:0")
+    a, b = mx.mx_topk_router_fwd(l, 4, expert_idx=ids, combine=w)
+    assert a is ids and b is w
+    want = torch.topk(torch.softmax(l.double(), 1), 4)
+    assert torch.equal(ids.long(), want.indices)
+    # logits whose rows are not dense reach the kernel as a copy
+    wide = torch.randn((5, 48), device="cuda:0")
+    x, y = mx.mx_topk_router(wide[:, ::2], 4), mx.mx_topk_router(wide[:, ::2].contiguous(), 4)
+    assert all(torch.equal(p, q) for p, q in zip(x, y))
+    with pytest.raises(ValueError, match="contiguous"):
+        mx.mx_topk_router_fwd(wide[:, ::2], 4)
+    with pytest.raises(ValueError):
+        mx.mx_topk_router_fwd(l, 4, bias=torch.zeros(23, device="cuda:0"))
+    for bad in ({"score": "relu"}, {"group_score": "sum"}):
+        with pytest.raises(ValueError):
+            mx.mx_topk_router(l, 4, **bad)
+    for bad in ({"groups": 5}, {"groups": 4, "topk_groups": 5}, {"scale": 0.0}):
+        with pytest.raises(mx.MXError):
+            mx.mx_topk_router(l, 4, **bad)
+    with pytest.raises(mx.MXError):
+        mx.mx_topk_router(l, 25)
+
+
+def test_ids_that_are_not_the_forwards():
+    """Ids out of range add nothing, a repeated one adds up."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    l = torch.randn((2, 70), device="cuda:0")
+    ids = torch.tensor([[3, -1, 70, 1 << 30], [5, 5, 69, 5]], dtype=torch.int32, device="cuda:0")
+    w, dw = torch.rand((2, 4), device="cuda:0"), torch.randn((2, 4), device="cuda:0")
+    dl = mx.mx_topk_router_bwd(l, ids, w, dw, "sigmoid", False)
+    part = (w * (1 - w) * dw).double()
+    want = torch.zeros((2, 70), dtype=torch.float64, device="cuda:0")
+    want[0, 3], want[1, 5], want[1, 69] = part[0, 0], part[1, 0] + part[1, 1] + part[1, 3], part[1, 2]
+    assert (dl.double() - want).abs().max() <= 2.0 ** -20
+
+
+def test_router_in_a_graph_and_on_a_stream():
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    bias = torch.randn(60, device="cuda:0") * 0.05
+    l = torch.randn((9, 60), device="cuda:0", dtype=torch.bfloat16)
+    ids, w = torch.empty((9, 4), dtype=torch.int32, device="cuda:0"), torch.empty((9, 4), device="cuda:0")
+    dw, dl = torch.randn((9, 4), device="cuda:0"), torch.empty_like(l)
+
+    def step():
+        mx.mx_topk_router_fwd(l, 4, "sigmoid", bias, 4, 2, "top2", expert_idx=ids, combine=w)
+        mx.mx_topk_router_bwd(l, ids, w, dw, "sigmoid", dlogits=dl)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(3):
+        l.copy_(torch.randn((9, 60), device="cuda:0"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (ids, w, dl)]
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, (ids, w, dl)))
+
+
+def test_large_batch_is_deterministic():
+    """More tokens than waves: every wave walks several.  Against the same call in pieces."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    l = torch.randn((40001, 32), device="cuda:0", dtype=torch.bfloat16)
+    a = mx.mx_topk_router(l, 8, renormalize=False)
+    parts = [mx.mx_topk_router(p.contiguous(), 8, renormalize=False) for p in l.split(1777)]
+    assert torch.equal(a[0], torch.cat([p[0] for p in parts])) and torch.equal(a[1], torch.cat([p[1] for p in parts]))
+    # a permutation of the tokens permutes the results
+    at = torch.randperm(l.shape[0], device="cuda:0")
+    b = mx.mx_topk_router(l[at], 8, renormalize=False)
+    assert torch.equal(a[0][at], b[0]) and torch.equal(a[1][at], b[1])
