@@ -584,7 +584,8 @@ mx_status mx_swiglu_bwd(const uint16_t* dh, const uint8_t* kept, const uint8_t* 
  * mx_swiglu_quantize_fwd: also q_t [N, ldq] and s_t [ldq/128, N, 4], h times
  * combine[rows[r]] (float [n_items], NULL: 1) in 32x1 blocks along the rows, an
  * operand of the weight gradient's GEMM (columns M..ldq-1: zero codes); and the
- * checkpoint of gu as mx_swiglu_fwd leaves it (rows without an item: of zeros).
+ * checkpoint of gu: kept [M, 2N] as in mx_swiglu_fwd, kept_s in the GEMM layout
+ * [2N/128, M, 4] (rows without an item: of zeros).
  * Requires M % 32 == 0, ldq % 128 == 0, ldq >= M.
  *
  * mx_swiglu_quantize_bwd: dh [M, N] bf16 is the gradient of h without the combine
@@ -596,8 +597,8 @@ mx_status mx_swiglu_bwd(const uint16_t* dh, const uint8_t* kept, const uint8_t* 
  * whose entry of pos is negative get 0.  ws: mx_swiglu_quantize_workspace_bytes(M, N),
  * 256-byte aligned, needs no initialisation.
  *
- * All require N % 128 == 0, n_items < 2^31, fewer than 65535 * 256 rows; gu,
- * dh, kept and codes 16-byte, the rest but kept_s 4-byte aligned. */
+ * All require N % 128 == 0, n_items < 2^31, fewer than 65535 * 128 rows; gu,
+ * dh, kept and codes 16-byte, the rest 4-byte aligned. */
 mx_status mx_swiglu_quantize(const uint16_t* gu, const int32_t* rows, int64_t n_items, int64_t M, int64_t N, uint8_t* q,
                              uint8_t* s, void* stream);
 mx_status mx_swiglu_quantize_fwd(const uint16_t* gu, const int32_t* rows, const float* combine, int64_t n_items,

@@ -1137,13 +1137,13 @@ def _halves(gu):
     return gu.shape[0], gu.shape[1] // 2
 
 
-def _kept(kept, kept_s, M, N):
+def _kept(kept, kept_s, M, N, s_shape):
     import torch
     _require(kept, torch.uint8, "kept")
     _require(kept_s, torch.uint8, "kept_s")
-    if tuple(kept.shape) != (M, 2 * N) or tuple(kept_s.shape) != (M, 2 * N // 32):
-        raise ValueError(f"the checkpoint must be codes {(M, 2 * N)} and scales {(M, 2 * N // 32)}, got "
-                         f"{tuple(kept.shape)} and {tuple(kept_s.shape)}")
+    if tuple(kept.shape) != (M, 2 * N) or tuple(kept_s.shape) != s_shape:
+        raise ValueError(f"the checkpoint must be codes {(M, 2 * N)} and scales {s_shape}, got {tuple(kept.shape)} and "
+                         f"{tuple(kept_s.shape)}")
 
 
 def mx_swiglu_fwd(gu, keep: bool = True, h=None, kept=None, kept_s=None):
@@ -1173,7 +1173,7 @@ def mx_swiglu_bwd(dh, kept, kept_s, dgu=None):
     if dh.dim() != 2:
         raise ValueError("dh must be [M, N]")
     M, N = dh.shape
-    _kept(kept, kept_s, M, N)
+    _kept(kept, kept_s, M, N, (M, 2 * N // 32))
     _same_device(dh, kept, kept_s)
     dev = dh.device
     dgu = _out(dgu, (M, 2 * N), torch.bfloat16, dev, "dgu")
@@ -1235,7 +1235,7 @@ def mx_swiglu_quantize_fwd(gu, rows=None, combine=None, ldq: Optional[int] = Non
       q [M, N], s [N/128, M, 4]         h = silu(gate) * up in 1x32 blocks along N, X of the down product
       q_t [N, ldq], s_t [ldq/128, N, 4] combine[rows[r]] * h in 32x1 blocks along the rows, for the down
                                         weights' gradient (combine fp32, one weight per item; None: 1)
-      kept [M, 2N], kept_s [M, 2N/32]   the checkpoint of gu in MXFP8, for mx_swiglu_quantize_bwd
+      kept [M, 2N], kept_s [2N/128, M, 4]  the checkpoint of gu in MXFP8, for mx_swiglu_quantize_bwd
 
     Rows whose entry of `rows` is negative or past the items count as zeros.  M % 32 == 0, N % 128 == 0; ldq
     defaults to M rounded up to 128."""
@@ -1252,7 +1252,7 @@ def mx_swiglu_quantize_fwd(gu, rows=None, combine=None, ldq: Optional[int] = Non
     q_t = _out(q_t, (N, ldq), torch.uint8, dev, "q_t")
     s_t = _out(s_t, (ldq // 128, N, 4), torch.uint8, dev, "s_t")
     kept = _out(kept, (M, 2 * N), torch.uint8, dev, "kept")
-    kept_s = _out(kept_s, (M, 2 * N // 32), torch.uint8, dev, "kept_s")
+    kept_s = _out(kept_s, (2 * N // 128, M, 4), torch.uint8, dev, "kept_s")
     with _on(dev):
         _check("mx_swiglu_quantize_fwd",
                lib.mx_swiglu_quantize_fwd(_ptr(gu), _ptr(rows), _ptr(combine), n, M, N, ldq, _ptr(q), _ptr(s), _ptr(q_t),
@@ -1277,7 +1277,7 @@ def mx_swiglu_quantize_bwd(dh, kept, kept_s, rows=None, pos=None, combine=None, 
     if dh.dim() != 2:
         raise ValueError("dh must be [M, N]")
     M, N = dh.shape
-    _kept(kept, kept_s, M, N)
+    _kept(kept, kept_s, M, N, (2 * N // 128, M, 4))
     n = _rows_of(dh, rows, combine, M)
     _same_device(dh, kept, kept_s)
     dev = dh.device

@@ -952,7 +952,7 @@ mx_status check_swiglu_tiles(const char* fn, int64_t M, int64_t N, int64_t ldq, 
   if (train && (M % 32 != 0 || ldq % 128 != 0 || ldq < M))
     return fail(MX_ERR_SHAPE, "%s: M=%lld must be a multiple of 32 and ldq=%lld one of 128, >= M", fn, (long long)M,
                 (long long)ldq);
-  if ((train ? ldq : M) / 256 >= 65535) return fail(MX_ERR_SHAPE, "%s: too many rows for one launch", fn);
+  if ((train ? ldq : M) / 128 >= 65535) return fail(MX_ERR_SHAPE, "%s: too many rows for one launch", fn);
   return MX_OK;
 }
 
@@ -1012,8 +1012,8 @@ mx_status mx_swiglu_quantize_fwd(const uint16_t* gu, const int32_t* rows, const 
   if (ldq == 0 || N == 0) return MX_OK;
   if (!q_t || !s_t || (M > 0 && (!gu || !q || !s || !kept || !kept_s))) return fail(MX_ERR_NULL, "%s: null pointer", fn);
   if (!aligned(gu, 16) || !aligned(q, 16) || !aligned(q_t, 16) || !aligned(kept, 16) || !aligned(s, 4) ||
-      !aligned(s_t, 4) || !aligned(rows, 4) || !aligned(combine, 4))
-    return fail(MX_ERR_ALIGN, "%s: gu, q, q_t and kept must be 16-byte, s, s_t, rows and combine 4-byte aligned", fn);
+      !aligned(s_t, 4) || !aligned(kept_s, 4) || !aligned(rows, 4) || !aligned(combine, 4))
+    return fail(MX_ERR_ALIGN, "%s: gu, q, q_t and kept must be 16-byte, the other tensors 4-byte aligned", fn);
   mxk::SwigluArgs a{};
   a.gu = gu;
   a.rows = rows;
@@ -1050,9 +1050,8 @@ mx_status mx_swiglu_quantize_bwd(const uint16_t* dh, const uint8_t* kept, const 
   if (ldq > 0 && N > 0 && (!q_t || !s_t || (M > 0 && (!dh || !kept || !kept_s || !q || !s))))
     return fail(MX_ERR_NULL, "%s: null pointer", fn);
   if (!aligned(dh, 16) || !aligned(kept, 16) || !aligned(q, 16) || !aligned(q_t, 16) || !aligned(s, 4) ||
-      !aligned(s_t, 4) || !aligned(rows, 4) || !aligned(pos, 4) || !aligned(combine, 4) || !aligned(dcombine, 4))
-    return fail(MX_ERR_ALIGN,
-                "%s: dh, kept, q and q_t must be 16-byte, the other tensors but kept_s 4-byte aligned", fn);
+      !aligned(s_t, 4) || !aligned(kept_s, 4) || !aligned(rows, 4) || !aligned(pos, 4) || !aligned(combine, 4) || !aligned(dcombine, 4))
+    return fail(MX_ERR_ALIGN, "%s: dh, kept, q and q_t must be 16-byte, the other tensors 4-byte aligned", fn);
   const size_t need = dcombine ? mx_swiglu_quantize_workspace_bytes(M, N) : 0;
   if (need && (!ws || ws_bytes < need))
     return fail(MX_ERR_WORKSPACE, "%s: workspace of %zu bytes at %p, need %zu", fn, ws_bytes, ws, need);

@@ -146,7 +146,7 @@ struct SwigluArgs {
   const int32_t* pos;         // row of each item, or null
   const float* combine;       // [n_items], or null: 1
   uint8_t* kept;              // [M, 2N] codes
-  uint8_t* kept_s;            // [M, 2N/32]
+  uint8_t* kept_s;            // [2N/128, M, 4]
   uint8_t *q, *s;             // rowwise codes and scales (GEMM layout) of h, or of dgu
   uint8_t *q_t, *s_t;         // colwise ones of w h (null: rowwise alone), or of dgu
   float* partial;             // [N/128, M] (backward), or null

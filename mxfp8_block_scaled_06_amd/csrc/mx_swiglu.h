@@ -31,6 +31,18 @@ __device__ __forceinline__ Sigmoid sigmoid_parts(float x) {
   return s;
 }
 
+// The same for |x| < 80, where nothing leaves fp32's range.
+__device__ __forceinline__ Sigmoid sigmoid_near(float x) {
+  const float y = x * -1.442695041f;
+  const float lo = fmaf(x, -1.925963033e-8f, fmaf(x, -1.442695041f, -y));
+  const float e = __builtin_amdgcn_exp2f(y), p = fmaf(e * lo, 0.6931471806f, e);
+  Sigmoid s;
+  s.m = __builtin_amdgcn_rcpf(1.f + p);
+  s.q = p * s.m;
+  s.far = false;
+  return s;
+}
+
 // a * b where a was computed from s.m.  The 2^-160 is split so that neither factor
 // falls below fp32's range where the product does not.
 __device__ __forceinline__ float scaled(const Sigmoid& s, float a, float b) {
@@ -61,33 +73,6 @@ __device__ __forceinline__ void values4(uint32_t codes, float scale, float* out)
 __device__ __forceinline__ void values8(v2i codes, float scale, float* out) {
   values4((uint32_t)codes[0], scale, out);
   values4((uint32_t)codes[1], scale, out + 4);
-}
-
-// E8M0 byte of a block from the bits of its largest |fp32|.
-__device__ __forceinline__ uint32_t e8m0_from_absbits32(uint32_t amax_bits) {
-  if (amax_bits >= 0x7F800000u) return 0xFFu;
-  const int e = (int)(amax_bits >> 23) - 8;
-  return (uint32_t)(e > 0 ? e : 0);
-}
-
-// Eight fp32 values of a block with scale byte `byte` -> E4M3 codes.
-__device__ __forceinline__ v2i quant8_f32(const float* x, uint32_t byte) {
-  if (byte == 0xFFu) return (v2i){0x7F7F7F7F, 0x7F7F7F7F};
-  const float m = inv_scale_from_e8m0(byte);
-  v2i r;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    int c = cvt2_e4m3<false>(x[4 * i] * m, x[4 * i + 1] * m, 0);
-    r[i] = cvt2_e4m3<true>(x[4 * i + 2] * m, x[4 * i + 3] * m, c);
-  }
-  return r;
-}
-
-__device__ __forceinline__ uint32_t absmax8_f32(const float* x) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  return m;
 }
 
 }  // namespace mxk

@@ -130,61 +130,143 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const uint16_t* __
 }
 
 // ---------------------------------------------------------------------------
-// Between two products of routed experts.  A workgroup of eight waves takes 256
-// rows and 128 columns of h; wave w rows 32w..32w+31, one block of the colwise
-// quantization, lane l rows 32w + 8 (l/16) + i (i < 8) and columns 8 (l%16)..: a
-// quad holds a block of 32 columns, the four lanes l%16, +16, +32, +48 one of 32
-// rows.  Codes of the rows go straight out, 128-byte runs; those of the columns
-// through LDS, 8-byte slots swizzled so that neither side meets a bank conflict,
-// and out as 256-byte runs.  Row r belongs to item rows[r]; a row with none (padding,
+// Between two products of routed experts.  A workgroup of eight waves takes 128
+// rows and 128 columns of h; wave w rows 32 (w/2).., one block of the colwise
+// quantization, and columns 64 (w%2)..; lane l rows 4 (l/8) + i (i < 4) and eight
+// columns 8 (l%8)..: a quad holds a block of 32 columns, the lanes l%8 + 8j one of 32
+// rows.  Codes of the rows go straight out; those of the columns through LDS, and
+// out as whole lines.  Row r belongs to item rows[r]; a row with none (padding,
 // behind the last group) holds anything and counts as zeros.
+//
+// 4 rows a lane instead of 8 hold both of the backward's gradients in fp32 in 128
+// registers, so that two workgroups share a CU and one computes while the other
+// waits for memory.
 // ---------------------------------------------------------------------------
 namespace {
 
-constexpr int kTileRows = 256, kTileCols = 128, kTileThreads = 512;
+constexpr int kTileRows = 128, kTileCols = 128, kTileThreads = 512, kLaneRows = 4;
+constexpr uint32_t kFarGate = 0x4280;       // bf16 bits of 64: below, sigmoid_near serves
+constexpr uint32_t kFarByte = 124;          // a block of this scale byte holds at most 448 * 2^-3 = 56
 
-__device__ __forceinline__ int slot16(int col, int s) { return s ^ (col >> 3 & 15); }
+// Conversions to E4M3 saturate from here on, to +-448 (bit 23 of the MODE register).
+__device__ __forceinline__ void saturate_conversions() { __builtin_amdgcn_s_setreg(1 | (23 << 6), 1); }
 
-struct ColCodes {
-  uint8_t codes[kTileCols * kTileRows];          // [column][row]
-  uint8_t scales[kTileRows / 128 * kTileCols * 4];   // [128 rows][column][block]
+struct Place {
+  int cp, rg, wr, wc, row, col;             // row and col: of the lane's first value within the tile
+  __device__ __forceinline__ Place() {
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    cp = lane & 7;
+    rg = lane >> 3;
+    wr = wv >> 1;
+    wc = wv & 1;
+    row = 32 * wr + kLaneRows * rg;
+    col = 64 * wc + 8 * cp;
+  }
 };
 
-// Colwise codes of the lane's 8 rows x 8 columns x[i][c] into LDS.
-__device__ __forceinline__ void put_columns(ColCodes& lds, const float (&x)[8][8], int wv, int cp, int rg) {
+struct ColCodes {
+  uint8_t codes[kTileCols * kTileRows];     // [column][row], see code_at
+  uint8_t scales[kTileCols * 4];            // [column][block]
+};
+
+// Where 16-byte slot s (16 rows) of a column lies.  Neighbouring groups of eight
+// columns take the halves of a 256-byte line in opposite order, and every second one
+// another slot: the writes of a wave (eight groups x eight lanes of 4 bytes) and the
+// reads (eight slots of eight columns) meet no bank twice.
+__device__ __forceinline__ int code_at(int col, int s) {
+  return (col ^ (col >> 3 & 1)) * kTileRows + 16 * (s ^ (2 * (col >> 4 & 3)));
+}
+
+// Byte of a block whose largest magnitude has these bits (finite), and the scale as
+// the conversions take it: the float whose exponent field is the byte.
+__device__ __forceinline__ uint32_t byte_of(uint32_t bits) { return max(bits >> 23, 8u) - 8u; }
+__device__ __forceinline__ float scale_bits(uint32_t byte) { return __uint_as_float(byte << 23); }
+__device__ __forceinline__ bool not_finite(uint32_t bits) { return bits >= 0x7F800000u; }
+
+__device__ __forceinline__ uint32_t absmax(const float* x, int n, int step) {
+  float m = __builtin_fabsf(x[0]);
+#pragma unroll
+  for (int i = 1; i < n; ++i) m = __builtin_elementwise_maximum(m, __builtin_fabsf(x[i * step]));   // a NaN stays one
+  return __float_as_uint(m);
+}
+
+// Four values -> codes, saturating (see saturate_conversions).
+__device__ __forceinline__ int codes4(float a, float b, float c, float d, float scale) {
+  s16x2 r = {0, 0};
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, scale, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, scale, 1);
+  return __builtin_bit_cast(int, r);
+}
+
+// Eight values of a block spread over a quad -> codes and the block's byte.
+__device__ __forceinline__ v2i quantize_row(const float* x, uint32_t& byte) {
+  const uint32_t bits = quad_max(absmax(x, 8, 1));
+  byte = byte_of(bits);
+  const float scale = scale_bits(byte);
+  v2i q = {codes4(x[0], x[1], x[2], x[3], scale), codes4(x[4], x[5], x[6], x[7], scale)};
+  if (__any(not_finite(bits))) {
+    byte = not_finite(bits) ? 0xFFu : byte;
+    q = not_finite(bits) ? (v2i){0x7F7F7F7F, 0x7F7F7F7F} : q;
+  }
+  return q;
+}
+
+// The same of eight bf16 values, as mx_quantize_rowwise; `bits`: the largest
+// magnitude's.
+__device__ __forceinline__ v2i quantize_row(v4i x, uint32_t& bits, uint32_t& byte) {
+  const us2 m = absmax8x2(x);
+  bits = quad_max(max((uint32_t)m[0], (uint32_t)m[1]));
+  byte = max(bits >> 7, 8u) - 8u;
+  const float scale = scale_bits(byte);
+  v2i q;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    s16x2 r = {0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, (uint32_t)x[2 * i]), scale, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, (uint32_t)x[2 * i + 1]), scale, 1);
+    q[i] = __builtin_bit_cast(int, r);
+  }
+  const bool nan = bits >= 0x7F80u;
+  if (__any(nan)) {
+    byte = nan ? 0xFFu : byte;
+    q = nan ? (v2i){0x7F7F7F7F, 0x7F7F7F7F} : q;
+  }
+  return q;
+}
+
+// Colwise codes of the lane's 4 rows x 8 columns into LDS.
+__device__ __forceinline__ void put_columns(ColCodes& lds, const float (&x)[kLaneRows][8], const Place& p) {
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i][c]) & 0x7FFFFFFFu);
-    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-    const uint32_t byte = e8m0_from_absbits32(m);
-    float col[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) col[i] = x[i][c];
-    const int k = 8 * cp + c, slot = 4 * wv + rg;
-    *(v2i*)(lds.codes + k * kTileRows + 16 * slot16(k, slot >> 1) + 8 * (slot & 1)) = quant8_f32(col, byte);
-    if (rg == 0) lds.scales[(wv >> 2) * (kTileCols * 4) + k * 4 + (wv & 3)] = (uint8_t)byte;
+    uint32_t m = absmax(&x[0][c], kLaneRows, 8);
+    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x128, 0xF, 0xF, false));     // lanes 8 apart (row_ror:8)
+    const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);                 // 16
+    m = max(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);                 // 32
+    m = max(b[0], b[1]);
+    uint32_t byte = byte_of(m);
+    int q = codes4(x[0][c], x[1][c], x[2][c], x[3][c], scale_bits(byte));
+    if (__any(not_finite(m))) {
+      byte = not_finite(m) ? 0xFFu : byte;
+      q = not_finite(m) ? 0x7F7F7F7F : q;
+    }
+    const int k = p.col + c;
+    *(int*)(lds.codes + code_at(k, p.row >> 4) + (p.row & 15)) = q;
+    if (p.rg == 0) lds.scales[k * 4 + p.wr] = (uint8_t)byte;
   }
 }
 
 // ... and from there to columns k0.. of q_t [., ldq] and s_t [ldq/128][cols][4].
 __device__ __forceinline__ void store_columns(const ColCodes& lds, int64_t n0, int64_t k0, int64_t cols, int64_t ldq,
                                               uint8_t* __restrict__ q_t, uint8_t* __restrict__ s_t) {
-  const int tid = threadIdx.x, s = tid & 15;
+  const int tid = threadIdx.x, s = tid & 7;
 #pragma unroll
-  for (int it = 0; it < kTileCols * 16 / kTileThreads; ++it) {
-    const int k = (tid >> 4) + kTileThreads / 16 * it;
-    const v4i x = *(const v4i*)(lds.codes + k * kTileRows + 16 * slot16(k, s));
-    if (n0 + 16 * s < ldq) *(v4i*)(q_t + (k0 + k) * ldq + n0 + 16 * s) = x;
+  for (int it = 0; it < kTileCols * 8 / kTileThreads; ++it) {
+    const int k = (tid >> 3) + kTileThreads / 8 * it;
+    *(v4i*)(q_t + (k0 + k) * ldq + n0 + 16 * s) = *(const v4i*)(lds.codes + code_at(k, s));
   }
-  if (tid < 2 * kTileCols) {
-    const int ch = tid / kTileCols, k = tid % kTileCols;
-    if (n0 + 128 * ch < ldq)
-      *(uint32_t*)(s_t + ((n0 >> 7) + ch) * cols * 4 + (k0 + k) * 4) =
-          *(const uint32_t*)(lds.scales + ch * (kTileCols * 4) + k * 4);
-  }
+  if (tid < kTileCols)
+    *(uint32_t*)(s_t + (n0 >> 7) * cols * 4 + (k0 + tid) * 4) = *(const uint32_t*)(lds.scales + tid * 4);
 }
 
 // Item of row r, or -1.
@@ -197,155 +279,205 @@ __device__ __forceinline__ int item_of(const SwigluArgs& a, int64_t r) {
 }  // namespace
 
 template <bool TRAIN>
-__global__ __launch_bounds__(kTileThreads) void swiglu_quantize_fwd_kernel(SwigluArgs a) {
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4))) void swiglu_quantize_fwd_kernel(
+    SwigluArgs a) {
   __shared__ __attribute__((aligned(16))) ColCodes lds;
-  __shared__ __attribute__((aligned(16))) uint8_t srow[kTileRows * 4];
-  const int tid = threadIdx.x, wv = tid >> 6, lane = tid & 63, cp = lane & 15, rg = lane >> 4;
+  __shared__ __attribute__((aligned(16))) uint8_t srow[3][kTileRows * 4];
+  const Place p;
+  const int tid = threadIdx.x, blk = 2 * p.wc + (p.cp >> 2);
   const int64_t n0 = (int64_t)blockIdx.y * kTileRows, k0 = (int64_t)blockIdx.x * kTileCols;
-  const int r0 = 32 * wv + 8 * rg;
-  int item[8];
+  const int64_t r0 = n0 + p.row, c0 = k0 + p.col;
+  saturate_conversions();
+  int item[kLaneRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) item[i] = item_of(a, n0 + r0 + i);
-  v4i gw[8], uw[8];
+  for (int i = 0; i < kLaneRows; ++i) item[i] = item_of(a, r0 + i);
+  v4i gw[kLaneRows], uw[kLaneRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kLaneRows; ++i) {
     gw[i] = uw[i] = (v4i){0, 0, 0, 0};
     if (item[i] >= 0) {
-      const uint16_t* src = a.gu + (n0 + r0 + i) * 2 * a.N + k0 + 8 * cp;
+      const uint16_t* src = a.gu + (r0 + i) * 2 * a.N + c0;
       gw[i] = __builtin_nontemporal_load((const v4i*)src);
       uw[i] = __builtin_nontemporal_load((const v4i*)(src + a.N));
     }
   }
-  float h[8][8];
+  float w[kLaneRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = n0 + r0 + i;
+  for (int i = 0; i < kLaneRows && TRAIN; ++i) w[i] = item[i] < 0 ? 0.f : a.combine ? a.combine[item[i]] : 1.f;
+  float h[kLaneRows][8];
+#pragma unroll
+  for (int i = 0; i < kLaneRows; ++i) {
+    const int64_t r = r0 + i;
     float g[8], u[8];
     floats8(gw[i], g);
     floats8(uw[i], u);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) h[i][c] = silu_mul(g[c], u[c]);
-    const uint32_t byte = e8m0_from_absbits32(quad_max(absmax8_f32(h[i])));
-    const v2i q = quant8_f32(h[i], byte);
-    if (r < a.M) *(v2i*)(a.q + r * a.N + k0 + 8 * cp) = q;
-    if ((cp & 3) == 0) srow[(r0 + i) * 4 + (cp >> 2)] = (uint8_t)byte;
+    uint32_t bits;
     if (TRAIN) {
-      uint32_t gb, ub;
-      const v2i gq = quantize_quad(gw[i], gb), uq = quantize_quad(uw[i], ub);
+      uint32_t gb, ub, other;
+      const v2i gq = quantize_row(gw[i], bits, gb), uq = quantize_row(uw[i], other, ub);
       if (r < a.M) {
-        uint8_t* dst = a.kept + r * 2 * a.N + k0 + 8 * cp;
+        uint8_t* dst = a.kept + r * 2 * a.N + c0;
         *(v2i*)dst = gq;
         *(v2i*)(dst + a.N) = uq;
-        if ((cp & 3) == 0) {
-          uint8_t* s = a.kept_s + r * (a.N / 16) + ((k0 + 8 * cp) >> 5);
-          s[0] = (uint8_t)gb;
-          s[a.N / 32] = (uint8_t)ub;
-        }
       }
-      const float w = item[i] < 0 ? 0.f : a.combine ? a.combine[item[i]] : 1.f;
+      if ((p.cp & 3) == 0) {
+        srow[1][(p.row + i) * 4 + blk] = (uint8_t)gb;
+        srow[2][(p.row + i) * 4 + blk] = (uint8_t)ub;
+      }
+    } else {
+      const us2 m = absmax8x2(gw[i]);
+      bits = max((uint32_t)m[0], (uint32_t)m[1]);
+    }
+    if (__any(bits >= kFarGate)) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) h[i][c] *= w;
+      for (int c = 0; c < 8; ++c) h[i][c] = silu_mul(g[c], u[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) h[i][c] = g[c] * sigmoid_near(g[c]).m * u[c];
+    }
+    uint32_t byte;
+    const v2i q = quantize_row(h[i], byte);
+    if (r < a.M) *(v2i*)(a.q + r * a.N + c0) = q;
+    if ((p.cp & 3) == 0) srow[0][(p.row + i) * 4 + blk] = (uint8_t)byte;
+#pragma unroll
+    for (int c = 0; c < 8 && TRAIN; ++c) h[i][c] *= w[i];
+  }
+  if (TRAIN) put_columns(lds, h, p);
+  __syncthreads();
+  {
+    const int part = tid / kTileRows, r = tid % kTileRows;      // scales of h, of the gate and of the up values
+    if (part < (TRAIN ? 3 : 1) && n0 + r < a.M) {
+      uint8_t* s = part == 0 ? a.s : a.kept_s + (part == 2 ? a.N >> 7 : 0) * a.M * 4;
+      *(uint32_t*)(s + (k0 >> 7) * a.M * 4 + (n0 + r) * 4) = *(const uint32_t*)(srow[part] + r * 4);
     }
   }
-  if (TRAIN) put_columns(lds, h, wv, cp, rg);
-  __syncthreads();
-  if (tid < kTileRows && n0 + tid < a.M)
-    *(uint32_t*)(a.s + (k0 >> 7) * a.M * 4 + (n0 + tid) * 4) = *(const uint32_t*)(srow + tid * 4);
   if (TRAIN) store_columns(lds, n0, k0, a.N, a.ldq, a.q_t, a.s_t);
 }
 
-__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void swiglu_quantize_bwd_kernel(
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4))) void swiglu_quantize_bwd_kernel(
     SwigluArgs a) {
   __shared__ __attribute__((aligned(16))) ColCodes lds[2];
   __shared__ __attribute__((aligned(16))) uint8_t srow[2][kTileRows * 4];
-  const int tid = threadIdx.x, wv = tid >> 6, lane = tid & 63, cp = lane & 15, rg = lane >> 4;
+  __shared__ float dots[2][kTileRows];
+  const Place p;
+  const int tid = threadIdx.x, blk = 2 * p.wc + (p.cp >> 2);
   const int64_t n0 = (int64_t)blockIdx.y * kTileRows, k0 = (int64_t)blockIdx.x * kTileCols;
-  const int r0 = 32 * wv + 8 * rg;
-  int item[8];
+  const int64_t r0 = n0 + p.row, c0 = k0 + p.col;
+  saturate_conversions();
+  int item[kLaneRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) item[i] = item_of(a, n0 + r0 + i);
-  v4i dw[8];
-  v2i gq[8], uq[8];
-  uint32_t gb[8], ub[8];
+  for (int i = 0; i < kLaneRows; ++i) item[i] = item_of(a, r0 + i);
+  v4i dw[kLaneRows];
+  v2i gq[kLaneRows], uq[kLaneRows];
+  uint32_t gs[kLaneRows], us[kLaneRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = n0 + r0 + i;
+  for (int i = 0; i < kLaneRows; ++i) {
+    const int64_t r = r0 + i;
     dw[i] = (v4i){0, 0, 0, 0};
     gq[i] = uq[i] = (v2i){0, 0};
-    gb[i] = ub[i] = 0;
+    gs[i] = us[i] = 0;
     if (item[i] >= 0) {
-      dw[i] = __builtin_nontemporal_load((const v4i*)(a.dh + r * a.N + k0 + 8 * cp));
-      const uint8_t* src = a.kept + r * 2 * a.N + k0 + 8 * cp;
+      dw[i] = __builtin_nontemporal_load((const v4i*)(a.dh + r * a.N + c0));
+      const uint8_t* src = a.kept + r * 2 * a.N + c0;
       gq[i] = __builtin_nontemporal_load((const v2i*)src);
       uq[i] = __builtin_nontemporal_load((const v2i*)(src + a.N));
-      const uint8_t* s = a.kept_s + r * (a.N / 16) + ((k0 + 8 * cp) >> 5);
-      gb[i] = s[0];
-      ub[i] = s[a.N / 32];
+      const uint8_t* s = a.kept_s + (k0 >> 7) * a.M * 4 + r * 4;
+      gs[i] = *(const uint32_t*)s;
+      us[i] = *(const uint32_t*)(s + (a.N >> 7) * a.M * 4);
     }
   }
-  float dg[8][8], du[8][8];
+  float w[kLaneRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = n0 + r0 + i;
-    const float w = item[i] < 0 ? 0.f : a.combine ? a.combine[item[i]] : 1.f;
+  for (int i = 0; i < kLaneRows; ++i) w[i] = item[i] < 0 ? 0.f : a.combine ? a.combine[item[i]] : 1.f;
+  float dg[kLaneRows][8], du[kLaneRows][8];
+#pragma unroll
+  for (int i = 0; i < kLaneRows; ++i) {
+    const int64_t r = r0 + i;
+    const uint32_t gb = gs[i] >> (8 * blk) & 0xFFu, ub = us[i] >> (8 * blk) & 0xFFu;
     float d[8], g[8], u[8];
     floats8(dw[i], d);
-    values8(gq[i], scale_from_e8m0(gb[i]), g);
-    values8(uq[i], scale_from_e8m0(ub[i]), u);
-    float dot = 0.f;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const Sigmoid s = sigmoid_parts(g[c]);
-      const float e = w * d[c], gs = g[c] * s.m;
-      dg[i][c] = scaled(s, s.m * fmaf(g[c], s.q, 1.f), e * u[c]);
-      du[i][c] = scaled(s, gs, e);
-      dot = fmaf(d[c], scaled(s, gs, u[c]), dot);
+    for (int c = 0; c < 4; ++c) {
+      const v2f x = c & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)gq[i][c >> 1], scale_bits(gb), true)
+                          : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)gq[i][c >> 1], scale_bits(gb), false);
+      const v2f y = c & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)uq[i][c >> 1], scale_bits(ub), true)
+                          : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)uq[i][c >> 1], scale_bits(ub), false);
+      g[2 * c] = x[0];
+      g[2 * c + 1] = x[1];
+      u[2 * c] = y[0];
+      u[2 * c + 1] = y[1];
+    }
+    float dot = 0.f;
+    if (__any(gb > kFarByte || ub == 0xFFu)) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float x = gb == 0xFFu ? __builtin_nanf("") : g[c], y = ub == 0xFFu ? __builtin_nanf("") : u[c];
+        const Sigmoid s = sigmoid_parts(x);
+        const float e = w[i] * d[c], xs = x * s.m;
+        dg[i][c] = scaled(s, s.m * fmaf(x, s.q, 1.f), e * y);
+        du[i][c] = scaled(s, xs, e);
+        dot = fmaf(d[c], scaled(s, xs, y), dot);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const Sigmoid s = sigmoid_near(g[c]);
+        const float e = w[i] * d[c], xs = g[c] * s.m;
+        dg[i][c] = s.m * fmaf(g[c], s.q, 1.f) * (e * u[c]);
+        du[i][c] = xs * e;
+        dot = fmaf(d[c], xs * u[c], dot);
+      }
     }
     if (a.partial) {
-      // over the 16 lanes of a row
-      auto add = [&](int v) __attribute__((always_inline)) { dot += __int_as_float(v); };
-      add(__builtin_amdgcn_mov_dpp(__float_as_int(dot), 0x128, 0xF, 0xF, false));    // row_ror:8, :4
-      add(__builtin_amdgcn_mov_dpp(__float_as_int(dot), 0x124, 0xF, 0xF, false));
-      add(__builtin_amdgcn_mov_dpp(__float_as_int(dot), 0x4E, 0xF, 0xF, false));     // quad [2,3,0,1], [1,0,3,2]
-      add(__builtin_amdgcn_mov_dpp(__float_as_int(dot), 0xB1, 0xF, 0xF, false));
-      if (cp == 0 && r < a.M) a.partial[(int64_t)blockIdx.x * a.M + r] = dot;
+      // over the eight lanes of a row
+      dot += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(dot), 0x141, 0xF, 0xF, false));   // half mirror
+      dot += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(dot), 0x4E, 0xF, 0xF, false));    // quad [2,3,0,1]
+      dot += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(dot), 0xB1, 0xF, 0xF, false));    // quad [1,0,3,2]
+      if (p.cp == 0) dots[p.wc][p.row + i] = dot;
     }
-    const uint32_t bg = e8m0_from_absbits32(quad_max(absmax8_f32(dg[i])));
-    const uint32_t bu = e8m0_from_absbits32(quad_max(absmax8_f32(du[i])));
-    const v2i qg = quant8_f32(dg[i], bg), qu = quant8_f32(du[i], bu);
+    uint32_t bg, bu;
+    const v2i qg = quantize_row(dg[i], bg), qu = quantize_row(du[i], bu);
     if (r < a.M) {
-      uint8_t* dst = a.q + r * 2 * a.N + k0 + 8 * cp;
+      uint8_t* dst = a.q + r * 2 * a.N + c0;
       *(v2i*)dst = qg;
       *(v2i*)(dst + a.N) = qu;
     }
-    if ((cp & 3) == 0) {
-      srow[0][(r0 + i) * 4 + (cp >> 2)] = (uint8_t)bg;
-      srow[1][(r0 + i) * 4 + (cp >> 2)] = (uint8_t)bu;
+    if ((p.cp & 3) == 0) {
+      srow[0][(p.row + i) * 4 + blk] = (uint8_t)bg;
+      srow[1][(p.row + i) * 4 + blk] = (uint8_t)bu;
     }
   }
-  put_columns(lds[0], dg, wv, cp, rg);
-  put_columns(lds[1], du, wv, cp, rg);
+  put_columns(lds[0], dg, p);
+  put_columns(lds[1], du, p);
   __syncthreads();
   {
-    const int half = tid / kTileRows, r = tid % kTileRows;
-    if (n0 + r < a.M)
-      *(uint32_t*)(a.s + ((half * a.N + k0) >> 7) * a.M * 4 + (n0 + r) * 4) = *(const uint32_t*)(srow[half] + r * 4);
+    const int part = tid / kTileRows, r = tid % kTileRows;      // scales of dg and of du, sums of the rows
+    if (part < 2 && n0 + r < a.M)
+      *(uint32_t*)(a.s + ((part * a.N + k0) >> 7) * a.M * 4 + (n0 + r) * 4) = *(const uint32_t*)(srow[part] + r * 4);
+    if (part == 2 && a.partial && n0 + r < a.M) a.partial[(int64_t)blockIdx.x * a.M + n0 + r] = dots[0][r] + dots[1][r];
   }
   store_columns(lds[0], n0, k0, 2 * a.N, a.ldq, a.q_t, a.s_t);
   store_columns(lds[1], n0, a.N + k0, 2 * a.N, a.ldq, a.q_t, a.s_t);
 }
 
-// dcombine[rows[r]] = sum over the column tiles of row r, in their order; items
-// without a row get 0.
+// dcombine[rows[r]] = sum over the column tiles of row r, in a fixed order; items
+// without a row get 0.  64 rows per workgroup, every fourth tile per wave.
 __global__ __launch_bounds__(kThreads) void swiglu_dcombine_kernel(SwigluArgs a, float* __restrict__ dcombine) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i < a.n_items && a.pos && a.pos[i] < 0) dcombine[i] = 0.f;
-  if (i >= a.M) return;
-  const int item = item_of(a, i);
-  if (item < 0) return;
+  __shared__ float part[kThreads];
+  const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t r = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t tiles = a.N / kTileCols;
   float sum = 0.f;
-  for (int64_t t = 0; t < a.N / kTileCols; ++t) sum += a.partial[t * a.M + i];
-  dcombine[item] = sum;
+  if (r < a.M) {
+#pragma unroll 8
+    for (int64_t t = wv; t < tiles; t += 4) sum += a.partial[t * a.M + r];
+  }
+  part[threadIdx.x] = sum;
+  __syncthreads();
+  if (wv != 0) return;
+  if (r < a.n_items && a.pos && a.pos[r] < 0) dcombine[r] = 0.f;
+  const int item = item_of(a, r);
+  if (item >= 0) dcombine[item] = part[lane] + part[64 + lane] + part[128 + lane] + part[192 + lane];
 }
 
 // ---------------------------------------------------------------------------
@@ -392,8 +524,7 @@ hipError_t launch_swiglu_quantize_bwd(const SwigluArgs& a, float* dcombine, hipS
   }
   const int64_t n = a.M > a.n_items ? a.M : a.n_items;
   if (!dcombine || n == 0) return hipSuccess;
-  hipLaunchKernelGGL(swiglu_dcombine_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, a,
-                     dcombine);
+  hipLaunchKernelGGL(swiglu_dcombine_kernel, dim3((unsigned)((n + 63) / 64)), dim3(kThreads), 0, st, a, dcombine);
   return hipGetLastError();
 }
 

@@ -59,7 +59,7 @@ def test_activation_refusals():
     q = lib.mx_swiglu_quantize
     assert q(P, None, 0, 4, 64, P, P, None) == SHAPE and "128" in _err(lib)
     assert q(P, P, -1, 4, 128, P, P, None) == SHAPE and q(P, P, 1 << 31, 4, 128, P, P, None) == SHAPE
-    assert q(P, P, 4, 1 << 24, 128, P, P, None) == SHAPE and "rows" in _err(lib)
+    assert q(P, P, 4, 1 << 23, 128, P, P, None) == SHAPE and "rows" in _err(lib)
     assert q(P, P, 4, 4, 128, None, P, None) == NULL and q(P, P, 4, 4, 128, P, P + 2, None) == ALIGN
 
 
