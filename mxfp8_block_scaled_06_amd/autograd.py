@@ -37,12 +37,11 @@ from __future__ import annotations
 
 import weakref
 
-from . import (_format, _on, mx_grouped_gemm_mx, mx_grouped_gemm_mx_rows, mx_grouped_gemm_mxfp4,
-               mx_grouped_mm_dgrad_fp4, mx_grouped_mm_dgrad_q, mx_grouped_mm_fwd_fp4, mx_grouped_mm_fwd_q,
-               mx_quantize_dual, mx_quantize_dual_gather, mx_quantize_rowwise_gather, mx_quantize_weights,
-               mx_quantize_weights_fp4, mx_route, mx_swiglu_bwd, mx_swiglu_fwd, mx_swiglu_quantize,
-               mx_swiglu_quantize_bwd, mx_swiglu_quantize_fwd, mx_topk_combine_bwd, mx_topk_combine_fwd,
-               mx_topk_router_bwd, mx_topk_router_fwd, mx_topk_sum_rows)
+from . import (SCORES, _check as _check_status, _format, _on, _ptr, _stream, load_library, mx_grouped_gemm_mx,
+               mx_grouped_gemm_mx_rows, mx_grouped_gemm_mxfp4, mx_grouped_mm_dgrad_fp4, mx_grouped_mm_dgrad_q,
+               mx_grouped_mm_fwd_fp4, mx_grouped_mm_fwd_q, mx_quantize_dual, mx_quantize_dual_gather,
+               mx_quantize_rowwise_gather, mx_quantize_weights, mx_quantize_weights_fp4, mx_route, mx_swiglu_fwd, mx_swiglu_quantize, mx_swiglu_quantize_bwd,
+               mx_swiglu_quantize_fwd, mx_topk_combine_fwd, mx_topk_router_fwd, mx_topk_sum_rows)
 
 
 class WeightCache:
@@ -369,6 +368,26 @@ def _wants_grad(*tensors):
     return torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
 
 
+def _first_order(backward):
+    """A backward without one of its own: under create_graph=True its results refuse to be
+    differentiated.  torch's decorator for that costs 4 us a call, so it is left out where no
+    graph is made."""
+    import torch
+    refusing = torch.autograd.function.once_differentiable(backward)
+
+    def call(ctx, *grads):
+        return refusing(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+
+    return staticmethod(call)
+
+
+# The backwards of the router, the activation and the weighted sum call the C ABI themselves: what
+# they pass was checked in the forward or made by it, autograd gives gradients of the outputs' shape,
+# type and device and makes that device current, and its thread runs 16 us longer through the binding's
+# checks (Python objects that the main thread has just used: 100 us for a router's forward and backward
+# instead of 72).
+
+
 class _MXRouter:
     """torch.autograd.Function of mx_topk_router (built lazily)."""
     fn = None
@@ -380,21 +399,29 @@ class _MXRouter:
 
             class Fn(torch.autograd.Function):
                 @staticmethod
-                def forward(ctx, logits, bias, k, score, groups, topk_groups, group_score, renormalize, scale):
-                    expert_idx, combine = mx_topk_router_fwd(logits, k, score, bias, groups, topk_groups, group_score,
-                                                             renormalize, scale)
+                def forward(ctx, logits, options):
+                    expert_idx, combine = mx_topk_router_fwd(logits, *options)
                     ctx.mark_non_differentiable(expert_idx)
+                    ctx.set_materialize_grads(False)       # no zeros in the place of a gradient of the ids
                     ctx.save_for_backward(logits, expert_idx, combine)
-                    ctx.score, ctx.renormalize, ctx.scale = score, renormalize, scale
+                    ctx.options = options
                     return expert_idx, combine
 
-                @staticmethod
-                @torch.autograd.function.once_differentiable
+                @_first_order
                 def backward(ctx, _, dcombine):
+                    if dcombine is None:
+                        return None, None
                     logits, expert_idx, combine = ctx.saved_tensors
-                    dlogits = mx_topk_router_bwd(logits, expert_idx, combine, dcombine.contiguous(), ctx.score,
-                                                 ctx.renormalize, ctx.scale)
-                    return dlogits, None, None, None, None, None, None, None, None
+                    k, score, _, _, _, _, renormalize, scale = ctx.options
+                    T, E = logits.shape
+                    dlogits, dcombine = torch.empty_like(logits), dcombine.contiguous()
+                    status = load_library().mx_topk_router_bwd(
+                        logits.data_ptr(), logits.dtype == torch.float32, expert_idx.data_ptr(), combine.data_ptr(),
+                        dcombine.data_ptr(), T, E, k, SCORES[score], renormalize, scale, dlogits.data_ptr(),
+                        _stream(logits.device))
+                    if status:
+                        _check_status("mx_topk_router_bwd", status)
+                    return dlogits, None
 
             cls.fn = Fn
         return cls.fn
@@ -411,7 +438,7 @@ def mx_topk_router(logits, k, score="softmax", bias=None, groups=1, topk_groups=
                          "gradient: pass bias.detach()")
     if not _wants_grad(logits):
         return mx_topk_router_fwd(logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale)
-    return _MXRouter.get().apply(logits, bias, k, score, groups, topk_groups, group_score, renormalize, scale)
+    return _MXRouter.get().apply(logits, (k, score, bias, groups, topk_groups, group_score, renormalize, scale))
 
 
 class _MXSwiglu:
@@ -430,10 +457,16 @@ class _MXSwiglu:
                     ctx.save_for_backward(kept, kept_s)
                     return h
 
-                @staticmethod
-                @torch.autograd.function.once_differentiable
+                @_first_order
                 def backward(ctx, dh):
-                    return mx_swiglu_bwd(dh.contiguous(), *ctx.saved_tensors)
+                    kept, kept_s = ctx.saved_tensors
+                    M, N = dh.shape
+                    dh, dgu = dh.contiguous(), torch.empty((M, 2 * N), dtype=torch.bfloat16, device=dh.device)
+                    status = load_library().mx_swiglu_bwd(dh.data_ptr(), kept.data_ptr(), kept_s.data_ptr(), M, N,
+                                                          dgu.data_ptr(), _stream(dh.device))
+                    if status:
+                        _check_status("mx_swiglu_bwd", status)
+                    return dgu
 
             cls.fn = Fn
         return cls.fn
@@ -462,12 +495,19 @@ class _MXCombine:
                     ctx.save_for_backward(y, combine, pos)
                     return mx_topk_combine_fwd(y, combine, pos)
 
-                @staticmethod
-                @torch.autograd.function.once_differentiable
+                @_first_order
                 def backward(ctx, dout):
                     y, combine, pos = ctx.saved_tensors
-                    dy, dcombine = mx_topk_combine_bwd(dout.contiguous(), y, combine, pos, ctx.needs_input_grad[0],
-                                                       ctx.needs_input_grad[1])
+                    T, k, N = y.shape
+                    need_y, need_c, _ = ctx.needs_input_grad
+                    dout = dout.contiguous()
+                    dy = torch.empty_like(y) if need_y else None
+                    dcombine = torch.empty_like(combine) if need_c else None
+                    status = load_library().mx_topk_combine_bwd(
+                        y.data_ptr(), y.dtype == torch.float32, combine.data_ptr(), _ptr(pos),
+                        dout.data_ptr(), T, k, N, _ptr(dy), _ptr(dcombine), _stream(y.device))
+                    if status:
+                        _check_status("mx_topk_combine_bwd", status)
                     return dy, dcombine, None
 
             cls.fn = Fn
@@ -513,11 +553,11 @@ class _MXLayer:
                     if not ctx.needs_input_grad[3]:
                         qht = sht = None
                     ctx.zero_fill, ctx.weight_format = zero_fill, weight_format
-                    ctx.save_for_backward(combine, offs, rows, pos, q13t, s13t, q2t, s2t, qxt, sxt, qht, sht, kept, kept_s)
+                    ctx.save_for_backward(combine, offs, rows, pos, q13t, s13t, q2t, s2t, qxt, sxt, qht, sht, kept,
+                                          kept_s)
                     return out
 
-                @staticmethod
-                @torch.autograd.function.once_differentiable
+                @_first_order
                 def backward(ctx, dout):
                     (combine, offs, rows, pos, q13t, s13t, q2t, s2t, qxt, sxt, qht, sht, kept,
                      kept_s) = ctx.saved_tensors
@@ -596,7 +636,7 @@ def mx_moe_layer(x, expert_idx, combine, W13, W2, check: bool = True, weights=No
     combine = combine.reshape(T, topk).contiguous()
     if T == 0:
         # no token, and zeros for the weights' gradients
-        return x * 1 + 0 * (W13.sum() + W2.sum() + combine.sum()).to(x.dtype) if _wants_grad(x, combine, W13, W2) else x.clone()
+        return x + (combine.sum() + W13[:0].sum() + W2[:0].sum()).to(x.dtype)
     with _on(x.device):
         offs, rows, pos, status = mx_route(expert_idx.contiguous().reshape(-1), E)
         if check and int(status.item()):
