@@ -17,10 +17,17 @@
 // two, c is computed in fp64: at fp32's 2^-24, one token in some thousand would
 // have two experts (of 256) out of order.
 //
-// One wave per token, expert v * 64 + lane in register v of a lane: every load
-// is a run of whole lines, and an expert's number follows from where it is
-// found.  An arg-max is a reduction over the lanes by DPP and one ballot per
-// register.  Nothing goes through LDS or memory.
+// router_pick_kernel serves every choice whose groups lie along lanes: L lanes per
+// token, each with V consecutive experts in registers, several tokens per wave.  A
+// lane sorts its experts once, as 32-bit keys (what the expert lacks to the best one,
+// and its index below): then one pick is a maximum over the lanes' first keys (DPP)
+// and a shift in the lane that had it.  The keys hold the logits of bf16 exactly; the
+// differences of fp32 logits and of computed scores they hold to 2^-14 of themselves
+// or better, so two picks that follow each other are only taken for ordered where
+// their keys are further apart than that and the error of the fp32 scores; a wave
+// with a token where they are not (random logits: one in some hundred) does its choice
+// again in fp64.  router_walk_kernel takes other groups: one wave per token, expert v *
+// 64 + lane in register v, an arg-max per pick over all registers, c in fp64.
 #include <type_traits>
 
 #include "mx_device.h"
@@ -31,6 +38,7 @@ namespace mxk {
 namespace {
 
 constexpr int kRouterWaves = 4;
+constexpr int kBwdCells = 512;       // logits that a wave of the backward takes (one token at least)
 
 __device__ __forceinline__ float lane_value(float x, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
@@ -95,9 +103,9 @@ struct Logits<uint16_t> {
   static constexpr float lowest = -3.389531390e38f;
 };
 
-// exp(x) for x <= 0: the hardware's 2^y of x / ln 2 in two parts, off by about
+// exp(x) for x < 88: the hardware's 2^y of x / ln 2 in two parts, off by about
 // 2^-23 of the result at any x.
-__device__ __forceinline__ float exp_neg(float x) {
+__device__ __forceinline__ float exp32(float x) {
   const float y = x * 1.442695041f;
   const float lo = fmaf(x, 1.925963033e-8f, fmaf(x, 1.442695041f, -y));
   const float p = __builtin_amdgcn_exp2f(y);
@@ -105,15 +113,389 @@ __device__ __forceinline__ float exp_neg(float x) {
 }
 
 __device__ __forceinline__ float sigmoid(float x) {
-  const float e = exp_neg(-fabsf(x));
+  const float e = exp32(-fabsf(x));
   return (x < 0.f ? e : 1.f) / (1.f + e);
 }
 
+// Over the L lanes of a token (L = 8 .. 64), in every one of them.
+template <int L, class F>
+__device__ __forceinline__ uint32_t over_lanes(uint32_t x, F f) {
+  x = f(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, false));      // lanes 1, then 2 apart
+  x = f(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, false));
+  x = f(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x141, 0xF, 0xF, false));     // the other half of 8, of 16
+  if (L >= 16) x = f(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x140, 0xF, 0xF, false));
+  if (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = f(r[0], r[1]);
+  }
+  if (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = f(r[0], r[1]);
+  }
+  return x;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
+  return over_lanes<L>(x, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float x) {
+  return __uint_as_float(over_lanes<L>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+  return __uint_as_float(over_lanes<L>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+
+// Descending sort of V keys in registers (odd-even merges).
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t hi = max(k[i + j], k[i + j + q]);
+            k[i + j + q] = min(k[i + j], k[i + j + q]);
+            k[i + j] = hi;
+          }
+}
+
+// V consecutive logits of a token from expert `e0` on; -inf past E.
+template <int V>
+__device__ __forceinline__ void load_logits(const float* row, int e0, int E, float (&l)[V]) {
+  if (E % 4 == 0) {
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+      typedef float v4f __attribute__((ext_vector_type(4)));
+      v4f x = {0.f, 0.f, 0.f, 0.f};
+      const bool in = e0 + v < E;
+      if (in) x = *(const v4f*)(row + e0 + v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[v + i] = in ? x[i] : -__builtin_inff();
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = e0 + v < E ? row[e0 + v] : -__builtin_inff();
+  }
+}
+template <int V>
+__device__ __forceinline__ void load_logits(const uint16_t* row, int e0, int E, float (&l)[V]) {
+  if (E % 4 == 0) {
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+      v2i x = {0, 0};
+      const bool in = e0 + v < E;
+      if (in) x = *(const v2i*)(row + e0 + v);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[v + 2 * i] = in ? bf16lo((uint32_t)x[i]) : -__builtin_inff();
+        l[v + 2 * i + 1] = in ? bf16hi((uint32_t)x[i]) : -__builtin_inff();
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = e0 + v < E ? Logits<uint16_t>::load(row + e0 + v) : -__builtin_inff();
+  }
+}
+
+__device__ __forceinline__ void store4(float* p, const float* x) {
+  typedef float v4f __attribute__((ext_vector_type(4)));
+  *(v4f*)p = (v4f){x[0], x[1], x[2], x[3]};
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float* x) {
+  *(v2i*)p = (v2i){(int)pack_bf16x2_rne(x[0], x[1]), (int)pack_bf16x2_rne(x[2], x[3])};
+}
+
+// How the picks compare.
+constexpr int kExact = 0, kLogits = 1, kValues = 2;     // bf16 logits, fp32 logits, scores with bias or sums of two
+
 }  // namespace
+
+template <int L, int V, class T, int BY>
+__global__ __launch_bounds__(kRouterWaves * 64) void router_pick_kernel(const T* __restrict__ logits,
+                                                                        const float* __restrict__ bias, RouterArgs a) {
+  constexpr int kSlots = MX_MOE_MAX_TOPK / L ? MX_MOE_MAX_TOPK / L : 1;      // slots a lane holds
+  constexpr float kInf = __builtin_inff();
+  const int sub = threadIdx.x % L;
+  const int64_t token = (int64_t)blockIdx.x * (kRouterWaves * 64 / L) + threadIdx.x / L;
+  const int64_t t = min(token, a.T - 1);
+  const T* row = logits + t * a.E;
+  const int e0 = sub * V;
+  float l[V];
+  load_logits<V>(row, e0, a.E, l);
+  uint32_t live = 0;                              // not masked
+#pragma unroll
+  for (int v = 0; v < V; ++v) live |= l[v] <= Logits<T>::lowest ? 0u : 1u << v;
+
+  // largest logit and sum of exponentials of the row
+  float top = 0.f, total = 1.f;
+  if (a.score == MX_SCORE_SOFTMAX && (BY == kValues || !a.renormalize)) {
+    float m = -kInf;
+#pragma unroll
+    for (int v = 0; v < V; ++v) m = fmaxf(m, live >> v & 1 ? l[v] : -kInf);
+    m = lanes_max<L>(m);
+    top = m > -kInf ? m : 0.f;
+    total = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) total += live >> v & 1 ? exp32(l[v] - top) : 0.f;
+    total = lanes_sum<L>(total);
+  }
+
+  float c[V];
+  const float inv = __builtin_amdgcn_rcpf(total);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if constexpr (BY == kValues) {
+      // (2^-19 of the largest score will do)
+      const float p = __builtin_amdgcn_exp2f((a.score == MX_SCORE_SOFTMAX ? l[v] - top : -l[v]) * 1.442695041f);
+      const float s = a.score == MX_SCORE_SOFTMAX ? p * inv : __builtin_amdgcn_rcpf(1.f + p);
+      c[v] = bias != nullptr && e0 + v < a.E ? s + bias[e0 + v] : s;
+    } else {
+      c[v] = l[v] + 0.f;                          // no negative zero beside a positive one
+    }
+    c[v] = (live >> v & 1) && c[v] > -kInf ? c[v] : -kInf;        // masked, NaN: behind the others
+  }
+
+  // Keys.  Low bits: the index, the lowest largest; 0 is no expert.
+  const int bits = 32 - __builtin_clz(a.E);       // 2^bits > E
+  const uint32_t low = (1u << bits) - 1;
+  uint32_t key[V];
+  float cmax = 0.f;
+  if constexpr (BY == kExact) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t u = __float_as_uint(c[v]);
+      const uint32_t order = (u >> 16) ^ ((int)u < 0 ? 0xFFFFu : 0x8000u);
+      key[v] = (c[v] > -kInf ? order << 16 : 0u) | (0xFFFFu - (uint32_t)(e0 + v));
+    }
+  } else {
+    float m = -kInf;
+#pragma unroll
+    for (int v = 0; v < V; ++v) m = fmaxf(m, c[v]);
+    cmax = lanes_max<L>(m);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t lack = min(__float_as_uint(fmaxf(cmax - c[v], 0.f)), 0x7F7FFFFFu);
+      const uint32_t order = max((0x7F7FFFFFu - lack) << 1 & ~low, low + 1);
+      key[v] = (c[v] > -kInf ? order : 0u) | (low - (uint32_t)(e0 + v));
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) key[v] = e0 + v < a.E ? key[v] : 0u;
+
+  // Difference below which two computed c may be out of order: scores to 2^-19 of
+  // the largest of them, the sum with the bias and the difference to cmax to 2^-24.
+  const float tol = BY != kValues ? 0.f : a.score == MX_SCORE_SOFTMAX ? 0x1p-17f * inv : 0x1p-20f;
+  const float rel = BY == kValues ? 0x1p-22f : 0.f;
+  bool unsure = BY != kExact && !(fabsf(cmax) < kInf) && cmax != -kInf;
+
+  if (a.groups > 1) {
+    // a group is n / V lanes (a power of two)
+    const int n = a.E / a.groups, lanes = n / V;
+    float m1 = -kInf, m2 = -kInf;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      m2 = fmaxf(m2, fminf(m1, c[v]));
+      m1 = fmaxf(m1, c[v]);
+    }
+    for (int d = 1; d < lanes; d <<= 1) {
+      const float o1 = __shfl_xor(m1, d), o2 = __shfl_xor(m2, d);
+      m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+      m1 = fmaxf(m1, o1);
+    }
+    const float value = a.group_top2 && m2 > -kInf ? m1 + m2 : m1;
+    // how many groups are better, and between which numbers that lies
+    const float far = 2.f * tol + 5.f * rel * fabsf(value), least = value - far, most = value + far;
+    const int mine = e0 / n, first = (threadIdx.x & 63) - sub;
+    int better = 0, surely = 0, maybe = -1;
+    for (int g = 0; g < a.groups; ++g) {
+      const float o = L == 64 ? lane_value(value, g * lanes) : __shfl(value, first + g * lanes);
+      better += o > value || (o == value && g < mine);
+      if (BY == kValues) {
+        surely += o > most;
+        maybe += o >= least;
+      }
+    }
+    // (a group of masked experts alone is behind every other for certain)
+    unsure = unsure || (BY == kValues && e0 < a.E && value > -kInf &&
+                        (better < a.topk_groups ? maybe >= a.topk_groups : surely < a.topk_groups));
+    if (better >= a.topk_groups) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = 0;
+    }
+  }
+  sort_keys<V>(key);
+
+  // slot r * L + sub of the token's picks in register r
+  int id[kSlots];
+#pragma unroll
+  for (int r = 0; r < kSlots; ++r) id[r] = 0;
+  uint32_t before = 0;
+  auto order_of = [&](uint32_t k) { return BY == kExact ? k >> 16 : k & ~low; };
+  for (int j = 0; j < (BY == kExact ? a.k : a.k + 1); ++j) {
+    const uint32_t best = lanes_max<L>(key[0]);
+    if constexpr (BY != kExact) {
+      // the one before has to be better beyond doubt (the masked follow by index)
+      const uint32_t p = order_of(before), q = order_of(best);
+      const float lack_p = __uint_as_float(0x7F7FFFFFu - (p >> 1));                    // at most
+      const float lack_q = __uint_as_float(0x7F7FFFFFu - ((q | low) >> 1));            // at least
+      unsure = unsure || (j > 0 && q != 0 && !(lack_q > lack_p + (tol + rel * (fabsf(cmax) + lack_p))));
+      before = best;
+      if (j == a.k) break;
+    }
+    // the lane that had it moves its keys up (by masks: of selects the compiler makes
+    // an index into the registers, V^2 instructions)
+    const uint32_t had = key[0] == best ? ~0u : 0u;
+#pragma unroll
+    for (int v = 0; v + 1 < V; ++v) key[v] = (key[v] & ~had) | (key[v + 1] & had);
+    key[V - 1] &= ~had;
+    const int e = BY == kExact ? 0xFFFF - (int)(best & 0xFFFFu) : (int)(low - (best & low));
+#pragma unroll
+    for (int r = 0; r < kSlots; ++r)
+      if (j == r * L + sub) id[r] = e;
+  }
+
+  if constexpr (BY != kExact) {
+    if (__any(unsure)) {
+      // again in fp64, an arg-max over all registers and lanes per pick
+      double x[V];
+      double sum = 0.;
+      if (BY == kValues && a.score == MX_SCORE_SOFTMAX) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          x[v] = live >> v & 1 ? exp((double)l[v] - (double)top) : 0.;
+          sum += x[v];
+        }
+        for (int d = 1; d < L; d <<= 1) sum += __shfl_xor(sum, d);
+      }
+      constexpr double kLow = -1.7976931348623157e308;
+      uint32_t open = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (BY == kValues) {
+          x[v] = a.score == MX_SCORE_SOFTMAX ? x[v] / sum : 1. / (1. + exp(-(double)l[v]));
+          if (bias != nullptr && e0 + v < a.E) x[v] += (double)bias[e0 + v];
+        } else {
+          x[v] = (double)l[v];
+        }
+        x[v] = (live >> v & 1) && x[v] > kLow ? x[v] : kLow;
+        open |= e0 + v < a.E ? 1u << v : 0u;
+      }
+      if (a.groups > 1) {
+        const int n = a.E / a.groups, lanes = n / V;
+        double m1 = kLow, m2 = kLow;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          m2 = fmax(m2, fmin(m1, x[v]));
+          m1 = fmax(m1, x[v]);
+        }
+        for (int d = 1; d < lanes; d <<= 1) {
+          const double o1 = __shfl_xor(m1, d), o2 = __shfl_xor(m2, d);
+          m2 = fmax(fmax(m2, o2), fmin(m1, o1));
+          m1 = fmax(m1, o1);
+        }
+        const double value = a.group_top2 && m2 > kLow ? m1 + m2 : m1;
+        const int mine = e0 / n, first = (threadIdx.x & 63) - sub;
+        int better = 0;
+        for (int g = 0; g < a.groups; ++g) {
+          const double o = L == 64 ? lane_value(value, g * lanes) : __shfl(value, first + g * lanes);
+          better += o > value || (o == value && g < mine);
+        }
+        if (better >= a.topk_groups) open = 0;
+      }
+      // a double's bits in the order of its values, high word, low word, index
+      auto high_of = [](double y) {
+        const uint64_t u = (uint64_t)__double_as_longlong(y);
+        return (uint32_t)(u >> 32) ^ ((int64_t)u < 0 ? 0xFFFFFFFFu : 0x80000000u);
+      };
+      auto low_of = [](double y) {
+        const uint64_t u = (uint64_t)__double_as_longlong(y);
+        return (uint32_t)u ^ ((int64_t)u < 0 ? 0xFFFFFFFFu : 0u);
+      };
+      for (int j = 0; j < a.k; ++j) {
+        double best = kLow;
+        uint32_t e = 0;                            // 1024 less the lane's best expert; 0: none left
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v)
+          if ((open >> v & 1) && x[v] >= best) {
+            best = x[v];
+            e = 1024u - (uint32_t)(e0 + v);
+          }
+        // (the reductions stand alone: every lane takes part in them)
+        const uint32_t high = e ? high_of(best) : 0u, high_most = lanes_max<L>(high);
+        const uint32_t lo = high == high_most ? low_of(best) : 0u, low_most = lanes_max<L>(lo);
+        e = 1024u - lanes_max<L>(high == high_most && lo == low_most ? e : 0u);
+        if (e >= (uint32_t)e0 && e < (uint32_t)(e0 + V)) open &= ~(1u << (e - e0));
+#pragma unroll
+        for (int r = 0; r < kSlots; ++r)
+          if (j == r * L + sub) id[r] = (int)e;
+      }
+    }
+  }
+
+  // weights of the slots
+  float picked[kSlots], w[kSlots];
+  bool on[kSlots];
+#pragma unroll
+  for (int r = 0; r < kSlots; ++r) {
+    const int j = r * L + sub;
+    picked[r] = j < a.k ? Logits<T>::load(row + id[r]) : -kInf;
+    on[r] = j < a.k && !(picked[r] <= Logits<T>::lowest);
+    w[r] = 0.f;
+  }
+  if (a.renormalize) {
+    // relative to the largest of the slots, so that their sum is no underflow
+    float m = -kInf;
+#pragma unroll
+    for (int r = 0; r < kSlots; ++r) m = fmaxf(m, on[r] ? picked[r] : -kInf);
+    m = lanes_max<L>(m);
+    m = m > -kInf ? m : 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < kSlots; ++r) {
+      if (on[r])
+        w[r] = a.score == MX_SCORE_SOFTMAX
+                   ? exp32(picked[r] - m)
+                   : exp32(fminf(picked[r], 0.f) - fminf(m, 0.f)) / (1.f + exp32(-fabsf(picked[r])));
+      sum += w[r];
+    }
+    sum = lanes_sum<L>(sum);
+    // a NaN anywhere is one in every softmax score of its token, chosen or not
+    uint32_t nan = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) nan |= a.score == MX_SCORE_SOFTMAX && l[v] != l[v] ? 1u : 0u;
+    nan = lanes_max<L>(nan);
+#pragma unroll
+    for (int r = 0; r < kSlots; ++r) w[r] = nan ? __builtin_nanf("") : on[r] ? w[r] / sum : 0.f;
+  } else {
+#pragma unroll
+    for (int r = 0; r < kSlots; ++r)
+      if (on[r]) w[r] = a.score == MX_SCORE_SOFTMAX ? exp32(picked[r] - top) / total : sigmoid(picked[r]);
+  }
+  if (token < a.T) {
+#pragma unroll
+    for (int r = 0; r < kSlots; ++r) {
+      const int j = r * L + sub;
+      if (j < a.k) {
+        a.expert_idx[t * a.k + j] = id[r];
+        a.combine[t * a.k + j] = w[r] * a.scale;
+      }
+    }
+  }
+}
 
 // V registers of experts per lane; VALUES: c in fp64, else the logits decide.
 template <int V, class T, bool VALUES>
-__global__ __launch_bounds__(kRouterWaves * 64) void router_fwd_kernel(const T* __restrict__ logits,
+__global__ __launch_bounds__(kRouterWaves * 64) void router_walk_kernel(const T* __restrict__ logits,
                                                                        const float* __restrict__ bias, RouterArgs a) {
   typedef std::conditional_t<VALUES, double, float> C;
   constexpr C kLowest = VALUES ? (C)-1.7976931348623157e308 : (C)-3.402823466e38f;
@@ -142,7 +524,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_fwd_kernel(const T* 
       top = wave_max(m);
       top = top > -kInf ? top : 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) total += live >> v & 1 ? exp_neg(l[v] - top) : 0.f;
+      for (int v = 0; v < V; ++v) total += live >> v & 1 ? exp32(l[v] - top) : 0.f;
       total = wave_sum(total);
     }
     C c[V];
@@ -248,8 +630,8 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_fwd_kernel(const T* 
       const float m0 = wave_max(on ? picked : -kInf);
       const float m = m0 > -kInf ? m0 : 0.f;
       if (on) {
-        if (a.score == MX_SCORE_SOFTMAX) w = exp_neg(picked - m);
-        else w = exp_neg(fminf(picked, 0.f) - fminf(m, 0.f)) / (1.f + exp_neg(-fabsf(picked)));
+        if (a.score == MX_SCORE_SOFTMAX) w = exp32(picked - m);
+        else w = exp32(fminf(picked, 0.f) - fminf(m, 0.f)) / (1.f + exp32(-fabsf(picked)));
       }
       const float sum = wave_sum(w);
       w = on ? w / sum : 0.f;
@@ -261,7 +643,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_fwd_kernel(const T* 
         if (__ballot(nan)) w = __builtin_nanf("");
       }
     } else if (on) {
-      w = a.score == MX_SCORE_SOFTMAX ? exp_neg(picked - top) / total : sigmoid(picked);
+      w = a.score == MX_SCORE_SOFTMAX ? exp32(picked - top) / total : sigmoid(picked);
     }
     if (lane < a.k) {
       a.expert_idx[t * a.k + lane] = id;
@@ -270,71 +652,95 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_fwd_kernel(const T* 
   }
 }
 
-// Gradient of the logits (see mx_topk_router_bwd).
-template <int V, class T>
-__global__ __launch_bounds__(kRouterWaves * 64) void router_bwd_kernel(const T* __restrict__ logits,
-                                                                       const float* __restrict__ dcombine,
-                                                                       RouterArgs a, T* __restrict__ dlogits) {
-  const int lane = threadIdx.x & 63;
-  const int64_t step = (int64_t)gridDim.x * kRouterWaves;
-  const float kInf = __builtin_inff();
-  for (int64_t t = (int64_t)blockIdx.x * kRouterWaves + (threadIdx.x >> 6); t < a.T; t += step) {
-    // slot j in lane j
-    int id = -1;
-    float w = 0.f, g = 0.f;
-    if (lane < a.k) {
-      id = a.expert_idx[t * a.k + lane];
-      w = a.combine[t * a.k + lane];
-      g = dcombine[t * a.k + lane];
+// Gradient of the logits (see mx_topk_router_bwd).  A wave takes `n` tokens, whose
+// slots and rows are runs of memory: a lane per slot, then one per token for the sum
+// over its slots, then one per slot again, which adds its part to the row in LDS (the
+// forward's ids are distinct: every cell gets one), and the rows leave 16 bytes a lane.  The softmax of a row needs no sum over it: its
+// largest slot's weight and logit give s[e] = p exp(l[e] - l).
+template <class T>
+__global__ __launch_bounds__(64) void router_bwd_kernel(const T* __restrict__ logits, const float* __restrict__ dcombine,
+                                                        RouterArgs a, int n, T* __restrict__ dlogits) {
+  extern __shared__ float lds[];
+  const int lane = threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * n;
+  n = (int)min((int64_t)n, a.T - t0);
+  const int slots = n * a.k, cells = n * a.E;
+  float* row = lds;                               // [n][E] the chosen experts' part
+  float* share = row + cells;                     // [n][k] weight over scale
+  float* grad = share + slots;                    // [n][k]
+  float* factor = grad + slots;                   // [n][k] what grad is multiplied with, or the logit
+  int* id = (int*)(factor + slots);               // [n][k]
+  float* ref = (float*)(id + slots);              // [n] sum over the slots, largest slot's logit and share
+  const bool dense = a.score == MX_SCORE_SOFTMAX && !a.renormalize;
+  for (int i = lane; i < slots; i += 64) {
+    const int e = a.expert_idx[t0 * a.k + i];
+    const float w = a.combine[t0 * a.k + i], p = w / a.scale;
+    const bool in = e >= 0 && e < a.E;
+    float x = w;
+    if (dense || (a.score == MX_SCORE_SIGMOID && a.renormalize)) {
+      const float l = in ? Logits<T>::load(logits + (t0 + (uint32_t)i / (uint32_t)a.k) * a.E + e) : 0.f;
+      x = dense ? l : w * sigmoid(-l);
+    } else if (a.score == MX_SCORE_SIGMOID) {
+      x = w * (1.f - p);
     }
-    const float p = w / a.scale;
-    float d;                                   // the slot's part of its expert's gradient
-    float dot = 0.f;
-    const bool dense = a.score == MX_SCORE_SOFTMAX && !a.renormalize;
-    if (a.renormalize || dense) dot = wave_sum(g * p);
-    if (dense) {
-      d = g * a.scale;
-      dot *= a.scale;
-    } else if (a.renormalize) {
-      d = w * (g - dot);
-      if (a.score == MX_SCORE_SIGMOID && lane < a.k && id >= 0 && id < a.E)
-        d *= sigmoid(-Logits<T>::load(logits + t * a.E + id));
-    } else {
-      d = w * (1.f - p) * g;
-    }
-    float out[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) out[v] = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-      const int e = __builtin_amdgcn_readlane(id, j);
-      const float dj = lane_value(d, j);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e == v * 64 + lane) out[v] += dj;
-    }
-    if (dense) {
-      float l[V], m = -kInf, total = 0.f;
-      uint32_t live = 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = v * 64 + lane;
-        l[v] = e < a.E ? Logits<T>::load(logits + t * a.E + e) : -kInf;
-        if (!(l[v] <= Logits<T>::lowest)) live |= 1u << v;
-        m = fmaxf(m, live >> v & 1 ? l[v] : -kInf);
+    share[i] = p;
+    grad[i] = dcombine[t0 * a.k + i];
+    factor[i] = x;
+    id[i] = in ? e : -1;
+  }
+  for (int i = lane; i < cells; i += 64) row[i] = 0.f;
+  __syncthreads();
+  if (a.renormalize || dense) {
+    for (int t = lane; t < n; t += 64) {
+      float dot = 0.f, most = 0.f, at = 0.f;
+#pragma unroll 4
+      for (int j = 0; j < a.k; ++j) {
+        const float p = share[t * a.k + j], x = factor[t * a.k + j];
+        dot = fmaf(grad[t * a.k + j], p, dot);
+        const bool more = !(p <= most);
+        most = more ? p : most;
+        at = more ? x : at;
       }
-      const float top = wave_max(m);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        l[v] = live >> v & 1 ? exp_neg(l[v] - top) : 0.f;
-        total += l[v];
-      }
-      total = wave_sum(total);
-#pragma unroll
-      for (int v = 0; v < V; ++v) out[v] = live >> v & 1 ? l[v] / total * (out[v] - dot) : 0.f;
+      ref[3 * t] = dot;
+      ref[3 * t + 1] = at;
+      ref[3 * t + 2] = most;
     }
+    __syncthreads();
+  }
+  for (int i = lane; i < slots; i += 64) {
+    const int t = (uint32_t)i / (uint32_t)a.k;
+    const float g = grad[i];
+    const float d = dense ? g : factor[i] * (a.renormalize ? g - ref[3 * t] : g);
+    if (id[i] >= 0) atomicAdd(row + t * a.E + id[i], d);
+  }
+  __syncthreads();
+  auto softmax_grad = [&](const float* r, float l, float g) {
+    const float s = l <= Logits<T>::lowest || r[2] == 0.f ? 0.f : exp32(l - r[1]) * r[2];
+    return s * (a.scale * (g - r[0]));
+  };
+  const T* src = logits + t0 * a.E;
+  T* dst = dlogits + t0 * a.E;
+  if (a.E % 4 == 0) {
+    for (int i = 4 * lane; i < cells; i += 256) {
+      float o[4];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * 64 + lane < a.E) Logits<T>::store(dlogits + t * a.E + v * 64 + lane, out[v]);
+      for (int u = 0; u < 4; ++u) o[u] = row[i + u];
+      if (dense) {
+        const float* p = ref + 3 * ((uint32_t)i / (uint32_t)a.E);
+        const float r[3] = {p[0], p[1], p[2]};
+        float l[4];
+        load_logits<4>(src + i, 0, 4, l);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) o[u] = softmax_grad(r, l[u], o[u]);
+      }
+      store4(dst + i, o);
+    }
+  } else {
+    for (int i = lane; i < cells; i += 64) {
+      float o = row[i];
+      if (dense) o = softmax_grad(ref + 3 * ((uint32_t)i / (uint32_t)a.E), Logits<T>::load(src + i), o);
+      Logits<T>::store(dst + i, o);
+    }
   }
 }
 
@@ -346,46 +752,76 @@ dim3 router_grid(int64_t T) {
   return dim3((unsigned)(n < 2048 ? n : 2048));
 }
 
+// A wave per token, for groups that do not lie along lanes.
 template <int V, class T>
-hipError_t launch_fwd(const RouterArgs& a, hipStream_t st) {
-  const bool values = a.bias != nullptr || (a.groups > 1 && a.group_top2);
-  if (values)
-    hipLaunchKernelGGL((router_fwd_kernel<V, T, true>), router_grid(a.T), dim3(kRouterWaves * 64), 0, st,
+hipError_t launch_walk(const RouterArgs& a, hipStream_t st) {
+  if (a.bias != nullptr || a.group_top2)
+    hipLaunchKernelGGL((router_walk_kernel<V, T, true>), router_grid(a.T), dim3(kRouterWaves * 64), 0, st,
                        (const T*)a.logits, a.bias, a);
   else
-    hipLaunchKernelGGL((router_fwd_kernel<V, T, false>), router_grid(a.T), dim3(kRouterWaves * 64), 0, st,
+    hipLaunchKernelGGL((router_walk_kernel<V, T, false>), router_grid(a.T), dim3(kRouterWaves * 64), 0, st,
                        (const T*)a.logits, a.bias, a);
   return hipGetLastError();
 }
 
-template <int V, class T>
+template <class T>
 hipError_t launch_bwd(const RouterArgs& a, const float* dcombine, void* dlogits, hipStream_t st) {
-  hipLaunchKernelGGL((router_bwd_kernel<V, T>), router_grid(a.T), dim3(kRouterWaves * 64), 0, st, (const T*)a.logits,
-                     dcombine, a, (T*)dlogits);
+  const int n = a.E <= kBwdCells / 64 ? 64 : a.E < kBwdCells ? kBwdCells / a.E : 1;
+  const size_t bytes = (size_t)n * (a.E + 4 * a.k + 3) * sizeof(float);
+  hipLaunchKernelGGL((router_bwd_kernel<T>), dim3((unsigned)((a.T + n - 1) / n)), dim3(64), bytes, st, (const T*)a.logits,
+                     dcombine, a, n, (T*)dlogits);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_router_fwd(const RouterArgs& a, hipStream_t st) {
+namespace {
+
+// Whether scores have to be compared: added to a bias, or to each other.
+bool by_values(const RouterArgs& a) { return a.bias != nullptr || (a.groups > 1 && a.group_top2); }
+
+// Whether every group is a power of two of lanes with V experts each.
+bool along_lanes(const RouterArgs& a, int V) {
+  const int n = a.E / a.groups;
+  return a.groups == 1 || (n % V == 0 && (n / V & (n / V - 1)) == 0);
+}
+
+template <int L, int V, class T>
+hipError_t launch_pick(const RouterArgs& a, hipStream_t st) {
+  constexpr int by = std::is_same_v<T, float> ? kLogits : kExact;
+  const int64_t per = kRouterWaves * 64 / L;
+  const dim3 grid((unsigned)((a.T + per - 1) / per)), block(kRouterWaves * 64);
+  if (by_values(a))
+    hipLaunchKernelGGL((router_pick_kernel<L, V, T, kValues>), grid, block, 0, st, (const T*)a.logits, a.bias, a);
+  else
+    hipLaunchKernelGGL((router_pick_kernel<L, V, T, by>), grid, block, 0, st, (const T*)a.logits, a.bias, a);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_fwd(const RouterArgs& a, hipStream_t st) {
+  if (a.E <= 32 && along_lanes(a, 4)) return launch_pick<8, 4, T>(a, st);
+  if (a.E <= 64 && along_lanes(a, 4)) return launch_pick<16, 4, T>(a, st);
+  if (a.E <= 128 && along_lanes(a, 4)) return launch_pick<32, 4, T>(a, st);
+  // (bf16 logits alone have no fp64 pass to wait for: half the lanes, 16384 x 256 8.1 us for 10.4)
+  if (std::is_same_v<T, uint16_t> && !by_values(a) && a.E > 128 && a.E <= 256 && along_lanes(a, 8))
+    return launch_pick<32, 8, T>(a, st);
+  if (a.E <= 256 && along_lanes(a, 4)) return launch_pick<64, 4, T>(a, st);
+  if (a.E <= 512 && along_lanes(a, 8)) return launch_pick<64, 8, T>(a, st);
+  if (a.E <= 1024 && along_lanes(a, 16)) return launch_pick<64, 16, T>(a, st);
   const int v = (a.E + 63) / 64;
-  if (a.logits_f32)
-    return v <= 1 ? launch_fwd<1, float>(a, st) : v <= 2 ? launch_fwd<2, float>(a, st) : v <= 4 ? launch_fwd<4, float>(a, st)
-           : v <= 8 ? launch_fwd<8, float>(a, st) : launch_fwd<16, float>(a, st);
-  return v <= 1 ? launch_fwd<1, uint16_t>(a, st) : v <= 2 ? launch_fwd<2, uint16_t>(a, st)
-         : v <= 4 ? launch_fwd<4, uint16_t>(a, st) : v <= 8 ? launch_fwd<8, uint16_t>(a, st)
-                                                             : launch_fwd<16, uint16_t>(a, st);
+  return v <= 1 ? launch_walk<1, T>(a, st) : v <= 2 ? launch_walk<2, T>(a, st) : v <= 4 ? launch_walk<4, T>(a, st)
+         : v <= 8 ? launch_walk<8, T>(a, st) : launch_walk<16, T>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_router_fwd(const RouterArgs& a, hipStream_t st) {
+  return a.logits_f32 ? launch_fwd<float>(a, st) : launch_fwd<uint16_t>(a, st);
 }
 
 hipError_t launch_router_bwd(const RouterArgs& a, const float* dcombine, void* dlogits, hipStream_t st) {
-  const int v = (a.E + 63) / 64;
-  if (a.logits_f32)
-    return v <= 1 ? launch_bwd<1, float>(a, dcombine, dlogits, st) : v <= 2 ? launch_bwd<2, float>(a, dcombine, dlogits, st)
-           : v <= 4 ? launch_bwd<4, float>(a, dcombine, dlogits, st) : v <= 8 ? launch_bwd<8, float>(a, dcombine, dlogits, st)
-                                                             : launch_bwd<16, float>(a, dcombine, dlogits, st);
-  return v <= 1 ? launch_bwd<1, uint16_t>(a, dcombine, dlogits, st) : v <= 2 ? launch_bwd<2, uint16_t>(a, dcombine, dlogits, st)
-         : v <= 4 ? launch_bwd<4, uint16_t>(a, dcombine, dlogits, st)
-         : v <= 8 ? launch_bwd<8, uint16_t>(a, dcombine, dlogits, st) : launch_bwd<16, uint16_t>(a, dcombine, dlogits, st);
+  return a.logits_f32 ? launch_bwd<float>(a, dcombine, dlogits, st) : launch_bwd<uint16_t>(a, dcombine, dlogits, st);
 }
 
 }  // namespace mxk

@@ -254,3 +254,29 @@ def test_large_batch_is_deterministic():
     at = torch.randperm(l.shape[0], device="cuda:0")
     b = mx.mx_topk_router(l[at], 8, renormalize=False)
     assert torch.equal(a[0][at], b[0]) and torch.equal(a[1][at], b[1])
+
+
+@pytest.mark.parametrize("E,groups", [(32, 1), (64, 8), (100, 1), (128, 4), (256, 8), (256, 1), (500, 5), (512, 16), (1024, 1)])
+def test_many_tokens_against_fp64(E, groups):
+    """Enough tokens that some have experts, or groups, which fp32 would put in the
+    wrong order: every choice that of the 64-bit scores, sorted with torch."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    gen = torch.Generator(device="cuda:0").manual_seed(E + groups)
+    kept = max(1, groups // 2)
+    for dtype in (torch.float32, torch.bfloat16):
+        for score in ("softmax", "sigmoid"):
+            l = (torch.randn((20000, E), generator=gen, device="cuda:0") * 1.5).to(dtype)
+            for bias, gs in ((None, "max"), (torch.randn(E, generator=gen, device="cuda:0") * 0.05, "top2")):
+                k = min(8, kept * (E // groups))
+                ids, _ = mx.mx_topk_router(l, k, score, bias, groups, kept, gs)
+                d = l.double()
+                c = d if bias is None else (torch.softmax(d, 1) if score == "softmax" else torch.sigmoid(d)) + bias.double()
+                if groups > 1:
+                    two = torch.sort(c.view(-1, groups, E // groups), dim=2, descending=True).values
+                    value = two[..., 0] if gs == "max" else two[..., :2].sum(2)
+                    best = torch.sort(value, dim=1, descending=True, stable=True).indices[:, :kept]
+                    on = torch.zeros_like(value, dtype=torch.bool).scatter_(1, best, True)
+                    c = c.masked_fill(~on.repeat_interleave(E // groups, 1), -float("inf"))
+                want = torch.sort(c, dim=1, descending=True, stable=True).indices[:, :k]
+                assert torch.equal(ids.long(), want), (dtype, score, gs)
