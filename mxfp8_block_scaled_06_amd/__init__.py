@@ -1059,25 +1059,34 @@ def _choice(value, of, name):
     return of[value]
 
 
+def _router_arguments(logits, k, score, bias, group_score):
+    """Checks of the router's operands: codes of the logits' type, the score and the groups' value."""
+    import torch
+    kind = _type(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    if not 0 <= k <= MOE_MAX_TOPK:
+        raise ValueError(f"k={k} outside [1, {MOE_MAX_TOPK}]")
+    if bias is not None:
+        E = logits.shape[1]
+        _require(bias, torch.float32, "bias")
+        if tuple(bias.shape) != (E,):
+            raise ValueError(f"bias must be [{E}] (one per expert), got {tuple(bias.shape)}")
+        _same_device(logits, bias)
+    return kind, _choice(score, SCORES, "score"), _choice(group_score, GROUP_SCORES, "group_score")
+
+
 def mx_topk_router_fwd(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
                        group_score: str = "max", renormalize: bool = True, scale: float = 1.0, expert_idx=None,
                        combine=None):
     """(expert_idx int32 [T, k], combine fp32 [T, k]) of the logits (see mx_topk_router), without a gradient."""
     import torch
     lib = load_library()
-    kind = _type(logits, "logits")
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T, E]")
+    kind, sc, gs = _router_arguments(logits, k, score, bias, group_score)
     T, E = logits.shape
-    if bias is not None:
-        _require(bias, torch.float32, "bias")
-        if tuple(bias.shape) != (E,):
-            raise ValueError(f"bias must be [{E}] (one per expert), got {tuple(bias.shape)}")
-        _same_device(logits, bias)
-    sc, gs = _choice(score, SCORES, "score"), _choice(group_score, GROUP_SCORES, "group_score")
     dev = logits.device
-    expert_idx = _out(expert_idx, (T, max(k, 0)), torch.int32, dev, "expert_idx")
-    combine = _out(combine, (T, max(k, 0)), torch.float32, dev, "combine")
+    expert_idx = _out(expert_idx, (T, k), torch.int32, dev, "expert_idx")
+    combine = _out(combine, (T, k), torch.float32, dev, "combine")
     with _on(dev):
         _check("mx_topk_router_fwd",
                lib.mx_topk_router_fwd(_ptr(logits), kind, _ptr(bias), T, E, k, sc, groups, topk_groups, gs,
@@ -1132,6 +1141,8 @@ def mx_topk_router(logits, k: int, score: str = "softmax", bias=None, groups: in
 
 
 def _halves(gu):
+    import torch
+    _require(gu, torch.bfloat16, "gu")
     if gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError(f"gu must be [M, 2N] (gate columns, then up columns), got {tuple(gu.shape)}")
     return gu.shape[0], gu.shape[1] // 2
@@ -1151,7 +1162,6 @@ def mx_swiglu_fwd(gu, keep: bool = True, h=None, kept=None, kept_s=None):
     the MXFP8 checkpoint of gu that mx_swiglu_bwd reads (None, None with keep=False).  N % 32 == 0."""
     import torch
     lib = load_library()
-    _require(gu, torch.bfloat16, "gu")
     M, N = _halves(gu)
     dev = gu.device
     h = _out(h, (M, N), torch.bfloat16, dev, "h")
@@ -1215,7 +1225,6 @@ def mx_swiglu_quantize(gu, rows=None, q=None, s=None):
     hold.  N % 128 == 0."""
     import torch
     lib = load_library()
-    _require(gu, torch.bfloat16, "gu")
     M, N = _halves(gu)
     n = _rows_of(gu, rows, None, M)
     dev = gu.device
@@ -1241,7 +1250,6 @@ def mx_swiglu_quantize_fwd(gu, rows=None, combine=None, ldq: Optional[int] = Non
     defaults to M rounded up to 128."""
     import torch
     lib = load_library()
-    _require(gu, torch.bfloat16, "gu")
     M, N = _halves(gu)
     n = _rows_of(gu, rows, combine, M)
     if ldq is None:

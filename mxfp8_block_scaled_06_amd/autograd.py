@@ -37,11 +37,11 @@ from __future__ import annotations
 
 import weakref
 
-from . import (SCORES, _check as _check_status, _format, _on, _ptr, _stream, load_library, mx_grouped_gemm_mx,
+from . import (MXError, _combine_sizes, _format, _halves, _on, _router_arguments, load_library, mx_grouped_gemm_mx,
                mx_grouped_gemm_mx_rows, mx_grouped_gemm_mxfp4, mx_grouped_mm_dgrad_fp4, mx_grouped_mm_dgrad_q,
                mx_grouped_mm_fwd_fp4, mx_grouped_mm_fwd_q, mx_quantize_dual, mx_quantize_dual_gather,
-               mx_quantize_rowwise_gather, mx_quantize_weights, mx_quantize_weights_fp4, mx_route, mx_swiglu_fwd, mx_swiglu_quantize, mx_swiglu_quantize_bwd,
-               mx_swiglu_quantize_fwd, mx_topk_combine_fwd, mx_topk_router_fwd, mx_topk_sum_rows)
+               mx_quantize_rowwise_gather, mx_quantize_weights, mx_quantize_weights_fp4, mx_route, mx_swiglu_quantize,
+               mx_swiglu_quantize_bwd, mx_swiglu_quantize_fwd, mx_topk_combine_fwd, mx_topk_sum_rows)
 
 
 class WeightCache:
@@ -368,63 +368,22 @@ def _wants_grad(*tensors):
     return torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
 
 
-def _first_order(backward):
-    """A backward without one of its own: under create_graph=True its results refuse to be
-    differentiated.  torch's decorator for that costs 4 us a call, so it is left out where no
-    graph is made."""
-    import torch
-    refusing = torch.autograd.function.once_differentiable(backward)
-
-    def call(ctx, *grads):
-        return refusing(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
-
-    return staticmethod(call)
+_nodes = None
 
 
-# The backwards of the router, the activation and the weighted sum call the C ABI themselves: what
-# they pass was checked in the forward or made by it, autograd gives gradients of the outputs' shape,
-# type and device and makes that device current, and its thread runs 16 us longer through the binding's
-# checks (Python objects that the main thread has just used: 100 us for a router's forward and backward
-# instead of 72).
-
-
-class _MXRouter:
-    """torch.autograd.Function of mx_topk_router (built lazily)."""
-    fn = None
-
-    @classmethod
-    def get(cls):
-        if cls.fn is None:
-            import torch
-
-            class Fn(torch.autograd.Function):
-                @staticmethod
-                def forward(ctx, logits, options):
-                    expert_idx, combine = mx_topk_router_fwd(logits, *options)
-                    ctx.mark_non_differentiable(expert_idx)
-                    ctx.set_materialize_grads(False)       # no zeros in the place of a gradient of the ids
-                    ctx.save_for_backward(logits, expert_idx, combine)
-                    ctx.options = options
-                    return expert_idx, combine
-
-                @_first_order
-                def backward(ctx, _, dcombine):
-                    if dcombine is None:
-                        return None, None
-                    logits, expert_idx, combine = ctx.saved_tensors
-                    k, score, _, _, _, _, renormalize, scale = ctx.options
-                    T, E = logits.shape
-                    dlogits, dcombine = torch.empty_like(logits), dcombine.contiguous()
-                    status = load_library().mx_topk_router_bwd(
-                        logits.data_ptr(), logits.dtype == torch.float32, expert_idx.data_ptr(), combine.data_ptr(),
-                        dcombine.data_ptr(), T, E, k, SCORES[score], renormalize, scale, dlogits.data_ptr(),
-                        _stream(logits.device))
-                    if status:
-                        _check_status("mx_topk_router_bwd", status)
-                    return dlogits, None
-
-            cls.fn = Fn
-        return cls.fn
+def _native():
+    """The autograd nodes of the router, the activation and the weighted sum (csrc/mx_nodes.cpp)."""
+    global _nodes
+    if _nodes is None:
+        load_library()
+        try:
+            from . import _nodes as nodes
+        except ImportError as e:
+            raise RuntimeError(f"_nodes.so is missing or does not fit this torch ({e}): build it with "
+                               "`python -m mxfp8_block_scaled_06_amd.build`") from e
+        nodes.set_error(MXError)
+        _nodes = nodes
+    return _nodes
 
 
 def mx_topk_router(logits, k, score="softmax", bias=None, groups=1, topk_groups=1, group_score="max",
@@ -436,90 +395,22 @@ def mx_topk_router(logits, k, score="softmax", bias=None, groups=1, topk_groups=
     if bias is not None and _wants_grad(bias):
         raise ValueError("mx_topk_router: the bias takes part in the choice of the experts alone and gets no "
                          "gradient: pass bias.detach()")
-    if not _wants_grad(logits):
-        return mx_topk_router_fwd(logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale)
-    return _MXRouter.get().apply(logits, (k, score, bias, groups, topk_groups, group_score, renormalize, scale))
-
-
-class _MXSwiglu:
-    """torch.autograd.Function of mx_swiglu (built lazily)."""
-    fn = None
-
-    @classmethod
-    def get(cls):
-        if cls.fn is None:
-            import torch
-
-            class Fn(torch.autograd.Function):
-                @staticmethod
-                def forward(ctx, gu):
-                    h, kept, kept_s = mx_swiglu_fwd(gu)
-                    ctx.save_for_backward(kept, kept_s)
-                    return h
-
-                @_first_order
-                def backward(ctx, dh):
-                    kept, kept_s = ctx.saved_tensors
-                    M, N = dh.shape
-                    dh, dgu = dh.contiguous(), torch.empty((M, 2 * N), dtype=torch.bfloat16, device=dh.device)
-                    status = load_library().mx_swiglu_bwd(dh.data_ptr(), kept.data_ptr(), kept_s.data_ptr(), M, N,
-                                                          dgu.data_ptr(), _stream(dh.device))
-                    if status:
-                        _check_status("mx_swiglu_bwd", status)
-                    return dgu
-
-            cls.fn = Fn
-        return cls.fn
+    _, sc, gs = _router_arguments(logits, k, score, bias, group_score)
+    return _native().topk_router(logits, k, sc, bias, groups, topk_groups, gs, renormalize, scale)
 
 
 def mx_swiglu(gu):
     """silu(gate) * up with an MXFP8 checkpoint of gu for the backward (the package's mx_swiglu)."""
     gu = gu.contiguous()
-    if not _wants_grad(gu):
-        return mx_swiglu_fwd(gu, keep=False)[0]
-    return _MXSwiglu.get().apply(gu)
-
-
-class _MXCombine:
-    """torch.autograd.Function of mx_topk_combine (built lazily)."""
-    fn = None
-
-    @classmethod
-    def get(cls):
-        if cls.fn is None:
-            import torch
-
-            class Fn(torch.autograd.Function):
-                @staticmethod
-                def forward(ctx, y, combine, pos):
-                    ctx.save_for_backward(y, combine, pos)
-                    return mx_topk_combine_fwd(y, combine, pos)
-
-                @_first_order
-                def backward(ctx, dout):
-                    y, combine, pos = ctx.saved_tensors
-                    T, k, N = y.shape
-                    need_y, need_c, _ = ctx.needs_input_grad
-                    dout = dout.contiguous()
-                    dy = torch.empty_like(y) if need_y else None
-                    dcombine = torch.empty_like(combine) if need_c else None
-                    status = load_library().mx_topk_combine_bwd(
-                        y.data_ptr(), y.dtype == torch.float32, combine.data_ptr(), _ptr(pos),
-                        dout.data_ptr(), T, k, N, _ptr(dy), _ptr(dcombine), _stream(y.device))
-                    if status:
-                        _check_status("mx_topk_combine_bwd", status)
-                    return dy, dcombine, None
-
-            cls.fn = Fn
-        return cls.fn
+    _halves(gu)
+    return _native().swiglu(gu)
 
 
 def mx_topk_combine(y, combine, pos=None):
     """Weighted sum over a token's experts, differentiable in y and combine (the package's mx_topk_combine)."""
     y, combine = y.contiguous(), combine.contiguous()
-    if not _wants_grad(y, combine):
-        return mx_topk_combine_fwd(y, combine, pos)
-    return _MXCombine.get().apply(y, combine, pos)
+    _combine_sizes(y, combine, pos)
+    return _native().topk_combine(y, combine, pos)
 
 
 class _MXLayer:
@@ -557,7 +448,8 @@ class _MXLayer:
                                           kept_s)
                     return out
 
-                @_first_order
+                @staticmethod
+                @torch.autograd.function.once_differentiable
                 def backward(ctx, dout):
                     (combine, offs, rows, pos, q13t, s13t, q2t, s2t, qxt, sxt, qht, sht, kept,
                      kept_s) = ctx.saved_tensors

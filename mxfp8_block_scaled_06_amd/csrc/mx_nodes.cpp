@@ -1,0 +1,183 @@
+// Autograd nodes of the router, the gated activation and the weighted sum over a
+// token's experts, on the C ABI of include/mxmoe.h.
+//
+// Host time is what a small call costs.  A forward and a backward through a node
+// written in Python took 80 - 90 us where one of torch's own took 48: the backward
+// runs on autograd's thread, which takes the GIL and then walks Python objects that
+// the main thread has just used.  These nodes take 56 and need no GIL in the backward.
+//
+// The binding checks types, shapes and devices before it calls (contiguous GPU
+// tensors here); the C ABI checks the rest, and its refusals become MXError.
+#include <torch/extension.h>
+
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+
+#include "mxmoe.h"
+
+namespace {
+
+using torch::Tensor;
+using Maybe = std::optional<Tensor>;
+using torch::autograd::AutogradContext;
+using torch::autograd::variable_list;
+
+struct Refused : std::exception {
+  const char* fn;
+  int status;
+  std::string text;
+  Refused(const char* f, int s) : fn(f), status(s), text(mx_last_error()) {}
+  const char* what() const noexcept override { return text.c_str(); }
+};
+
+void check(const char* fn, mx_status st) {
+  if (st != MX_OK) throw Refused(fn, (int)st);
+}
+
+// In a backward there is no caller of the C ABI to hand a status to.
+void check_backward(const char* fn, mx_status st) {
+  TORCH_CHECK(st == MX_OK, fn, ": ", mx_last_error());
+}
+
+void* stream_of(const Tensor& t) { return c10::hip::getCurrentHIPStream(t.device().index()).stream(); }
+int type_of(const Tensor& t) { return t.scalar_type() == torch::kFloat ? MX_F32 : MX_BF16; }
+const uint16_t* bf16(const Tensor& t) { return (const uint16_t*)t.data_ptr(); }
+template <class T>
+T* ptr(const Tensor& t) {
+  return t.defined() ? (T*)t.data_ptr() : nullptr;
+}
+
+// Gradients made while a graph of them is asked for (create_graph=True): they
+// refuse to be differentiated, as there is no second derivative here.
+variable_list first_order(variable_list grads) {
+  if (!at::GradMode::is_enabled()) return grads;
+  for (auto& g : grads)
+    if (g.defined()) g = g.detach().set_requires_grad(true);
+  auto refuse = std::make_shared<torch::autograd::DelayedError>(
+      "this gradient has no derivative of its own (the kernels compute first derivatives)", (int64_t)grads.size());
+  return (*refuse)(std::move(grads));
+}
+
+struct Router : torch::autograd::Function<Router> {
+  static variable_list forward(AutogradContext* ctx, const Tensor& logits, int64_t k, int64_t score, const Maybe& bias,
+                               int64_t groups, int64_t topk_groups, int64_t group_score, bool renormalize,
+                               double scale) {
+    const int64_t T = logits.size(0), E = logits.size(1);
+    Tensor ids = torch::empty({T, k}, logits.options().dtype(torch::kInt32));
+    Tensor combine = torch::empty({T, k}, logits.options().dtype(torch::kFloat));
+    check("mx_topk_router_fwd",
+          mx_topk_router_fwd(logits.data_ptr(), type_of(logits), bias ? ptr<float>(*bias) : nullptr, T, E, k, (int)score, groups,
+                             topk_groups, (int)group_score, renormalize, (float)scale, ptr<int32_t>(ids),
+                             ptr<float>(combine), stream_of(logits)));
+    ctx->mark_non_differentiable({ids});
+    ctx->set_materialize_grads(false);       // no zeros in the place of a gradient of the ids
+    ctx->save_for_backward({logits, ids, combine});
+    ctx->saved_data["score"] = score;
+    ctx->saved_data["renormalize"] = renormalize;
+    ctx->saved_data["scale"] = scale;
+    return {ids, combine};
+  }
+
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    variable_list out(9);
+    if (!grads[1].defined()) return out;
+    const variable_list saved = ctx->get_saved_variables();
+    const Tensor &logits = saved[0], &ids = saved[1], &combine = saved[2], d = grads[1].contiguous();
+    out[0] = torch::empty_like(logits);
+    check_backward("mx_topk_router_bwd",
+                   mx_topk_router_bwd(logits.data_ptr(), type_of(logits), ptr<int32_t>(ids), ptr<float>(combine),
+                                      ptr<float>(d), logits.size(0), logits.size(1), ids.size(1),
+                                      (int)ctx->saved_data["score"].toInt(), ctx->saved_data["renormalize"].toBool(),
+                                      (float)ctx->saved_data["scale"].toDouble(), out[0].data_ptr(),
+                                      stream_of(logits)));
+    return first_order(std::move(out));
+  }
+};
+
+struct Swiglu : torch::autograd::Function<Swiglu> {
+  // keep: whether a backward may follow
+  static Tensor forward(AutogradContext* ctx, const Tensor& gu, bool keep) {
+    const int64_t M = gu.size(0), N = gu.size(1) / 2;
+    Tensor h = torch::empty({M, N}, gu.options()), kept, kept_s;
+    if (keep) {
+      kept = torch::empty({M, 2 * N}, gu.options().dtype(torch::kByte));
+      kept_s = torch::empty({M, 2 * N / 32}, gu.options().dtype(torch::kByte));
+    }
+    check("mx_swiglu_fwd", mx_swiglu_fwd(bf16(gu), M, N, ptr<uint16_t>(h), ptr<uint8_t>(kept), ptr<uint8_t>(kept_s),
+                                         stream_of(gu)));
+    if (keep) ctx->save_for_backward({kept, kept_s});
+    return h;
+  }
+
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const variable_list saved = ctx->get_saved_variables();
+    const Tensor d = grads[0].contiguous();
+    const int64_t M = d.size(0), N = d.size(1);
+    Tensor dgu = torch::empty({M, 2 * N}, d.options());
+    check_backward("mx_swiglu_bwd", mx_swiglu_bwd(bf16(d), ptr<uint8_t>(saved[0]), ptr<uint8_t>(saved[1]), M, N,
+                                                  ptr<uint16_t>(dgu), stream_of(d)));
+    return first_order({dgu, Tensor()});
+  }
+};
+
+struct Combine : torch::autograd::Function<Combine> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& y, const Tensor& combine, const Maybe& pos) {
+    const int64_t T = y.size(0), k = y.size(1), N = y.size(2);
+    Tensor out = torch::empty({T, N}, y.options().dtype(torch::kBFloat16));
+    check("mx_topk_combine_fwd", mx_topk_combine_fwd(y.data_ptr(), type_of(y), ptr<float>(combine),
+                                                     pos ? ptr<int32_t>(*pos) : nullptr, T, k, N, ptr<uint16_t>(out),
+                                                     stream_of(y)));
+    ctx->save_for_backward({y, combine, pos ? *pos : Tensor()});
+    return out;
+  }
+
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const variable_list saved = ctx->get_saved_variables();
+    const Tensor &y = saved[0], &combine = saved[1], &pos = saved[2], d = grads[0].contiguous();
+    Tensor dy, dcombine;
+    if (ctx->needs_input_grad(0)) dy = torch::empty_like(y);
+    if (ctx->needs_input_grad(1)) dcombine = torch::empty_like(combine);
+    check_backward("mx_topk_combine_bwd",
+                   mx_topk_combine_bwd(y.data_ptr(), type_of(y), ptr<float>(combine), ptr<int32_t>(pos), bf16(d),
+                                       y.size(0), y.size(1), y.size(2), ptr<void>(dy), ptr<float>(dcombine),
+                                       stream_of(y)));
+    return first_order({dy, dcombine, Tensor()});
+  }
+};
+
+}  // namespace
+
+PYBIND11_MODULE(_nodes, m) {
+  static py::object error;
+  // MXError of the package
+  m.def("set_error", [](py::object cls) { error = std::move(cls); });
+  py::register_exception_translator([](std::exception_ptr p) {
+    try {
+      if (p) std::rethrow_exception(p);
+    } catch (const Refused& r) {
+      PyErr_SetObject(error.ptr(), error(r.fn, r.status, r.text).ptr());
+    }
+  });
+  using no_gil = py::call_guard<py::gil_scoped_release>;
+  m.def("topk_router",
+        [](const Tensor& logits, int64_t k, int64_t score, const Maybe& bias, int64_t groups,
+           int64_t topk_groups, int64_t group_score, bool renormalize, double scale) {
+          const c10::DeviceGuard on(logits.device());
+          const variable_list out = Router::apply(logits, k, score, bias, groups, topk_groups, group_score,
+                                                  renormalize, scale);
+          return std::make_pair(out[0], out[1]);
+        },
+        no_gil());
+  m.def("swiglu",
+        [](const Tensor& gu) {
+          const c10::DeviceGuard on(gu.device());
+          return Swiglu::apply(gu, at::GradMode::is_enabled() && gu.requires_grad());
+        },
+        no_gil());
+  m.def("topk_combine",
+        [](const Tensor& y, const Tensor& combine, const Maybe& pos) {
+          const c10::DeviceGuard on(y.device());
+          return Combine::apply(y, combine, pos);
+        },
+        no_gil());
+}
