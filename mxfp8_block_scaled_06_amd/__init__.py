@@ -172,6 +172,24 @@ def load_library():
     return lib
 
 
+_bound = None
+
+
+def _native():
+    """_nodes.so (csrc/mx_nodes.cpp): autograd nodes, and calls that allocate their results."""
+    global _bound
+    if _bound is None:
+        load_library()
+        try:
+            from . import _nodes as nodes
+        except ImportError as e:
+            raise RuntimeError(f"_nodes.so is missing or does not fit this torch ({e}): build it with "
+                               "`python -m mxfp8_block_scaled_06_amd.build`") from e
+        nodes.set_error(MXError)
+        _bound = nodes
+    return _bound
+
+
 def version() -> str:
     return load_library().mx_version().decode()
 
@@ -1028,7 +1046,6 @@ def mx_dequantize(q, s, scale_layout: str = "rowmajor", out=None):
     in either layout (as mx_dequantize_fp4).  Exact from 2^-126 on; a NaN/Inf
     block's scale byte 255 gives NaN."""
     import torch
-    lib = load_library()
     _require(q, torch.uint8, "q")
     _require(s, torch.uint8, "s")
     B, R, C = _as3d(q)
@@ -1037,6 +1054,9 @@ def mx_dequantize(q, s, scale_layout: str = "rowmajor", out=None):
     if tuple(s.shape) != s_shape:
         raise ValueError(f"s must have shape {s_shape} for codes {tuple(q.shape)}, got {tuple(s.shape)}")
     _same_device(q, s)
+    if out is None:
+        return _native().dequantize(q, s, B, R, C, layout)
+    lib = load_library()
     out = _out(out, tuple(q.shape), torch.bfloat16, dev, "out")
     with _on(dev):
         _check("mx_dequantize", lib.mx_dequantize(_ptr(q), _ptr(s), B, R, C, layout, _ptr(out), _stream(dev)))
@@ -1224,10 +1244,11 @@ def mx_swiglu_quantize(gu, rows=None, q=None, s=None):
     grouped product.  rows int32 [M] (of mx_route): rows with a negative entry count as zeros, whatever they
     hold.  N % 128 == 0."""
     import torch
-    lib = load_library()
     M, N = _halves(gu)
     n = _rows_of(gu, rows, None, M)
-    dev = gu.device
+    if q is None and s is None:
+        return tuple(_native().swiglu_quantize(gu, rows, n))
+    lib, dev = load_library(), gu.device
     q = _out(q, (M, N), torch.uint8, dev, "q")
     s = _out(s, (N // 128, M, 4), torch.uint8, dev, "s")
     with _on(dev):
@@ -1249,12 +1270,13 @@ def mx_swiglu_quantize_fwd(gu, rows=None, combine=None, ldq: Optional[int] = Non
     Rows whose entry of `rows` is negative or past the items count as zeros.  M % 32 == 0, N % 128 == 0; ldq
     defaults to M rounded up to 128."""
     import torch
-    lib = load_library()
     M, N = _halves(gu)
     n = _rows_of(gu, rows, combine, M)
     if ldq is None:
         ldq = (M + 127) // 128 * 128
-    dev = gu.device
+    if q is None and s is None and q_t is None and s_t is None and kept is None and kept_s is None:
+        return tuple(_native().swiglu_quantize_fwd(gu, rows, combine, n, ldq))
+    lib, dev = load_library(), gu.device
     q = _out(q, (M, N), torch.uint8, dev, "q")
     s = _out(s, (N // 128, M, 4), torch.uint8, dev, "s")
     q_t = _out(q_t, (N, ldq), torch.uint8, dev, "q_t")
@@ -1280,7 +1302,6 @@ def mx_swiglu_quantize_bwd(dh, kept, kept_s, rows=None, pos=None, combine=None, 
     combine; None without it) each item's sum over N of dh * h.  rows and pos as mx_route returned them; items
     whose pos is negative get dcombine 0.  `ws`: uint8 scratch of mx_swiglu_quantize_workspace_bytes(M, N)."""
     import torch
-    lib = load_library()
     _require(dh, torch.bfloat16, "dh")
     if dh.dim() != 2:
         raise ValueError("dh must be [M, N]")
@@ -1288,13 +1309,11 @@ def mx_swiglu_quantize_bwd(dh, kept, kept_s, rows=None, pos=None, combine=None, 
     _kept(kept, kept_s, M, N, (2 * N // 128, M, 4))
     n = _rows_of(dh, rows, combine, M)
     _same_device(dh, kept, kept_s)
-    dev = dh.device
     if combine is None:
         if dcombine is not None:
             raise ValueError("dcombine goes with combine")
         pos = None
     else:
-        dcombine = _out(dcombine, tuple(combine.shape), torch.float32, dev, "dcombine")
         if (rows is None) != (pos is None):
             raise ValueError("rows and pos go together (both of mx_route)")
         if pos is not None:
@@ -1302,13 +1321,18 @@ def mx_swiglu_quantize_bwd(dh, kept, kept_s, rows=None, pos=None, combine=None, 
             _same_device(dh, pos)
             if pos.numel() != n:
                 raise ValueError(f"pos must hold one entry per item ({n}), got {pos.numel()}")
+    if ldq is None:
+        ldq = (M + 127) // 128 * 128
+    if q is None and s is None and q_t is None and s_t is None and dcombine is None and ws is None:
+        return tuple(_native().swiglu_quantize_bwd(dh, kept, kept_s, rows, pos, combine, n, ldq))
+    lib, dev = load_library(), dh.device
+    if combine is not None:
+        dcombine = _out(dcombine, tuple(combine.shape), torch.float32, dev, "dcombine")
         if ws is None:
             ws = torch.empty(max(mx_swiglu_quantize_workspace_bytes(M, N), 1), dtype=torch.uint8, device=dev)
         else:
             _require(ws, torch.uint8, "ws")
             _same_device(dh, ws)
-    if ldq is None:
-        ldq = (M + 127) // 128 * 128
     q = _out(q, (M, 2 * N), torch.uint8, dev, "q")
     s = _out(s, (2 * N // 128, M, 4), torch.uint8, dev, "s")
     q_t = _out(q_t, (2 * N, ldq), torch.uint8, dev, "q_t")

@@ -37,7 +37,7 @@ from __future__ import annotations
 
 import weakref
 
-from . import (MXError, _combine_sizes, _format, _halves, _on, _router_arguments, load_library, mx_grouped_gemm_mx,
+from . import (_combine_sizes, _format, _halves, _native, _on, _router_arguments, mx_grouped_gemm_mx,
                mx_grouped_gemm_mx_rows, mx_grouped_gemm_mxfp4, mx_grouped_mm_dgrad_fp4, mx_grouped_mm_dgrad_q,
                mx_grouped_mm_fwd_fp4, mx_grouped_mm_fwd_q, mx_quantize_dual, mx_quantize_dual_gather,
                mx_quantize_rowwise_gather, mx_quantize_weights, mx_quantize_weights_fp4, mx_route, mx_swiglu_quantize,
@@ -366,24 +366,6 @@ def mx_routed_experts(x, expert_idx, W, check: bool = True, weights=None, cache:
 def _wants_grad(*tensors):
     import torch
     return torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
-
-
-_nodes = None
-
-
-def _native():
-    """The autograd nodes of the router, the activation and the weighted sum (csrc/mx_nodes.cpp)."""
-    global _nodes
-    if _nodes is None:
-        load_library()
-        try:
-            from . import _nodes as nodes
-        except ImportError as e:
-            raise RuntimeError(f"_nodes.so is missing or does not fit this torch ({e}): build it with "
-                               "`python -m mxfp8_block_scaled_06_amd.build`") from e
-        nodes.set_error(MXError)
-        _nodes = nodes
-    return _nodes
 
 
 def mx_topk_router(logits, k, score="softmax", bias=None, groups=1, topk_groups=1, group_score="max",

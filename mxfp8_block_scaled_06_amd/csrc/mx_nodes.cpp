@@ -1,5 +1,6 @@
 // Autograd nodes of the router, the gated activation and the weighted sum over a
-// token's experts, on the C ABI of include/mxmoe.h.
+// token's experts, on the C ABI of include/mxmoe.h; and the calls between the
+// experts' products that allocate up to six results.
 //
 // Host time is what a small call costs.  A forward and a backward through a node
 // written in Python took 80 - 90 us where one of torch's own took 48: the backward
@@ -145,6 +146,59 @@ struct Combine : torch::autograd::Function<Combine> {
   }
 };
 
+Tensor bytes(const Tensor& like, std::initializer_list<int64_t> shape) {
+  return torch::empty(shape, like.options().dtype(torch::kByte));
+}
+
+Tensor dequantize(const Tensor& q, const Tensor& s, int64_t batch, int64_t rows, int64_t cols, int64_t layout) {
+  const c10::DeviceGuard on(q.device());
+  Tensor out = torch::empty(q.sizes(), q.options().dtype(torch::kBFloat16));
+  check("mx_dequantize", mx_dequantize(ptr<uint8_t>(q), ptr<uint8_t>(s), batch, rows, cols, (int)layout,
+                                       ptr<uint16_t>(out), stream_of(q)));
+  return out;
+}
+
+std::vector<Tensor> swiglu_quantize(const Tensor& gu, const Maybe& rows, int64_t n_items) {
+  const c10::DeviceGuard on(gu.device());
+  const int64_t M = gu.size(0), N = gu.size(1) / 2;
+  Tensor q = bytes(gu, {M, N}), s = bytes(gu, {N / 128, M, 4});
+  check("mx_swiglu_quantize", mx_swiglu_quantize(bf16(gu), rows ? ptr<int32_t>(*rows) : nullptr, n_items, M, N,
+                                                 ptr<uint8_t>(q), ptr<uint8_t>(s), stream_of(gu)));
+  return {q, s};
+}
+
+std::vector<Tensor> swiglu_quantize_fwd(const Tensor& gu, const Maybe& rows, const Maybe& combine, int64_t n_items,
+                                        int64_t ldq) {
+  const c10::DeviceGuard on(gu.device());
+  const int64_t M = gu.size(0), N = gu.size(1) / 2;
+  Tensor q = bytes(gu, {M, N}), s = bytes(gu, {N / 128, M, 4}), q_t = bytes(gu, {N, ldq});
+  Tensor s_t = bytes(gu, {ldq / 128, N, 4}), kept = bytes(gu, {M, 2 * N}), kept_s = bytes(gu, {2 * N / 128, M, 4});
+  check("mx_swiglu_quantize_fwd",
+        mx_swiglu_quantize_fwd(bf16(gu), rows ? ptr<int32_t>(*rows) : nullptr, combine ? ptr<float>(*combine) : nullptr,
+                               n_items, M, N, ldq, ptr<uint8_t>(q), ptr<uint8_t>(s), ptr<uint8_t>(q_t),
+                               ptr<uint8_t>(s_t), ptr<uint8_t>(kept), ptr<uint8_t>(kept_s), stream_of(gu)));
+  return {q, s, q_t, s_t, kept, kept_s};
+}
+
+std::vector<Maybe> swiglu_quantize_bwd(const Tensor& dh, const Tensor& kept, const Tensor& kept_s, const Maybe& rows,
+                                       const Maybe& pos, const Maybe& combine, int64_t n_items, int64_t ldq) {
+  const c10::DeviceGuard on(dh.device());
+  const int64_t M = dh.size(0), N = dh.size(1);
+  Tensor q = bytes(dh, {M, 2 * N}), s = bytes(dh, {2 * N / 128, M, 4}), q_t = bytes(dh, {2 * N, ldq});
+  Tensor s_t = bytes(dh, {ldq / 128, 2 * N, 4}), dcombine, ws;
+  if (combine) {
+    dcombine = torch::empty_like(*combine);
+    ws = bytes(dh, {(int64_t)mx_swiglu_quantize_workspace_bytes(M, N)});
+  }
+  check("mx_swiglu_quantize_bwd",
+        mx_swiglu_quantize_bwd(bf16(dh), ptr<uint8_t>(kept), ptr<uint8_t>(kept_s),
+                               rows ? ptr<int32_t>(*rows) : nullptr, pos ? ptr<int32_t>(*pos) : nullptr,
+                               combine ? ptr<float>(*combine) : nullptr, n_items, M, N, ldq, ptr<uint8_t>(q),
+                               ptr<uint8_t>(s), ptr<uint8_t>(q_t), ptr<uint8_t>(s_t), ptr<float>(dcombine),
+                               ptr<void>(ws), ws.defined() ? (size_t)ws.numel() : 0, stream_of(dh)));
+  return {q, s, q_t, s_t, dcombine.defined() ? Maybe(dcombine) : std::nullopt};
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_nodes, m) {
@@ -180,4 +234,8 @@ PYBIND11_MODULE(_nodes, m) {
           return Combine::apply(y, combine, pos);
         },
         no_gil());
+  m.def("dequantize", &dequantize, no_gil());
+  m.def("swiglu_quantize", &swiglu_quantize, no_gil());
+  m.def("swiglu_quantize_fwd", &swiglu_quantize_fwd, no_gil());
+  m.def("swiglu_quantize_bwd", &swiglu_quantize_bwd, no_gil());
 }

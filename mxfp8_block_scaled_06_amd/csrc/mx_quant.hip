@@ -729,8 +729,10 @@ hipError_t launch_quant_32x32(const uint16_t* x, int64_t rows_total, int64_t col
 }
 
 // ---------------------------------------------------------------------------
-// Values of MXFP8 codes, x viewed as [rows, cols]: one thread per 16 codes (half a
-// block), 1 + 1/32 bytes read and 2 written per element.
+// Values of MXFP8 codes, x viewed as [rows, cols]: one thread per 8 codes, so that
+// every store instruction writes a run of 1 KiB; 1 + 1/32 bytes read and 2 written per
+// element, both streamed: 16896 x 16384 in 142 us, 5.9 TB/s (16 codes a thread and
+// plain stores: 153 us).
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kRowThreads) void dequant_kernel(const uint8_t* __restrict__ q,
                                                               const uint8_t* __restrict__ s, int64_t pieces,
@@ -738,29 +740,24 @@ __global__ __launch_bounds__(kRowThreads) void dequant_kernel(const uint8_t* __r
                                                               uint16_t* __restrict__ out) {
   const int64_t i = wide_block() * kRowThreads + threadIdx.x;
   if (i >= pieces) return;
-  const uint32_t block = (uint32_t)(i >> 1);          // fewer than 2^32 of them
+  const uint32_t block = (uint32_t)(i >> 2);          // fewer than 2^32 of them
   int64_t at = block;
   if (gemm_rows) {
     const uint32_t row = block / kb, b = block - row * kb, e = row / gemm_rows, r = row - e * gemm_rows;
     at = ((int64_t)e * (kb / 4) + b / 4) * gemm_rows * 4 + (int64_t)r * 4 + b % 4;
   }
-  const v4i c = __builtin_nontemporal_load((const v4i*)(q + i * 16));
-  const float m = scale_from_e8m0(s[at]);
-  v4i o[2];
+  const v2i c = __builtin_nontemporal_load((const v2i*)(q + i * 8));
+  float x[8];
+  values8(c, scale_from_e8m0(s[at]), x);
+  v4i o;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float x[8];
-    values8((v2i){c[2 * h], c[2 * h + 1]}, m, x);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[h][j] = (int)pack_bf16x2_rne(x[2 * j], x[2 * j + 1]);
-  }
-  *(v4i*)(out + i * 16) = o[0];
-  *(v4i*)(out + i * 16 + 8) = o[1];
+  for (int j = 0; j < 4; ++j) o[j] = (int)pack_bf16x2_rne(x[2 * j], x[2 * j + 1]);
+  __builtin_nontemporal_store(o, (v4i*)(out + i * 8));
 }
 
 hipError_t launch_dequant(const uint8_t* q, const uint8_t* s, int64_t rows_total, int64_t cols, uint16_t* out,
                           int64_t gemm_rows_per_batch, hipStream_t st) {
-  const int64_t pieces = rows_total * (cols / 16);
+  const int64_t pieces = rows_total * (cols / 8);
   if (pieces == 0) return hipSuccess;
   hipLaunchKernelGGL(dequant_kernel, wide_grid((pieces + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0, st, q, s,
                      pieces, (uint32_t)(cols / 32), (uint32_t)gemm_rows_per_batch, out);
