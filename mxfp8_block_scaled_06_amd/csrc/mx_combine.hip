@@ -6,7 +6,13 @@
 // y [T, k, N] bf16 or fp32.  An item (t, j) whose entry of pos is negative was not
 // routed: its row of y is not read, its gradients are 0.  Streaming passes, bound by
 // HBM: forward k + 1 rows of a token, backward 2k + 1 (k = 8, bf16: 16 + 2 and 32 +
-// 2 bytes per column).
+// 2 bytes per column).  The k rows go past the caches, 16 bytes a lane, so that a
+// wave's load or store is one run of 1 KiB (fp32 at 32 bytes a lane wrote half lines:
+// 79 us instead of 62 for the backward below); the token's own row, which was just
+// written or is read next, goes through them.  T x k x N, forward and backward:
+//   8192 x 8 x 7168 bf16   173 us (6.1 TB/s)   337 us (5.9 TB/s)
+//   16384 x 2 x 7168 bf16  104 us (6.8 TB/s)   170 us (6.9 TB/s)
+//   2047 x 4 x 5120 fp32    33 us (5.8 TB/s)    62 us (5.7 TB/s)
 #include <type_traits>
 
 #include "mx_device.h"
@@ -17,57 +23,50 @@ namespace mxk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSlots = 4;      // slots whose loads go out together
 
-// Eight values of a row.
+// Sixteen bytes of a row: eight columns of bf16, four of fp32.
 template <class Y>
-struct Eight;
-template <>
-struct Eight<uint16_t> {
-  v4i w;
-  __device__ __forceinline__ void load(const uint16_t* p) { w = __builtin_nontemporal_load((const v4i*)p); }
-  __device__ __forceinline__ void zero() { w = (v4i){0, 0, 0, 0}; }
-  __device__ __forceinline__ float operator[](int i) const {
-    const uint32_t u = (uint32_t)w[i >> 1];
-    return i & 1 ? bf16hi(u) : bf16lo(u);
-  }
-};
-template <>
-struct Eight<float> {
-  v4i a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = __builtin_nontemporal_load((const v4i*)p);
-    b = __builtin_nontemporal_load((const v4i*)p + 1);
-  }
-  __device__ __forceinline__ void zero() { a = b = (v4i){0, 0, 0, 0}; }
-  __device__ __forceinline__ float operator[](int i) const { return __int_as_float(i < 4 ? a[i & 3] : b[i & 3]); }
-};
+constexpr int kCols = 16 / (int)sizeof(Y);
 
-__device__ __forceinline__ void store8(uint16_t* p, const float* x) {
-  *(v4i*)p = (v4i){(int)pack_bf16x2_rne(x[0], x[1]), (int)pack_bf16x2_rne(x[2], x[3]),
-                   (int)pack_bf16x2_rne(x[4], x[5]), (int)pack_bf16x2_rne(x[6], x[7])};
+template <int C>
+using Halves = std::conditional_t<C == 8, v4i, v2i>;   // C columns of bf16
+
+template <class V>
+__device__ __forceinline__ float half_at(V w, int i) {
+  const uint32_t u = (uint32_t)w[i >> 1];
+  return i & 1 ? bf16hi(u) : bf16lo(u);
 }
-__device__ __forceinline__ void store8(float* p, const float* x) {
-  typedef float v4f __attribute__((ext_vector_type(4)));
-  *(v4f*)p = (v4f){x[0], x[1], x[2], x[3]};
-  *((v4f*)p + 1) = (v4f){x[4], x[5], x[6], x[7]};
+__device__ __forceinline__ float column(v4i w, int i, const uint16_t*) { return half_at(w, i); }
+__device__ __forceinline__ float column(v4i w, int i, const float*) { return __int_as_float(w[i]); }
+
+template <int C>
+__device__ __forceinline__ Halves<C> pack_halves(const float* x) {
+  Halves<C> o;
+#pragma unroll
+  for (int i = 0; i < C / 2; ++i) o[i] = (int)pack_bf16x2_rne(x[2 * i], x[2 * i + 1]);
+  return o;
+}
+__device__ __forceinline__ v4i pack_columns(const float* x, const uint16_t*) { return pack_halves<8>(x); }
+__device__ __forceinline__ v4i pack_columns(const float* x, const float*) {
+  return (v4i){__float_as_int(x[0]), __float_as_int(x[1]), __float_as_int(x[2]), __float_as_int(x[3])};
 }
 
 }  // namespace
 
-// One thread per eight columns of a token.
+// One thread per 16 bytes of a token's rows, four slots' loads at a time.
 template <class Y>
 __global__ __launch_bounds__(kThreads) void combine_fwd_kernel(const Y* __restrict__ y, const float* __restrict__ combine,
                                                                const int32_t* __restrict__ pos, int64_t chunks, int k,
                                                                int64_t N, uint16_t* __restrict__ out) {
   const int64_t i = wide_block() * kThreads + threadIdx.x;
   if (i >= chunks) return;
-  const int64_t per_row = N / 8;
+  constexpr int C = kCols<Y>, kSlots = 4;
+  const int64_t per_row = N / C;
   const int64_t t = chunks <= (int64_t)UINT32_MAX ? (int64_t)((uint32_t)i / (uint32_t)per_row) : i / per_row;
-  const int64_t c = (i - t * per_row) * 8;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const int64_t c = (i - t * per_row) * C;
+  float acc[C] = {};
   for (int j0 = 0; j0 < k; j0 += kSlots) {
-    Eight<Y> x[kSlots];
+    v4i x[kSlots];
     float w[kSlots];
     bool on[kSlots];
 #pragma unroll
@@ -75,62 +74,66 @@ __global__ __launch_bounds__(kThreads) void combine_fwd_kernel(const Y* __restri
       const int64_t item = t * k + min(j0 + j, k - 1);
       on[j] = j0 + j < k && (pos == nullptr || pos[item] >= 0);
       w[j] = combine[item];
-      x[j].zero();
-      if (on[j]) x[j].load(y + item * N + c);
+      x[j] = (v4i){0, 0, 0, 0};
+      if (on[j]) x[j] = __builtin_nontemporal_load((const v4i*)(y + item * N + c));
     }
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) acc[u] = on[j] ? fmaf(w[j], x[j][u], acc[u]) : acc[u];
+      for (int u = 0; u < C; ++u) acc[u] = on[j] ? fmaf(w[j], column(x[j], u, y), acc[u]) : acc[u];
   }
-  store8(out + t * N + c, acc);
+  *(Halves<C>*)(out + t * N + c) = pack_halves<C>(acc);
 }
 
-// One workgroup per token and four slots.
-template <class Y>
-__global__ __launch_bounds__(kThreads) void combine_bwd_kernel(const Y* __restrict__ y, const float* __restrict__ combine,
-                                                               const int32_t* __restrict__ pos,
-                                                               const uint16_t* __restrict__ dout, int64_t T, int k,
-                                                               int64_t N, Y* __restrict__ dy,
-                                                               float* __restrict__ dcombine) {
-  __shared__ float part[kThreads / 64][kSlots];
+// One workgroup of W threads per token and S slots: all slots together up to eight, so
+// that dout is read once (4 a workgroup: 425 us instead of 373 for 8192 x 8 x 7168).
+// From three slots on 512 threads (8192 x 8 x 7168: 337 us, 353 with 256; 2047 x 4 x
+// 5120 fp32: 62 and 65); a token with fewer is too short for them (16384 x 1 x 5120:
+// 82 us, 74 with 256).
+template <class Y, int S, int W>
+__global__ __launch_bounds__(W) void combine_bwd_kernel(const Y* __restrict__ y, const float* __restrict__ combine,
+                                                        const int32_t* __restrict__ pos,
+                                                        const uint16_t* __restrict__ dout, int64_t T, int k,
+                                                        int64_t N, Y* __restrict__ dy,
+                                                        float* __restrict__ dcombine) {
+  constexpr int C = kCols<Y>;
+  __shared__ float part[W / 64][S];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int64_t t = wide_block();
   if (t >= T) return;
-  const int j0 = (int)blockIdx.z * kSlots, n = min(kSlots, k - j0);
-  float w[kSlots], dot[kSlots];
-  bool on[kSlots];
+  const int j0 = (int)blockIdx.z * S, n = min(S, k - j0);
+  float w[S], dot[S];
+  bool on[S];
 #pragma unroll
-  for (int j = 0; j < kSlots; ++j) {
+  for (int j = 0; j < S; ++j) {
     const int64_t item = t * k + min(j0 + j, k - 1);
     on[j] = j < n && (pos == nullptr || pos[item] >= 0);
     w[j] = combine[item];
     dot[j] = 0.f;
   }
-  for (int64_t c = tid * 8; c < N; c += kThreads * 8) {
-    Eight<uint16_t> d;
-    d.load(dout + t * N + c);
-    Eight<Y> x[kSlots];
+  for (int64_t c = tid * C; c < N; c += W * C) {
+    const Halves<C> d = *(const Halves<C>*)(dout + t * N + c);
+    v4i x[S];
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
-      x[j].zero();
-      if (on[j] && dcombine) x[j].load(y + (t * k + j0 + j) * N + c);
+    for (int j = 0; j < S; ++j) {
+      x[j] = (v4i){0, 0, 0, 0};
+      if (on[j] && dcombine) x[j] = __builtin_nontemporal_load((const v4i*)(y + (t * k + j0 + j) * N + c));
     }
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
+    for (int j = 0; j < S; ++j) {
       if (j >= n) continue;
-      float o[8];
+      float o[C];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        dot[j] = fmaf(d[u], x[j][u], dot[j]);
-        o[u] = on[j] ? w[j] * d[u] : 0.f;
+      for (int u = 0; u < C; ++u) {
+        dot[j] = fmaf(half_at(d, u), column(x[j], u, y), dot[j]);
+        o[u] = on[j] ? w[j] * half_at(d, u) : 0.f;
       }
-      if (dy) store8(dy + (t * k + j0 + j) * N + c, o);
+      if (dy) __builtin_nontemporal_store(pack_columns(o, y), (v4i*)(dy + (t * k + j0 + j) * N + c));
     }
   }
   if (!dcombine) return;
 #pragma unroll
-  for (int j = 0; j < kSlots; ++j) {
+  for (int j = 0; j < S; ++j) {
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) dot[j] += __shfl_xor(dot[j], s);
     if (lane == 0) part[wv][j] = dot[j];
@@ -139,14 +142,14 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(const Y* __restri
   if (tid < n) {
     float sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < kThreads / 64; ++v) sum += part[v][tid];
+    for (int v = 0; v < W / 64; ++v) sum += part[v][tid];
     bool routed = pos == nullptr || pos[t * k + j0 + tid] >= 0;
     dcombine[t * k + j0 + tid] = routed ? sum : 0.f;
   }
 }
 
 hipError_t launch_combine_fwd(const CombineArgs& a, uint16_t* out, hipStream_t st) {
-  const int64_t chunks = a.T * (a.N / 8);
+  const int64_t chunks = a.T * (a.N / (a.y_f32 ? kCols<float> : kCols<uint16_t>));
   if (chunks == 0) return hipSuccess;
   const dim3 grid = wide_grid((chunks + kThreads - 1) / kThreads);
   if (a.y_f32)
@@ -158,16 +161,30 @@ hipError_t launch_combine_fwd(const CombineArgs& a, uint16_t* out, hipStream_t s
   return hipGetLastError();
 }
 
+template <class Y, int S, int W>
+static void combine_bwd_grid(const CombineArgs& a, const uint16_t* dout, void* dy, float* dcombine, hipStream_t st) {
+  dim3 grid = wide_grid(a.T);
+  grid.z = (unsigned)((a.k + S - 1) / S);
+  hipLaunchKernelGGL((combine_bwd_kernel<Y, S, W>), grid, dim3(W), 0, st, (const Y*)a.y, a.combine, a.pos, dout, a.T,
+                     a.k, a.N, (Y*)dy, dcombine);
+}
+
+template <class Y>
+static void combine_bwd_slots(const CombineArgs& a, const uint16_t* dout, void* dy, float* dcombine, hipStream_t st) {
+  if (a.k > 4)
+    combine_bwd_grid<Y, 8, 512>(a, dout, dy, dcombine, st);
+  else if (a.k > 2)
+    combine_bwd_grid<Y, 4, 512>(a, dout, dy, dcombine, st);
+  else
+    combine_bwd_grid<Y, 2, 256>(a, dout, dy, dcombine, st);
+}
+
 hipError_t launch_combine_bwd(const CombineArgs& a, const uint16_t* dout, void* dy, float* dcombine, hipStream_t st) {
   if (a.T == 0) return hipSuccess;
-  dim3 grid = wide_grid(a.T);
-  grid.z = (unsigned)((a.k + kSlots - 1) / kSlots);
   if (a.y_f32)
-    hipLaunchKernelGGL(combine_bwd_kernel<float>, grid, dim3(kThreads), 0, st, (const float*)a.y, a.combine, a.pos, dout,
-                       a.T, a.k, a.N, (float*)dy, dcombine);
+    combine_bwd_slots<float>(a, dout, dy, dcombine, st);
   else
-    hipLaunchKernelGGL(combine_bwd_kernel<uint16_t>, grid, dim3(kThreads), 0, st, (const uint16_t*)a.y, a.combine, a.pos,
-                       dout, a.T, a.k, a.N, (uint16_t*)dy, dcombine);
+    combine_bwd_slots<uint16_t>(a, dout, dy, dcombine, st);
   return hipGetLastError();
 }
 
