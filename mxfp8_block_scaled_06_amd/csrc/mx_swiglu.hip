@@ -30,152 +30,12 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight bf16 of a block spread over a quad -> codes and the block's byte.
-__device__ __forceinline__ v2i quantize_quad(v4i x, uint32_t& byte) {
-  byte = e8m0_from_absbits(quad_max(absmax8(x)));
-  const float m = inv_scale_from_e8m0(byte == 0xFFu ? 127u : byte);
-  return byte == 0xFFu ? (v2i){0x7F7F7F7F, 0x7F7F7F7F} : quant8(x, m);
-}
-
-__device__ __forceinline__ void floats8(v4i x, float* out) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    out[2 * i] = bf16lo((uint32_t)x[i]);
-    out[2 * i + 1] = bf16hi((uint32_t)x[i]);
-  }
-}
-
-__device__ __forceinline__ v4i pack8(const float* x) {
-  return (v4i){(int)pack_bf16x2_rne(x[0], x[1]), (int)pack_bf16x2_rne(x[2], x[3]), (int)pack_bf16x2_rne(x[4], x[5]),
-               (int)pack_bf16x2_rne(x[6], x[7])};
-}
-
-// Row and chunk of eight columns of chunk `i`; 32-bit division where it fits.
-__device__ __forceinline__ void row_of(int64_t i, int64_t per_row, int64_t& row, int64_t& at) {
-  if (i <= (int64_t)UINT32_MAX && per_row <= (int64_t)UINT32_MAX) {
-    const uint32_t r = (uint32_t)i / (uint32_t)per_row;
-    row = r;
-    at = (uint32_t)i - r * (uint32_t)per_row;
-  } else {
-    row = i / per_row;
-    at = i - row * per_row;
-  }
-}
-
-// Gradients of eight gate and up values.
-__device__ __forceinline__ void grad8(const float* dh, const float* g, const float* u, float* dg, float* du) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const Sigmoid s = sigmoid_parts(g[i]);
-    dg[i] = scaled(s, s.m * fmaf(g[i], s.q, 1.f), dh[i] * u[i]);
-    du[i] = scaled(s, g[i] * s.m, dh[i]);
-  }
-}
-
-}  // namespace
-
-// One thread per eight columns of h.  A DPP quad holds a block of 32.
-template <bool KEEP>
-__global__ __launch_bounds__(kThreads) void swiglu_fwd_kernel(const uint16_t* __restrict__ gu, int64_t chunks,
-                                                              int64_t N, uint16_t* __restrict__ h,
-                                                              uint8_t* __restrict__ kept, uint8_t* __restrict__ kept_s) {
-  const int64_t i = wide_block() * kThreads + threadIdx.x;
-  if (i >= chunks) return;
-  int64_t row, c;
-  row_of(i, N / 8, row, c);
-  const uint16_t* src = gu + row * 2 * N + 8 * c;
-  const v4i gw = __builtin_nontemporal_load((const v4i*)src);
-  const v4i uw = __builtin_nontemporal_load((const v4i*)(src + N));
-  float g[8], u[8], o[8];
-  floats8(gw, g);
-  floats8(uw, u);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = silu_mul(g[j], u[j]);
-  *(v4i*)(h + row * N + 8 * c) = pack8(o);
-  if (KEEP) {
-    uint32_t gb, ub;
-    const v2i gq = quantize_quad(gw, gb), uq = quantize_quad(uw, ub);
-    uint8_t* dst = kept + row * 2 * N + 8 * c;
-    *(v2i*)dst = gq;
-    *(v2i*)(dst + N) = uq;
-    if ((c & 3) == 0) {
-      uint8_t* s = kept_s + row * (N / 16) + (c >> 2);
-      s[0] = (uint8_t)gb;
-      s[N / 32] = (uint8_t)ub;
-    }
-  }
-}
-
-__global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const uint16_t* __restrict__ dh,
-                                                              const uint8_t* __restrict__ kept,
-                                                              const uint8_t* __restrict__ kept_s, int64_t chunks,
-                                                              int64_t N, uint16_t* __restrict__ dgu) {
-  const int64_t i = wide_block() * kThreads + threadIdx.x;
-  if (i >= chunks) return;
-  int64_t row, c;
-  row_of(i, N / 8, row, c);
-  const v4i dw = __builtin_nontemporal_load((const v4i*)(dh + row * N + 8 * c));
-  const uint8_t* src = kept + row * 2 * N + 8 * c;
-  const v2i gq = __builtin_nontemporal_load((const v2i*)src);
-  const v2i uq = __builtin_nontemporal_load((const v2i*)(src + N));
-  const uint8_t* s = kept_s + row * (N / 16) + (c >> 2);
-  float d[8], g[8], u[8], dg[8], du[8];
-  floats8(dw, d);
-  values8(gq, scale_from_e8m0(s[0]), g);
-  values8(uq, scale_from_e8m0(s[N / 32]), u);
-  grad8(d, g, u, dg, du);
-  uint16_t* dst = dgu + row * 2 * N + 8 * c;
-  *(v4i*)dst = pack8(dg);
-  *(v4i*)(dst + N) = pack8(du);
-}
-
-// ---------------------------------------------------------------------------
-// Between two products of routed experts.  A workgroup of eight waves takes 128
-// rows and 128 columns of h; wave w rows 32 (w/2).., one block of the colwise
-// quantization, and columns 64 (w%2)..; lane l rows 4 (l/8) + i (i < 4) and eight
-// columns 8 (l%8)..: a quad holds a block of 32 columns, the lanes l%8 + 8j one of 32
-// rows.  Codes of the rows go straight out; those of the columns through LDS, and
-// out as whole lines.  Row r belongs to item rows[r]; a row with none (padding,
-// behind the last group) holds anything and counts as zeros.
-//
-// 4 rows a lane instead of 8 hold both of the backward's gradients in fp32 in 128
-// registers, so that two workgroups share a CU and one computes while the other
-// waits for memory.
-// ---------------------------------------------------------------------------
-namespace {
-
-constexpr int kTileRows = 128, kTileCols = 128, kTileThreads = 512, kLaneRows = 4;
 constexpr uint32_t kFarGate = 0x4280;       // bf16 bits of 64: below, sigmoid_near serves
 constexpr uint32_t kFarByte = 124;          // a block of this scale byte holds at most 448 * 2^-3 = 56
 
 // Conversions to E4M3 saturate from here on, to +-448 (bit 23 of the MODE register).
+// Called before the loads of what they convert, which keeps them behind it.
 __device__ __forceinline__ void saturate_conversions() { __builtin_amdgcn_s_setreg(1 | (23 << 6), 1); }
-
-struct Place {
-  int cp, rg, wr, wc, row, col;             // row and col: of the lane's first value within the tile
-  __device__ __forceinline__ Place() {
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    cp = lane & 7;
-    rg = lane >> 3;
-    wr = wv >> 1;
-    wc = wv & 1;
-    row = 32 * wr + kLaneRows * rg;
-    col = 64 * wc + 8 * cp;
-  }
-};
-
-struct ColCodes {
-  uint8_t codes[kTileCols * kTileRows];     // [column][row], see code_at
-  uint8_t scales[4 * kTileCols];            // [block][column]
-};
-
-// Where 16-byte slot s (16 rows) of a column lies.  Neighbouring groups of eight
-// columns take the halves of a 256-byte line in opposite order, and every second one
-// another slot: the writes of a wave (eight groups x eight lanes of 4 bytes) and the
-// reads (eight slots of eight columns) meet no bank twice.
-__device__ __forceinline__ int code_at(int col, int s) {
-  return (col ^ (col >> 3 & 1)) * kTileRows + 16 * (s ^ (2 * (col >> 4 & 3)));
-}
 
 // Scale bytes need the exponents of the largest magnitudes alone: two at a time, the
 // high halves of their fp32 bits packed in a dword.  A half from 0x7F80 on is not finite.
@@ -248,6 +108,174 @@ __device__ __forceinline__ uint32_t quantize2(const X& x, const X& y, uint32_t h
     bytes = (bx ? 0xFFu : bytes & 0xFFu) | (by ? 0xFF0000u : bytes & 0xFF0000u);
   }
   return bytes;
+}
+
+__device__ __forceinline__ void floats8(v4i x, float* out) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    out[2 * i] = bf16lo((uint32_t)x[i]);
+    out[2 * i + 1] = bf16hi((uint32_t)x[i]);
+  }
+}
+
+__device__ __forceinline__ v4i pack8(const float* x) {
+  return (v4i){(int)pack_bf16x2_rne(x[0], x[1]), (int)pack_bf16x2_rne(x[2], x[3]), (int)pack_bf16x2_rne(x[4], x[5]),
+               (int)pack_bf16x2_rne(x[6], x[7])};
+}
+
+// Row and chunk of eight columns of chunk `i`; 32-bit division where it fits.
+__device__ __forceinline__ void row_of(int64_t i, int64_t per_row, int64_t& row, int64_t& at) {
+  if (i <= (int64_t)UINT32_MAX && per_row <= (int64_t)UINT32_MAX) {
+    const uint32_t r = (uint32_t)i / (uint32_t)per_row;
+    row = r;
+    at = (uint32_t)i - r * (uint32_t)per_row;
+  } else {
+    row = i / per_row;
+    at = i - row * per_row;
+  }
+}
+
+// Eight codes -> their values (of a block of byte 255, which holds NaN, anything).
+__device__ __forceinline__ void finite8(v2i codes, uint32_t byte, float* out) {
+  const float scale = scale_bits(byte);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)codes[i], scale, false);
+    const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)codes[i], scale, true);
+    out[4 * i] = a[0];
+    out[4 * i + 1] = a[1];
+    out[4 * i + 2] = b[0];
+    out[4 * i + 3] = b[1];
+  }
+}
+
+}  // namespace
+
+// One thread per eight columns of h.  A DPP quad holds a block of 32.  The vector unit
+// has as much to do as HBM: the whole-range sigmoid, whose far branch a wave takes only
+// where one of its gates is beyond 64 (the same result for the others), conversions
+// that saturate by themselves and streamed stores took 16384 x 8192 forward from 217
+// to 172 us and backward from 212 to 171 us (6.3 TB/s; 1.08 GB each); 4099 x 2048 takes
+// 15 us each.
+template <bool KEEP>
+__global__ __launch_bounds__(kThreads) void swiglu_fwd_kernel(const uint16_t* __restrict__ gu, int64_t chunks,
+                                                              int64_t N, uint16_t* __restrict__ h,
+                                                              uint8_t* __restrict__ kept, uint8_t* __restrict__ kept_s) {
+  const int64_t i = wide_block() * kThreads + threadIdx.x;
+  if (i >= chunks) return;
+  saturate_conversions();
+  int64_t row, c;
+  row_of(i, N / 8, row, c);
+  const uint16_t* src = gu + row * 2 * N + 8 * c;
+  const v4i gw = __builtin_nontemporal_load((const v4i*)src);
+  const v4i uw = __builtin_nontemporal_load((const v4i*)(src + N));
+  float g[8], u[8], o[8];
+  floats8(gw, g);
+  floats8(uw, u);
+  const us2 mg = absmax8x2(gw), mu = absmax8x2(uw);
+  uint32_t highs = max((uint32_t)mg[0], (uint32_t)mg[1]) | max((uint32_t)mu[0], (uint32_t)mu[1]) << 16;
+  if (__any((highs & 0xFFFFu) >= kFarGate)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = silu_mul(g[j], u[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid_near(g[j]).m * u[j];
+  }
+  __builtin_nontemporal_store(pack8(o), (v4i*)(h + row * N + 8 * c));
+  if (KEEP) {
+    v2i gq, uq;
+    const uint32_t bytes = quantize2(gw, uw, quad_max2(highs), gq, uq);
+    uint8_t* dst = kept + row * 2 * N + 8 * c;
+    __builtin_nontemporal_store(gq, (v2i*)dst);
+    __builtin_nontemporal_store(uq, (v2i*)(dst + N));
+    if ((c & 3) == 0) {
+      uint8_t* s = kept_s + row * (N / 16) + (c >> 2);
+      s[0] = (uint8_t)bytes;
+      s[N / 32] = (uint8_t)(bytes >> 16);
+    }
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const uint16_t* __restrict__ dh,
+                                                              const uint8_t* __restrict__ kept,
+                                                              const uint8_t* __restrict__ kept_s, int64_t chunks,
+                                                              int64_t N, uint16_t* __restrict__ dgu) {
+  const int64_t i = wide_block() * kThreads + threadIdx.x;
+  if (i >= chunks) return;
+  int64_t row, c;
+  row_of(i, N / 8, row, c);
+  const v4i dw = __builtin_nontemporal_load((const v4i*)(dh + row * N + 8 * c));
+  const uint8_t* src = kept + row * 2 * N + 8 * c;
+  const v2i gq = __builtin_nontemporal_load((const v2i*)src);
+  const v2i uq = __builtin_nontemporal_load((const v2i*)(src + N));
+  const uint8_t* s = kept_s + row * (N / 16) + (c >> 2);
+  float d[8], g[8], u[8], dg[8], du[8];
+  floats8(dw, d);
+  const uint32_t gb = s[0], ub = s[N / 32];
+  finite8(gq, gb, g);
+  finite8(uq, ub, u);
+  if (__any(gb > kFarByte || ub == 0xFFu)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = gb == 0xFFu ? __builtin_nanf("") : g[j], y = ub == 0xFFu ? __builtin_nanf("") : u[j];
+      const Sigmoid p = sigmoid_parts(x);
+      dg[j] = scaled(p, p.m * fmaf(x, p.q, 1.f), d[j] * y);
+      du[j] = scaled(p, x * p.m, d[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const Sigmoid p = sigmoid_near(g[j]);
+      dg[j] = p.m * fmaf(g[j], p.q, 1.f) * (d[j] * u[j]);
+      du[j] = g[j] * p.m * d[j];
+    }
+  }
+  uint16_t* dst = dgu + row * 2 * N + 8 * c;
+  __builtin_nontemporal_store(pack8(dg), (v4i*)dst);
+  __builtin_nontemporal_store(pack8(du), (v4i*)(dst + N));
+}
+
+// ---------------------------------------------------------------------------
+// Between two products of routed experts.  A workgroup of eight waves takes 128
+// rows and 128 columns of h; wave w rows 32 (w/2).., one block of the colwise
+// quantization, and columns 64 (w%2)..; lane l rows 4 (l/8) + i (i < 4) and eight
+// columns 8 (l%8)..: a quad holds a block of 32 columns, the lanes l%8 + 8j one of 32
+// rows.  Codes of the rows go straight out; those of the columns through LDS, and
+// out as whole lines.  Row r belongs to item rows[r]; a row with none (padding,
+// behind the last group) holds anything and counts as zeros.
+//
+// 4 rows a lane instead of 8 hold both of the backward's gradients in fp32 in 128
+// registers, so that two workgroups share a CU and one computes while the other
+// waits for memory.
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kTileRows = 128, kTileCols = 128, kTileThreads = 512, kLaneRows = 4;
+
+struct Place {
+  int cp, rg, wr, wc, row, col;             // row and col: of the lane's first value within the tile
+  __device__ __forceinline__ Place() {
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    cp = lane & 7;
+    rg = lane >> 3;
+    wr = wv >> 1;
+    wc = wv & 1;
+    row = 32 * wr + kLaneRows * rg;
+    col = 64 * wc + 8 * cp;
+  }
+};
+
+struct ColCodes {
+  uint8_t codes[kTileCols * kTileRows];     // [column][row], see code_at
+  uint8_t scales[4 * kTileCols];            // [block][column]
+};
+
+// Where 16-byte slot s (16 rows) of a column lies.  Neighbouring groups of eight
+// columns take the halves of a 256-byte line in opposite order, and every second one
+// another slot: the writes of a wave (eight groups x eight lanes of 4 bytes) and the
+// reads (eight slots of eight columns) meet no bank twice.
+__device__ __forceinline__ int code_at(int col, int s) {
+  return (col ^ (col >> 3 & 1)) * kTileRows + 16 * (s ^ (2 * (col >> 4 & 3)));
 }
 
 // Byte b of `x` into byte i of `bytes`.
@@ -457,17 +485,8 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4)
     const uint32_t gb = gs[i] >> (8 * blk) & 0xFFu, ub = us[i] >> (8 * blk) & 0xFFu;
     float d[8], g[8], u[8];
     floats8(dw[i], d);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const v2f x = c & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)gq[i][c >> 1], scale_bits(gb), true)
-                          : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)gq[i][c >> 1], scale_bits(gb), false);
-      const v2f y = c & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)uq[i][c >> 1], scale_bits(ub), true)
-                          : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)uq[i][c >> 1], scale_bits(ub), false);
-      g[2 * c] = x[0];
-      g[2 * c + 1] = x[1];
-      u[2 * c] = y[0];
-      u[2 * c + 1] = y[1];
-    }
+    finite8(gq[i], gb, g);
+    finite8(uq[i], ub, u);
     float dot = 0.f;
     if (__any(gb > kFarByte || ub == 0xFFu)) {
 #pragma unroll
