@@ -507,6 +507,10 @@ def mx_moe_layer(x, expert_idx, combine, W13, W2, check: bool = True, weights=No
         raise ValueError("mx_moe_layer: k must be at least 1")
     if weights is not None and len(weights) != 2:
         raise ValueError("mx_moe_layer: weights must be the 4-tuples of W13 and W2")
+    if x.is_cuda:
+        with _on(x.device):
+            for leaf in (x, combine, W13, W2):
+                _native().check_capture(leaf)
     combine = combine.reshape(T, topk).contiguous()
     if T == 0:
         # no token, and zeros for the weights' gradients

@@ -952,7 +952,8 @@ mx_status check_swiglu_tiles(const char* fn, int64_t M, int64_t N, int64_t ldq, 
   if (train && (M % 32 != 0 || ldq % 128 != 0 || ldq < M))
     return fail(MX_ERR_SHAPE, "%s: M=%lld must be a multiple of 32 and ldq=%lld one of 128, >= M", fn, (long long)M,
                 (long long)ldq);
-  if ((train ? ldq : M) / 128 >= 65535) return fail(MX_ERR_SHAPE, "%s: too many rows for one launch", fn);
+  if ((train ? ldq : M) / 128 >= 65535 || N >= ((int64_t)1 << 30))
+    return fail(MX_ERR_SHAPE, "%s: too many rows or columns for one launch", fn);
   return MX_OK;
 }
 

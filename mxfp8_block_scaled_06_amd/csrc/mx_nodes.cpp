@@ -11,6 +11,7 @@
 // tensors here); the C ABI checks the rest, and its refusals become MXError.
 #include <torch/extension.h>
 
+#include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 
@@ -57,6 +58,23 @@ variable_list first_order(variable_list grads) {
   auto refuse = std::make_shared<torch::autograd::DelayedError>(
       "this gradient has no derivative of its own (the kernels compute first derivatives)", (int64_t)grads.size());
   return (*refuse)(std::move(grads));
+}
+
+// A leaf's gradient is accumulated on the stream on which the leaf first entered a
+// living graph.  Where that is not the stream being captured, a captured backward
+// would make a stream outside the capture wait for one inside, and the failure of
+// that ends the process: refuse such a leaf while it is still an ordinary error.  To be
+// called before the node is made, which takes the leaf into the new graph.
+void check_capture(const Tensor& t) {
+  if (!at::GradMode::is_enabled() || !t.requires_grad() || !t.is_leaf() ||
+      c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None)
+    return;
+  const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
+  if (!node) return;
+  const auto stream = node->stream();
+  TORCH_CHECK(!stream || stream->id() == c10::hip::getCurrentHIPStream(t.device().index()).id(),
+              "captured into a graph while a graph of the same leaf from another stream lives: its backward could not "
+              "be captured (drop the results of the eager calls first, or detach)");
 }
 
 struct Router : torch::autograd::Function<Router> {
@@ -217,6 +235,7 @@ PYBIND11_MODULE(_nodes, m) {
         [](const Tensor& logits, int64_t k, int64_t score, const Maybe& bias, int64_t groups,
            int64_t topk_groups, int64_t group_score, bool renormalize, double scale) {
           const c10::DeviceGuard on(logits.device());
+          check_capture(logits);
           const variable_list out = Router::apply(logits, k, score, bias, groups, topk_groups, group_score,
                                                   renormalize, scale);
           return std::make_pair(out[0], out[1]);
@@ -225,15 +244,19 @@ PYBIND11_MODULE(_nodes, m) {
   m.def("swiglu",
         [](const Tensor& gu) {
           const c10::DeviceGuard on(gu.device());
+          check_capture(gu);
           return Swiglu::apply(gu, at::GradMode::is_enabled() && gu.requires_grad());
         },
         no_gil());
   m.def("topk_combine",
         [](const Tensor& y, const Tensor& combine, const Maybe& pos) {
           const c10::DeviceGuard on(y.device());
+          check_capture(y);
+          check_capture(combine);
           return Combine::apply(y, combine, pos);
         },
         no_gil());
+  m.def("check_capture", &check_capture, no_gil());
   m.def("dequantize", &dequantize, no_gil());
   m.def("swiglu_quantize", &swiglu_quantize, no_gil());
   m.def("swiglu_quantize_fwd", &swiglu_quantize_fwd, no_gil());

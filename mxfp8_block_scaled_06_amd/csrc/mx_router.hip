@@ -226,7 +226,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_pick_kernel(const T*
   constexpr int kSlots = MX_MOE_MAX_TOPK / L ? MX_MOE_MAX_TOPK / L : 1;      // slots a lane holds
   constexpr float kInf = __builtin_inff();
   const int sub = threadIdx.x % L;
-  const int64_t token = (int64_t)blockIdx.x * (kRouterWaves * 64 / L) + threadIdx.x / L;
+  const int64_t token = wide_block() * (kRouterWaves * 64 / L) + threadIdx.x / L;
   const int64_t t = min(token, a.T - 1);
   const T* row = logits + t * a.E;
   const int e0 = sub * V;
@@ -662,7 +662,8 @@ __global__ __launch_bounds__(64) void router_bwd_kernel(const T* __restrict__ lo
                                                         RouterArgs a, int n, T* __restrict__ dlogits) {
   extern __shared__ float lds[];
   const int lane = threadIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.x * n;
+  const int64_t t0 = wide_block() * n;
+  if (t0 >= a.T) return;
   n = (int)min((int64_t)n, a.T - t0);
   const int slots = n * a.k, cells = n * a.E;
   float* row = lds;                               // [n][E] the chosen experts' part
@@ -768,7 +769,7 @@ template <class T>
 hipError_t launch_bwd(const RouterArgs& a, const float* dcombine, void* dlogits, hipStream_t st) {
   const int n = a.E <= kBwdCells / 64 ? 64 : a.E < kBwdCells ? kBwdCells / a.E : 1;
   const size_t bytes = (size_t)n * (a.E + 4 * a.k + 3) * sizeof(float);
-  hipLaunchKernelGGL((router_bwd_kernel<T>), dim3((unsigned)((a.T + n - 1) / n)), dim3(64), bytes, st, (const T*)a.logits,
+  hipLaunchKernelGGL((router_bwd_kernel<T>), wide_grid((a.T + n - 1) / n), dim3(64), bytes, st, (const T*)a.logits,
                      dcombine, a, n, (T*)dlogits);
   return hipGetLastError();
 }
@@ -790,7 +791,7 @@ template <int L, int V, class T>
 hipError_t launch_pick(const RouterArgs& a, hipStream_t st) {
   constexpr int by = std::is_same_v<T, float> ? kLogits : kExact;
   const int64_t per = kRouterWaves * 64 / L;
-  const dim3 grid((unsigned)((a.T + per - 1) / per)), block(kRouterWaves * 64);
+  const dim3 grid = wide_grid((a.T + per - 1) / per), block(kRouterWaves * 64);
   if (by_values(a))
     hipLaunchKernelGGL((router_pick_kernel<L, V, T, kValues>), grid, block, 0, st, (const T*)a.logits, a.bias, a);
   else

@@ -548,7 +548,7 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4)
 __global__ __launch_bounds__(kThreads) void swiglu_dcombine_kernel(SwigluArgs a, float* __restrict__ dcombine) {
   __shared__ float part[kThreads];
   const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t r = wide_block() * 64 + lane;
   const int64_t tiles = a.N / kTileCols;
   float sum = 0.f;
   if (r < a.M) {
@@ -607,7 +607,7 @@ hipError_t launch_swiglu_quantize_bwd(const SwigluArgs& a, float* dcombine, hipS
   }
   const int64_t n = a.M > a.n_items ? a.M : a.n_items;
   if (!dcombine || n == 0) return hipSuccess;
-  hipLaunchKernelGGL(swiglu_dcombine_kernel, dim3((unsigned)((n + 63) / 64)), dim3(kThreads), 0, st, a, dcombine);
+  hipLaunchKernelGGL(swiglu_dcombine_kernel, wide_grid((n + 63) / 64), dim3(kThreads), 0, st, a, dcombine);
   return hipGetLastError();
 }
 
