@@ -168,8 +168,11 @@ def test_second_derivatives_of_each_are_refused():
     for op, inputs, d in _ops(mx, torch):
         leaves = _leaves(inputs)
         grads = torch.autograd.grad(op(*leaves), leaves, d, create_graph=True)
+        total = sum(g.float().square().sum() for g in grads)
+        with pytest.raises(RuntimeError):         # not connected to the leaves
+            torch.autograd.grad(total, leaves, retain_graph=True)
         with pytest.raises(RuntimeError, match="no derivative"):
-            torch.autograd.grad(sum(g.float().square().sum() for g in grads), leaves)
+            total.backward()
 
 
 def test_strided_inputs_and_gradients():
