@@ -597,7 +597,7 @@ mx_status mx_swiglu_bwd(const uint16_t* dh, const uint8_t* kept, const uint8_t* 
  * whose entry of pos is negative get 0.  ws: mx_swiglu_quantize_workspace_bytes(M, N),
  * 256-byte aligned, needs no initialisation.
  *
- * All require N % 128 == 0, n_items < 2^31, fewer than 65535 * 128 rows; gu,
+ * All require N % 128 == 0, N < 2^30, n_items < 2^31, fewer than 65535 * 128 rows; gu,
  * dh, kept and codes 16-byte, the rest 4-byte aligned. */
 mx_status mx_swiglu_quantize(const uint16_t* gu, const int32_t* rows, int64_t n_items, int64_t M, int64_t N, uint8_t* q,
                              uint8_t* s, void* stream);

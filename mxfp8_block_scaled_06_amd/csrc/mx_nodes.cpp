@@ -5,7 +5,8 @@
 // Host time is what a small call costs.  A forward and a backward through a node
 // written in Python took 80 - 90 us where one of torch's own took 48: the backward
 // runs on autograd's thread, which takes the GIL and then walks Python objects that
-// the main thread has just used.  These nodes take 56 and need no GIL in the backward.
+// the main thread has just used.  These nodes take 40 - 49 and need no GIL in the
+// backward.
 //
 // The binding checks types, shapes and devices before it calls (contiguous GPU
 // tensors here); the C ABI checks the rest, and its refusals become MXError.

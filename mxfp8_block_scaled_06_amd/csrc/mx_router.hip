@@ -28,6 +28,12 @@
 // with a token where they are not (random logits: one in some hundred) does its choice
 // again in fp64.  router_walk_kernel takes other groups: one wave per token, expert v *
 // 64 + lane in register v, an arg-max per pick over all registers, c in fp64.
+//
+// What it reads and writes is little (4096 x 256 fp32: 4.5 MB, a microsecond); the time
+// is that of k dependent picks and, where values are compared, of the one token in a
+// wave that goes through fp64.  4096 x 256, 8 groups, top 8: 10 - 13 us (24 with one wave
+// per token and an arg-max over its registers for each pick); 65600 x 32, top 8: 7 - 9
+// (54); one token 2.2; the gradients 4 - 5 and 9 - 11 us.
 #include <type_traits>
 
 #include "mx_device.h"
@@ -655,8 +661,9 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_walk_kernel(const T*
 // Gradient of the logits (see mx_topk_router_bwd).  A wave takes `n` tokens, whose
 // slots and rows are runs of memory: a lane per slot, then one per token for the sum
 // over its slots, then one per slot again, which adds its part to the row in LDS (the
-// forward's ids are distinct: every cell gets one), and the rows leave 16 bytes a lane.  The softmax of a row needs no sum over it: its
-// largest slot's weight and logit give s[e] = p exp(l[e] - l).
+// forward's ids are distinct: every cell gets one), and the rows leave 16 bytes a lane.
+// The softmax of a row needs no sum over it: its largest slot's weight and logit give
+// s[e] = p exp(l[e] - l).
 template <class T>
 __global__ __launch_bounds__(64) void router_bwd_kernel(const T* __restrict__ logits, const float* __restrict__ dcombine,
                                                         RouterArgs a, int n, T* __restrict__ dlogits) {
@@ -801,6 +808,8 @@ hipError_t launch_pick(const RouterArgs& a, hipStream_t st) {
 
 template <class T>
 hipError_t launch_fwd(const RouterArgs& a, hipStream_t st) {
+  // Four experts a lane and as many lanes as that takes, so that few tokens share a wave:
+  // it waits for the one of them whose choice fp32 does not decide.
   if (a.E <= 32 && along_lanes(a, 4)) return launch_pick<8, 4, T>(a, st);
   if (a.E <= 64 && along_lanes(a, 4)) return launch_pick<16, 4, T>(a, st);
   if (a.E <= 128 && along_lanes(a, 4)) return launch_pick<32, 4, T>(a, st);
