@@ -594,7 +594,8 @@ mx_status mx_swiglu_bwd(const uint16_t* dh, const uint8_t* kept, const uint8_t* 
  * dcombine (float [n_items], or NULL) is each item's sum_n dh[n] h[n], h from the
  * checkpoint, in fp32 with a fixed order of additions; it needs pos (int32
  * [n_items], the `pos` of mx_route, the inverse of rows; NULL without rows) and a workspace: items
- * whose entry of pos is negative get 0.  ws: mx_swiglu_quantize_workspace_bytes(M, N),
+ * that pos gives no row, or one that is not theirs by rows, get 0 (an item with several
+ * rows: the sum of the one in pos).  ws: mx_swiglu_quantize_workspace_bytes(M, N),
  * 256-byte aligned, needs no initialisation.
  *
  * All require N % 128 == 0, N < 2^30, n_items < 2^31, fewer than 65535 * 128 rows; gu,

@@ -1060,7 +1060,7 @@ mx_status mx_swiglu_quantize_bwd(const uint16_t* dh, const uint8_t* kept, const 
   mxk::SwigluArgs a{};
   a.dh = dh;
   a.rows = rows;
-  a.pos = pos;
+  a.pos = rows ? pos : nullptr;
   a.combine = combine;
   a.kept = const_cast<uint8_t*>(kept);
   a.kept_s = const_cast<uint8_t*>(kept_s);

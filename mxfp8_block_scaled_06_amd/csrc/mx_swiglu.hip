@@ -546,8 +546,9 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4)
   store_columns(lds[1], n0, a.N + k0, 2 * a.N, a.ldq, a.q_t, a.s_t);
 }
 
-// dcombine[rows[r]] = sum over the column tiles of row r, in a fixed order; items
-// without a row get 0.  64 rows per workgroup, every fourth tile per wave.
+// dcombine[rows[r]] = sum over the column tiles of row r, in a fixed order, where pos
+// agrees; items without such a row get 0.  64 rows per workgroup, every fourth tile per
+// wave; 5 us for 33792 rows.
 __global__ __launch_bounds__(kThreads) void swiglu_dcombine_kernel(SwigluArgs a, float* __restrict__ dcombine) {
   __shared__ float part[kThreads];
   const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -561,9 +562,14 @@ __global__ __launch_bounds__(kThreads) void swiglu_dcombine_kernel(SwigluArgs a,
   part[threadIdx.x] = sum;
   __syncthreads();
   if (wv != 0) return;
-  if (r < a.n_items && a.pos && a.pos[r] < 0) dcombine[r] = 0.f;
+  // every item is written once, whatever rows and pos hold: by its row where the two agree, else here
+  if (r < a.n_items && a.pos) {
+    const int64_t row = a.pos[r];
+    if (row < 0 || row >= a.M || a.rows[row] != r) dcombine[r] = 0.f;
+  }
   const int item = item_of(a, r);
-  if (item >= 0) dcombine[item] = part[lane] + part[64 + lane] + part[128 + lane] + part[192 + lane];
+  if (item >= 0 && (!a.pos || a.pos[item] == r))
+    dcombine[item] = part[lane] + part[64 + lane] + part[128 + lane] + part[192 + lane];
 }
 
 // ---------------------------------------------------------------------------

@@ -188,6 +188,25 @@ def test_strided_inputs_and_gradients():
             assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_rows_and_pos_that_do_not_agree():
+    """An item with several rows takes the sum of the one that pos names; one whose pos leads elsewhere gets 0."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    M, N, n = 64, 256, 6
+    gu, dh = torch.randn((M, 2 * N), device="cuda:0").bfloat16(), torch.randn((M, N), device="cuda:0").bfloat16()
+    rows = torch.full((M,), -1, dtype=torch.int32)
+    rows[[0, 1, 2, 40, 63]] = torch.tensor([3, 0, 3, 1, 5], dtype=torch.int32)
+    pos = torch.tensor([1, 40, -1, 2, 7, 1 << 30], dtype=torch.int32)      # 4: a row without an item; 5: no row
+    rows, pos, w = rows.cuda(), pos.cuda(), torch.rand(n, device="cuda:0")
+    kept, kept_s = mx.mx_swiglu_quantize_fwd(gu, rows, w)[4:]
+    ones = torch.ones(M, device="cuda:0")
+    each = mx.mx_swiglu_quantize_bwd(dh, *mx.mx_swiglu_quantize_fwd(gu)[4:], combine=ones)[4]
+    for _ in range(3):
+        dw = mx.mx_swiglu_quantize_bwd(dh, kept, kept_s, rows, pos, w)[4]
+        want = torch.stack([each[1], each[40], 0 * each[0], each[2], 0 * each[0], 0 * each[0]])
+        assert torch.equal(dw, want)
+
+
 def _room(torch, gib):
     torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < gib * GIB:
