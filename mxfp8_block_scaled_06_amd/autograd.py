@@ -495,8 +495,8 @@ def mx_moe_layer(x, expert_idx, combine, W13, W2, check: bool = True, weights=No
     if tuple(W13.shape) != (E, 2 * N, K) or tuple(W2.shape) != (E, K, N):
         raise ValueError(f"mx_moe_layer: W13 must be [E, 2N, K={K}] and W2 [E, K={K}, N], got {tuple(W13.shape)} and "
                          f"{tuple(W2.shape)}")
-    if K % 128 or N % 128:
-        raise ValueError(f"mx_moe_layer: K={K} and N={N} must be multiples of 128")
+    if K % 128 or N % 128 or not K or not N or not E:
+        raise ValueError(f"mx_moe_layer: K={K} and N={N} must be positive multiples of 128, E={E} at least 1")
     if expert_idx.dtype != torch.int32 or combine.dtype != torch.float32:
         raise TypeError("mx_moe_layer: expert_idx must be int32 and combine float32")
     if expert_idx.dim() not in (1, 2) or expert_idx.shape[0] != T or expert_idx.shape != combine.shape:

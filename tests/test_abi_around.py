@@ -134,3 +134,11 @@ def test_binding_refuses():
     bias = torch.zeros(8, requires_grad=True)
     with pytest.raises(ValueError, match="no gradient"):
         mx.mx_topk_router(torch.zeros(4, 8), 2, bias=bias)
+
+
+def test_layer_refuses_empty_weights():
+    bf = torch.bfloat16
+    ids, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for E, K, N in ((0, 128, 128), (2, 0, 128), (2, 128, 0), (2, 128, 64)):
+        with pytest.raises(ValueError, match="positive multiples"):
+            mx.mx_moe_layer(torch.zeros(4, K, dtype=bf), ids, w, torch.zeros(E, 2 * N, K, dtype=bf), torch.zeros(E, K, N, dtype=bf))
