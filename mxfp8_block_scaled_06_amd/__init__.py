@@ -37,6 +37,7 @@ __all__ = [
 
 OP_FWD, OP_DGRAD, OP_WGRAD, OP_FWD_Q, OP_DGRAD_Q = 0, 1, 2, 3, 4
 SCALES_ROWMAJOR, SCALES_GEMM = 0, 1
+_LAYOUTS = {"rowmajor": SCALES_ROWMAJOR, "gemm": SCALES_GEMM}
 MOE_MAX_TOKENS, MOE_MAX_TOPK = 128, 32     # MX_MOE_MAX_TOKENS, MX_MOE_MAX_TOPK
 FORMATS = {"mxfp8": 0, "mxfp4": 1}    # MX_FMT_FP8, MX_FMT_FP4
 SCORES = {"softmax": 0, "sigmoid": 1}     # MX_SCORE_SOFTMAX, MX_SCORE_SIGMOID
@@ -176,7 +177,8 @@ _bound = None
 
 
 def _native():
-    """_nodes.so (csrc/mx_nodes.cpp): autograd nodes, and calls that allocate their results."""
+    """_nodes.so (csrc/mx_nodes.cpp): autograd nodes, and calls that allocate their results; each returns None
+    where an operand does not fit, for the checks here to say which."""
     global _bound
     if _bound is None:
         load_library()
@@ -1046,6 +1048,10 @@ def mx_dequantize(q, s, scale_layout: str = "rowmajor", out=None):
     in either layout (as mx_dequantize_fp4).  Exact from 2^-126 on; a NaN/Inf
     block's scale byte 255 gives NaN."""
     import torch
+    if out is None:
+        out = _native().dequantize(q, s, _LAYOUTS.get(scale_layout, -1))
+        if out is not None:
+            return out
     _require(q, torch.uint8, "q")
     _require(s, torch.uint8, "s")
     B, R, C = _as3d(q)
@@ -1054,8 +1060,6 @@ def mx_dequantize(q, s, scale_layout: str = "rowmajor", out=None):
     if tuple(s.shape) != s_shape:
         raise ValueError(f"s must have shape {s_shape} for codes {tuple(q.shape)}, got {tuple(s.shape)}")
     _same_device(q, s)
-    if out is None:
-        return _native().dequantize(q, s, B, R, C, layout)
     lib = load_library()
     out = _out(out, tuple(q.shape), torch.bfloat16, dev, "out")
     with _on(dev):
@@ -1156,6 +1160,10 @@ def mx_topk_router(logits, k: int, score: str = "softmax", bias=None, groups: in
     The choice is that of 64-bit scores, the weights are fp32.  Experts whose logit is -inf (or the lowest
     finite value of the type) are masked: score 0, chosen after all others; a token with no other expert gets
     weights 0.  E up to 1024, k up to MOE_MAX_TOPK, groups up to ROUTER_MAX_GROUPS."""
+    out = _native().topk_router(logits, k, SCORES.get(score, -1), bias, groups, topk_groups,
+                                GROUP_SCORES.get(group_score, -1), renormalize, scale)
+    if out is not None:
+        return out
     from .autograd import mx_topk_router as _f
     return _f(logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale)
 
@@ -1218,6 +1226,9 @@ def mx_swiglu(gu):
     The backward keeps gu in MXFP8 (2.06 bytes per element of h instead of 4) and is the gradient at the
     values kept: each gate and up value off by at most 1/16 of itself (or, in a block of 32 with a larger
     one, 2^-18 of the largest's power of two; up to 1/8 for values from 7/8 of the next power of two on)."""
+    out = _native().swiglu(gu)
+    if out is not None:
+        return out
     from .autograd import mx_swiglu as _f
     return _f(gu)
 
@@ -1244,10 +1255,12 @@ def mx_swiglu_quantize(gu, rows=None, q=None, s=None):
     grouped product.  rows int32 [M] (of mx_route): rows with a negative entry count as zeros, whatever they
     hold.  N % 128 == 0."""
     import torch
+    if q is None and s is None:
+        out = _native().swiglu_quantize(gu, rows)
+        if out is not None:
+            return out
     M, N = _halves(gu)
     n = _rows_of(gu, rows, None, M)
-    if q is None and s is None:
-        return tuple(_native().swiglu_quantize(gu, rows, n))
     lib, dev = load_library(), gu.device
     q = _out(q, (M, N), torch.uint8, dev, "q")
     s = _out(s, (N // 128, M, 4), torch.uint8, dev, "s")
@@ -1270,12 +1283,14 @@ def mx_swiglu_quantize_fwd(gu, rows=None, combine=None, ldq: Optional[int] = Non
     Rows whose entry of `rows` is negative or past the items count as zeros.  M % 32 == 0, N % 128 == 0; ldq
     defaults to M rounded up to 128."""
     import torch
+    if q is None and s is None and q_t is None and s_t is None and kept is None and kept_s is None:
+        out = _native().swiglu_quantize_fwd(gu, rows, combine, ldq)
+        if out is not None:
+            return out
     M, N = _halves(gu)
     n = _rows_of(gu, rows, combine, M)
     if ldq is None:
         ldq = (M + 127) // 128 * 128
-    if q is None and s is None and q_t is None and s_t is None and kept is None and kept_s is None:
-        return tuple(_native().swiglu_quantize_fwd(gu, rows, combine, n, ldq))
     lib, dev = load_library(), gu.device
     q = _out(q, (M, N), torch.uint8, dev, "q")
     s = _out(s, (N // 128, M, 4), torch.uint8, dev, "s")
@@ -1302,6 +1317,10 @@ def mx_swiglu_quantize_bwd(dh, kept, kept_s, rows=None, pos=None, combine=None, 
     combine; None without it) each item's sum over N of dh * h.  rows and pos as mx_route returned them; items
     whose pos is negative get dcombine 0.  `ws`: uint8 scratch of mx_swiglu_quantize_workspace_bytes(M, N)."""
     import torch
+    if q is None and s is None and q_t is None and s_t is None and dcombine is None and ws is None:
+        out = _native().swiglu_quantize_bwd(dh, kept, kept_s, rows, pos, combine, ldq)
+        if out is not None:
+            return out
     _require(dh, torch.bfloat16, "dh")
     if dh.dim() != 2:
         raise ValueError("dh must be [M, N]")
@@ -1323,8 +1342,6 @@ def mx_swiglu_quantize_bwd(dh, kept, kept_s, rows=None, pos=None, combine=None, 
                 raise ValueError(f"pos must hold one entry per item ({n}), got {pos.numel()}")
     if ldq is None:
         ldq = (M + 127) // 128 * 128
-    if q is None and s is None and q_t is None and s_t is None and dcombine is None and ws is None:
-        return tuple(_native().swiglu_quantize_bwd(dh, kept, kept_s, rows, pos, combine, n, ldq))
     lib, dev = load_library(), dh.device
     if combine is not None:
         dcombine = _out(dcombine, tuple(combine.shape), torch.float32, dev, "dcombine")
@@ -1403,6 +1420,9 @@ def mx_topk_combine(y, combine, pos=None):
     y bf16 or fp32 [T, k, N] (what mx_routed_experts returns for a top-k router) and combine fp32 [T, k].
     Summed in fp32 in slot order and rounded once.  pos int32 [T * k] (of mx_route): items with a negative
     entry were not routed; their rows are not read, add nothing and get zero gradients.  N % 8 == 0."""
+    out = _native().topk_combine(y, combine, pos)
+    if out is not None:
+        return out
     from .autograd import mx_topk_combine as _f
     return _f(y, combine, pos)
 
