@@ -1159,7 +1159,7 @@ def mx_topk_router(logits, k: int, score: str = "softmax", bias=None, groups: in
     experts; a group counts with its largest c (group_score="max") or the sum of its two largest ("top2").
     The choice is that of 64-bit scores, the weights are fp32.  Experts whose logit is -inf (or the lowest
     finite value of the type) are masked: score 0, chosen after all others; a token with no other expert gets
-    weights 0.  E up to 1024, k up to MOE_MAX_TOPK, groups up to ROUTER_MAX_GROUPS."""
+    weights 0.  E up to 1024, k up to MOE_MAX_TOPK, groups up to ROUTER_MAX_GROUPS, scale in [2^-64, 2^64]."""
     out = _native().topk_router(logits, k, SCORES.get(score, -1), bias, groups, topk_groups,
                                 GROUP_SCORES.get(group_score, -1), renormalize, scale)
     if out is not None:

@@ -858,8 +858,9 @@ mx_status check_router(const char* fn, int logits_type, int64_t T, int64_t E, in
   if (k < 1 || k > MX_MOE_MAX_TOPK || k > E)
     return fail(MX_ERR_SHAPE, "%s: k=%lld outside [1, %d], or more than the %lld experts", fn, (long long)k,
                 MX_MOE_MAX_TOPK, (long long)E);
-  if (!(scale > 0.f) || !(scale <= 3.402823466e38f))
-    return fail(MX_ERR_SHAPE, "%s: scale must be positive and finite (got %g)", fn, (double)scale);
+  // the gradient takes scores back from the weights: these may not leave fp32's normal range before the scores do
+  if (!(scale >= 0x1p-64f) || !(scale <= 0x1p64f))
+    return fail(MX_ERR_SHAPE, "%s: scale must be positive and finite, in [2^-64, 2^64] (got %g)", fn, (double)scale);
   return MX_OK;
 }
 

@@ -81,3 +81,10 @@ def test_slots_of_a_token_share_a_workgroup_up_to_eight():
     for k, slots in ((1, 1), (2, 1), (4, 1), (8, 1), (9, 2), (1024, 128)):
         call, = record([("mx_topk_combine_bwd", (P, BF16, P, P, P, 7, k, 128, P, P, None))])
         assert tuple(call.launches[0].grid) == (7, 1, slots)
+
+
+def test_scales_from_which_no_score_comes_back_are_refused():
+    for scale, status in ((2.0 ** -64, 0), (2.0 ** 64, 0), (2.0 ** -65, 2), (2.0 ** 65, 2), (1e-45, 2), (-1.0, 2), (float("nan"), 2)):
+        for call in record([("mx_topk_router_fwd", (P, BF16, P, 4, 32, 8, 0, 1, 1, 0, 1, scale, P, P, None)),
+                            ("mx_topk_router_bwd", (P, BF16, P, P, P, 4, 32, 8, 0, 1, scale, P, None))]):
+            assert call.status == status and bool(call.launches) == (status == 0), (scale, call.text)
