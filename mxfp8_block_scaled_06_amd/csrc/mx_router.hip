@@ -391,7 +391,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_pick_kernel(const T*
           x[v] = a.score == MX_SCORE_SOFTMAX ? x[v] / sum : 1. / (1. + exp(-(double)l[v]));
           if (bias != nullptr && e0 + v < a.E) x[v] += (double)bias[e0 + v];
         } else {
-          x[v] = (double)l[v];
+          x[v] = (double)l[v] + 0.;       // as c: bits are compared below
         }
         x[v] = (live >> v & 1) && x[v] > kLow ? x[v] : kLow;
         open |= e0 + v < a.E ? 1u << v : 0u;

@@ -280,3 +280,19 @@ def test_many_tokens_against_fp64(E, groups):
                     c = c.masked_fill(~on.repeat_interleave(E // groups, 1), -float("inf"))
                 want = torch.sort(c, dim=1, descending=True, stable=True).indices[:, :k]
                 assert torch.equal(ids.long(), want), (dtype, score, gs)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_zeros_of_either_sign_are_equal(dtype):
+    """-0.0 beside +0.0, as logits times a mask of zeros and ones hold them: one value, so the lowest index,
+    whichever lanes have them."""
+    require_gpu()
+    rng = np.random.default_rng(11)
+    for E, k, groups in ((16, 1, 1), (40, 6, 1), (256, 8, 1), (256, 8, 8), (96, 5, 4), (60, 4, 4), (512, 8, 16), (1024, 32, 1)):
+        l = -np.abs(_logits(rng, 40, E, dtype))
+        at = rng.random(l.shape) < 0.5
+        l[at] = rng.choice(np.array([-0.0, 0.0], np.float32), size=int(at.sum()))
+        l[0] = np.where(np.arange(E) < E // 4, -0.0, 0.0)
+        l[1] = np.where(np.arange(E) < E // 4, 0.0, -0.0)
+        for score in ("softmax", "sigmoid"):
+            _check(l, dtype, k, rng, score=score, groups=groups, topk_groups=max(1, groups // 2))
