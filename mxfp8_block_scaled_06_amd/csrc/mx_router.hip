@@ -318,9 +318,12 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_pick_kernel(const T*
       m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
       m1 = fmaxf(m1, o1);
     }
-    const float value = a.group_top2 && m2 > -kInf ? m1 + m2 : m1;
-    // how many groups are better, and between which numbers that lies
-    const float far = 2.f * tol + 5.f * rel * fabsf(value), least = value - far, most = value + far;
+    const bool two = a.group_top2 && m2 > -kInf;
+    const float value = two ? m1 + m2 : m1;
+    // how many groups are better, and between which numbers that lies: both c round to 2^-24
+    // of themselves, which may be much more than that of a sum in which they cancel
+    const float far = 2.f * tol + 5.f * rel * fabsf(m1) + (two ? 5.f * rel * fabsf(m2) : 0.f);
+    const float least = value - far, most = value + far;
     const int mine = e0 / n, first = (threadIdx.x & 63) - sub;
     int better = 0, surely = 0, maybe = -1;
     for (int g = 0; g < a.groups; ++g) {
@@ -331,9 +334,11 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_pick_kernel(const T*
         maybe += o >= least;
       }
     }
-    // (a group of masked experts alone is behind every other for certain)
-    unsure = unsure || (BY == kValues && e0 < a.E && value > -kInf &&
-                        (better < a.topk_groups ? maybe >= a.topk_groups : surely < a.topk_groups));
+    // (a group of masked experts alone is behind every other for certain; a sum that leaves
+    // fp32's range is not)
+    unsure = unsure || (BY == kValues && e0 < a.E && m1 > -kInf &&
+                        (!(fabsf(value) < kInf) ||
+                         (better < a.topk_groups ? maybe >= a.topk_groups : surely < a.topk_groups)));
     if (better >= a.topk_groups) {
 #pragma unroll
       for (int v = 0; v < V; ++v) key[v] = 0;

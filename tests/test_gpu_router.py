@@ -296,3 +296,43 @@ def test_zeros_of_either_sign_are_equal(dtype):
         l[1] = np.where(np.arange(E) < E // 4, 0.0, -0.0)
         for score in ("softmax", "sigmoid"):
             _check(l, dtype, k, rng, score=score, groups=groups, topk_groups=max(1, groups // 2))
+
+
+@pytest.mark.parametrize("E,groups", [(32, 8), (256, 8), (512, 16)])
+def test_group_sums_that_cancel(E, groups):
+    """A large positive c and a large negative one in every group: their sums lie far below what fp32 keeps of
+    them.  Every choice that of the 64-bit sums."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    gen = torch.Generator(device="cuda:0").manual_seed(E)
+    n = E // groups
+    for big in (1e3, 1e5, 3e38):
+        # (at 3e38 the two largest of every group add up to infinity in fp32)
+        bias = torch.full((groups, n), -big, device="cuda:0")
+        bias[:, 0] = big
+        if big > 1e30:
+            bias = -bias * (1 + torch.arange(groups, device="cuda:0") / 256).unsqueeze(1)
+        bias = bias.reshape(-1)
+        for score in ("softmax", "sigmoid"):
+            l = torch.randn((40000, E), generator=gen, device="cuda:0") * 1.5
+            ids, _ = mx.mx_topk_router(l, 1, score, bias, groups, 1, "top2")
+            d = l.double()
+            c = (torch.softmax(d, 1) if score == "softmax" else torch.sigmoid(d)) + bias.double()
+            value = torch.sort(c.view(-1, groups, n), dim=2, descending=True).values[..., :2].sum(2)
+            best = torch.sort(value, dim=1, descending=True, stable=True).indices[:, :1]
+            c = c.view(-1, groups, n).gather(1, best.unsqueeze(2).expand(-1, 1, n)).squeeze(1)
+            want = best * n + torch.sort(c, dim=1, descending=True, stable=True).indices[:, :1]
+            assert torch.equal(ids.long(), want), (big, score, int((ids.long() != want).sum()))
+
+
+def test_group_sums_below_fp32():
+    """Biases of the lowest value: a group of such experts alone has a sum below fp32's range and comes before a
+    group of masked ones."""
+    require_gpu()
+    rng = np.random.default_rng(12)
+    l = _logits(rng, 9, 32, "fp32")
+    l[:, :8] = -np.inf
+    bias = np.zeros(32, np.float32)
+    bias[8:24] = LOWEST["fp32"]
+    for kept, k in ((1, 4), (2, 12), (3, 12)):
+        _check(l, "fp32", k, rng, bias, score="sigmoid", groups=4, topk_groups=kept, group_score="top2")
