@@ -88,13 +88,14 @@ def router_grad(logits, lowest, ids, dw, score, renormalize, scale):
     out, mag = np.zeros_like(l), np.zeros_like(l)
     for t in range(T):
         i, si = ids[t], s[t, ids[t]]
+        rest = sigmoid(-l[t, i])                    # 1 - s, of which nothing is lost where s is close to 1
         g = scale * np.asarray(dw[t], np.float64)
         if renormalize:
             # through the shares, whose derivative by the logarithm of score m is p_j (delta - p_m)
             d, m = p[t] * (g - (g * p[t]).sum()), p[t] * (np.abs(g) + (np.abs(g) * p[t]).sum())
-            out[t, i], mag[t, i] = (d * (1 - si), m) if score == "sigmoid" else (d, m)
+            out[t, i], mag[t, i] = (d * rest, m * rest) if score == "sigmoid" else (d, m)
         elif score == "sigmoid":
-            out[t, i], mag[t, i] = g * si * (1 - si), np.abs(g) * si
+            out[t, i], mag[t, i] = g * si * rest, np.abs(g) * si * rest
         else:
             ds, dm = np.zeros(E), np.zeros(E)
             ds[i], dm[i] = g, np.abs(g)

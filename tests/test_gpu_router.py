@@ -336,3 +336,28 @@ def test_group_sums_below_fp32():
     bias[8:24] = LOWEST["fp32"]
     for kept, k in ((1, 4), (2, 12), (3, 12)):
         _check(l, "fp32", k, rng, bias, score="sigmoid", groups=4, topk_groups=kept, group_score="top2")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_gradient_of_sure_experts(dtype):
+    """Sigmoid scores next to 1: their gradient is s (1 - s), of which fp32's 1 - s leaves nothing from a logit of
+    17 on.  The weight at 2^-19, the logit's own sigmoid at 2^-21, two products at 2^-24: below REL_D of the value."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    rng = np.random.default_rng(13)
+    for scale in (1.0, 2.5, 2.0 ** -20):
+        l = (rng.random(size=(50, 24)).astype(np.float32) * 32 - 2).astype(np.float32)
+        x = _dev(l, dtype).requires_grad_()
+        v = x.detach().cpu().double().numpy()
+        ids, w = mx.mx_topk_router(x, 6, "sigmoid", renormalize=False, scale=scale)
+        dw = rng.normal(size=(50, 6)).astype(np.float32)
+        dl, = torch.autograd.grad(w, x, torch.from_numpy(dw).to("cuda:0"))
+        at = ids.cpu().numpy()
+        p = np.take_along_axis(v, at, 1)
+        want = np.zeros(v.shape)
+        np.put_along_axis(want, at, scale * dw.astype(np.float64) / ((1 + np.exp(-p)) * (1 + np.exp(p))), 1)
+        tol = REL_D * np.abs(want)
+        if dtype == "bf16":
+            tol = tol + 0.5 * ulp_bf16(np.abs(want) + tol)
+        err = np.abs(dl.cpu().double().numpy() - want)
+        assert (err <= tol + TINY).all(), (err / (tol + TINY)).max()
