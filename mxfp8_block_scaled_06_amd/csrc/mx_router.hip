@@ -704,7 +704,7 @@ __global__ __launch_bounds__(64) void router_bwd_kernel(const T* __restrict__ lo
       }
     }
     share[i] = p;
-    grad[i] = dcombine[t0 * a.k + i];
+    grad[i] = w != 0.f ? dcombine[t0 * a.k + i] : 0.f;      // none from a masked expert's slot, whatever comes in
     factor[i] = x;
     id[i] = in ? e : -1;
   }
@@ -730,13 +730,12 @@ __global__ __launch_bounds__(64) void router_bwd_kernel(const T* __restrict__ lo
   for (int i = lane; i < slots; i += 64) {
     const int t = (uint32_t)i / (uint32_t)a.k;
     const float g = grad[i];
-    const float d = dense ? g : factor[i] * (a.renormalize ? g - ref[3 * t] : g);
+    const float x = factor[i], d = dense ? g : share[i] == 0.f ? 0.f : x * (a.renormalize ? g - ref[3 * t] : g);
     if (id[i] >= 0) atomicAdd(row + t * a.E + id[i], d);
   }
   __syncthreads();
   auto softmax_grad = [&](const float* r, float l, float g) {
-    const float s = l <= Logits<T>::lowest || r[2] == 0.f ? 0.f : exp32(l - r[1]) * r[2];
-    return s * (a.scale * (g - r[0]));
+    return l <= Logits<T>::lowest || r[2] == 0.f ? 0.f : exp32(l - r[1]) * r[2] * (a.scale * (g - r[0]));
   };
   const T* src = logits + t0 * a.E;
   T* dst = dlogits + t0 * a.E;

@@ -361,3 +361,31 @@ def test_gradient_of_sure_experts(dtype):
             tol = tol + 0.5 * ulp_bf16(np.abs(want) + tol)
         err = np.abs(dl.cpu().double().numpy() - want)
         assert (err <= tol + TINY).all(), (err / (tol + TINY)).max()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_masked_experts_pass_no_gradient(score, renormalize, dtype):
+    """Slots of masked experts, whose weights are 0: whatever comes in as their gradient (NaN and infinity of a
+    padding token), the logits' gradient is that of zeros there, and 0 at the masked experts."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    rng = np.random.default_rng(14)
+    l = _logits(rng, 12, 20, dtype)
+    l[:, 5:] = np.where(rng.random((12, 15)) < 0.5, -np.inf, LOWEST[dtype])        # five left for six slots
+    l[:3] = -np.inf                                                               # and none in padding tokens
+    x = _dev(l, dtype)
+    ids, w = mx.mx_topk_router_fwd(x, 6, score, renormalize=renormalize)
+    dw = torch.from_numpy(rng.normal(size=(12, 6)).astype(np.float32)).to("cuda:0")
+    off = torch.from_numpy(np.take_along_axis(l <= LOWEST[dtype], ids.cpu().numpy(), 1)).to("cuda:0")
+    assert (w[off] == 0).all() and off[:3].all() and off[3:].sum() == 9
+    want = mx.mx_topk_router_bwd(x, ids, w, dw.masked_fill(off, 0.0), score, renormalize)
+    assert (want[x <= LOWEST[dtype]] == 0).all() and want[3:, :5].any()
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        got = mx.mx_topk_router_bwd(x, ids, w, dw.masked_fill(off, bad), score, renormalize)
+        assert torch.equal(got, want), bad
+    # a gradient that is not finite where it counts stays in its token's experts
+    dw[4, 0] = float("nan")
+    got = mx.mx_topk_router_bwd(x, ids, w, dw, score, renormalize)
+    assert torch.isnan(got[4, ids[4, 0]]) and (got[4, 5:] == 0).all() and torch.equal(got[5:], want[5:])
