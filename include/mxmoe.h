@@ -531,7 +531,8 @@ mx_status mx_moe_few_tokens(const uint16_t* x, const int32_t* expert_idx, const 
  * The ids of a token are distinct and lie in [0, E) whatever the logits hold.
  * Requires 0 <= T < 2^31, 1 <= E <= 1024, 1 <= k <= MX_MOE_MAX_TOPK, 1 <= groups <=
  * MX_ROUTER_MAX_GROUPS, groups dividing E, topk_groups * (E/groups) >= k, scale
- * in [2^-64, 2^64].  logits 16-byte, the rest 4-byte aligned. */
+ * in [2^-64, 2^64].  logits (and dlogits below) aligned to four of their elements,
+ * or to one where E % 4 != 0 (so rows of them from any token on), the rest to 4 bytes. */
 mx_status mx_topk_router_fwd(const void* logits, int logits_type, const float* bias, int64_t T, int64_t E, int64_t k,
                              int score, int64_t groups, int64_t topk_groups, int group_score, int renormalize,
                              float scale, int32_t* expert_idx, float* combine, void* stream);

@@ -864,6 +864,14 @@ mx_status check_router(const char* fn, int logits_type, int64_t T, int64_t E, in
   return MX_OK;
 }
 
+// The router reads and writes rows of a multiple of four experts four logits at a time, others
+// one by one.
+bool row_aligned(const void* p, int logits_type, int64_t E) {
+  const size_t size = logits_type == MX_F32 ? 4 : 2;
+  return aligned(p, E % 4 == 0 ? 4 * size : size);
+}
+constexpr const char* kRowAlign = "aligned to four of their elements, or to one where E is no multiple of four";
+
 }  // namespace
 
 extern "C" {
@@ -885,8 +893,10 @@ mx_status mx_topk_router_fwd(const void* logits, int logits_type, const float* b
                 MX_GROUP_MAX, MX_GROUP_TOP2, group_score);
   if (T == 0) return MX_OK;
   if (!logits || !expert_idx || !combine) return fail(MX_ERR_NULL, "%s: null pointer", fn);
-  if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(expert_idx, 4) || !aligned(combine, 4))
-    return fail(MX_ERR_ALIGN, "%s: logits must be 16-byte, the other tensors 4-byte aligned", fn);
+  if (!row_aligned(logits, logits_type, E))
+    return fail(MX_ERR_ALIGN, "%s: logits must be %s", fn, kRowAlign);
+  if (!aligned(bias, 4) || !aligned(expert_idx, 4) || !aligned(combine, 4))
+    return fail(MX_ERR_ALIGN, "%s: bias, expert_idx and combine must be 4-byte aligned", fn);
   mxk::RouterArgs a{};
   a.logits = logits;
   a.bias = bias;
@@ -913,9 +923,10 @@ mx_status mx_topk_router_bwd(const void* logits, int logits_type, const int32_t*
   if (st != MX_OK) return st;
   if (T == 0) return MX_OK;
   if (!logits || !expert_idx || !combine || !dcombine || !dlogits) return fail(MX_ERR_NULL, "%s: null pointer", fn);
-  if (!aligned(logits, 16) || !aligned(dlogits, 16) || !aligned(expert_idx, 4) || !aligned(combine, 4) ||
-      !aligned(dcombine, 4))
-    return fail(MX_ERR_ALIGN, "%s: logits and dlogits must be 16-byte, the other tensors 4-byte aligned", fn);
+  if (!row_aligned(logits, logits_type, E) || !row_aligned(dlogits, logits_type, E))
+    return fail(MX_ERR_ALIGN, "%s: logits and dlogits must be %s", fn, kRowAlign);
+  if (!aligned(expert_idx, 4) || !aligned(combine, 4) || !aligned(dcombine, 4))
+    return fail(MX_ERR_ALIGN, "%s: expert_idx, combine and dcombine must be 4-byte aligned", fn);
   mxk::RouterArgs a{};
   a.logits = logits;
   a.expert_idx = const_cast<int32_t*>(expert_idx);

@@ -389,3 +389,25 @@ def test_masked_experts_pass_no_gradient(score, renormalize, dtype):
     dw[4, 0] = float("nan")
     got = mx.mx_topk_router_bwd(x, ids, w, dw, score, renormalize)
     assert torch.isnan(got[4, ids[4, 0]]) and (got[4, 5:] == 0).all() and torch.equal(got[5:], want[5:])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_logits_of_a_slice_of_tokens(dtype):
+    """logits[t0:]: rows of any expert count, wherever they start, and a gradient written there."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    for E in (5, 20, 30, 37, 60, 130, 260, 1022):
+        whole = _dev(_logits(np.random.default_rng(E), 9, E, dtype), dtype)
+        dw = torch.randn((9, 3), device="cuda:0")
+        for score, renormalize in (("softmax", False), ("sigmoid", True)):
+            ids, w = mx.mx_topk_router_fwd(whole, 3, score, renormalize=renormalize)
+            dl = mx.mx_topk_router_bwd(whole, ids, w, dw, score, renormalize)
+            for t0 in (1, 2, 3, 7):
+                got = mx.mx_topk_router_fwd(whole[t0:], 3, score, renormalize=renormalize)
+                assert torch.equal(got[0], ids[t0:]) and torch.equal(got[1], w[t0:])
+                out = torch.zeros_like(whole)
+                mx.mx_topk_router_bwd(whole[t0:], *got, dw[t0:], score, renormalize, dlogits=out[t0:])
+                assert torch.equal(out[t0:], dl[t0:]) and not out[:t0].any()
+                leaf = whole[t0:].detach().requires_grad_()
+                again, w2 = mx.mx_topk_router(leaf, 3, score, renormalize=renormalize)
+                assert torch.equal(again, ids[t0:]) and torch.equal(torch.autograd.grad(w2, leaf, dw[t0:])[0], dl[t0:])

@@ -88,3 +88,13 @@ def test_scales_from_which_no_score_comes_back_are_refused():
         for call in record([("mx_topk_router_fwd", (P, BF16, P, 4, 32, 8, 0, 1, 1, 0, 1, scale, P, P, None)),
                             ("mx_topk_router_bwd", (P, BF16, P, P, P, 4, 32, 8, 0, 1, scale, P, None))]):
             assert call.status == status and bool(call.launches) == (status == 0), (scale, call.text)
+
+
+def test_rows_of_logits_may_start_at_any_token():
+    """logits[t0:] and a gradient there: four elements' alignment where rows are multiples of four, else one's."""
+    for kind, E, past, status in ((F32, 32, 16, 0), (F32, 32, 8, 3), (F32, 30, 4, 0), (F32, 30, 2, 3), (BF16, 32, 8, 0),
+                                  (BF16, 20, 8, 0), (BF16, 20, 4, 3), (BF16, 30, 2, 0), (BF16, 30, 1, 3)):
+        for call in record([("mx_topk_router_fwd", (P + past, kind, P, 4, E, 2, 0, 1, 1, 0, 1, 1.0, P, P, None)),
+                            ("mx_topk_router_bwd", (P + past, kind, P, P, P, 4, E, 2, 0, 1, 1.0, P, None)),
+                            ("mx_topk_router_bwd", (P, kind, P, P, P, 4, E, 2, 0, 1, 1.0, P + past, None))]):
+            assert call.status == status and bool(call.launches) == (status == 0), (kind, E, past, call.text)
