@@ -44,6 +44,12 @@ from . import (_combine_sizes, _format, _halves, _native, _on, _router_arguments
                mx_swiglu_quantize_bwd, mx_swiglu_quantize_fwd, mx_topk_combine_fwd, mx_topk_sum_rows)
 
 
+def _dense(t):
+    """t as the kernels read it: contiguous, at a multiple of 16 bytes; a copy where it is not."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class WeightCache:
     """Prequantized expert weights kept across micro-batches until the weights
     change: the weight cache of the "feat(moe): add MoK MXFP8 expert support"
@@ -373,7 +379,7 @@ def mx_topk_router(logits, k, score="softmax", bias=None, groups=1, topk_groups=
     """(expert_idx int32 [T, k], combine fp32 [T, k]) of the router's logits [T, E], differentiable in the
     logits (the package's mx_topk_router).  The bias takes part in the choice alone: it gets no gradient,
     and one that requires it is refused."""
-    logits = logits.contiguous()
+    logits = _dense(logits)
     if bias is not None and _wants_grad(bias):
         raise ValueError("mx_topk_router: the bias takes part in the choice of the experts alone and gets no "
                          "gradient: pass bias.detach()")
@@ -383,14 +389,14 @@ def mx_topk_router(logits, k, score="softmax", bias=None, groups=1, topk_groups=
 
 def mx_swiglu(gu):
     """silu(gate) * up with an MXFP8 checkpoint of gu for the backward (the package's mx_swiglu)."""
-    gu = gu.contiguous()
+    gu = _dense(gu)
     _halves(gu)
     return _native().swiglu(gu)
 
 
 def mx_topk_combine(y, combine, pos=None):
     """Weighted sum over a token's experts, differentiable in y and combine (the package's mx_topk_combine)."""
-    y, combine = y.contiguous(), combine.contiguous()
+    y, combine = _dense(y), combine.contiguous()
     _combine_sizes(y, combine, pos)
     return _native().topk_combine(y, combine, pos)
 
@@ -441,7 +447,7 @@ class _MXLayer:
                     dx = dcombine = dW13 = dW2 = None
                     # each item's gradient without its combine weight: the weight is in the columns of h
                     # (down weights) and enters the gradient of gu in the activation's backward
-                    qg, sg, qgt, sgt = mx_quantize_dual_gather(dout.contiguous(), rows, topk=topk, ldq=cap)
+                    qg, sg, qgt, sgt = mx_quantize_dual_gather(_dense(dout), rows, topk=topk, ldq=cap)
                     if need_2:
                         dW2 = mx_grouped_gemm_mx(qgt, sgt, qht, sht, offs, 1)
                     del qgt, sgt
@@ -519,7 +525,7 @@ def mx_moe_layer(x, expert_idx, combine, W13, W2, check: bool = True, weights=No
         offs, rows, pos, status = mx_route(expert_idx.contiguous().reshape(-1), E)
         if check and int(status.item()):
             raise ValueError(f"mx_moe_layer: an expert id lies outside [0, {E})")
-        x, W13, W2 = x.contiguous(), W13.contiguous(), W2.contiguous()
+        x, W13, W2 = _dense(x), _dense(W13), _dense(W2)
         mx13, mx2 = (_weights_for(W, w, cache, weight_format) for W, w in zip((W13, W2), weights or (None, None)))
         if _wants_grad(x, combine, W13, W2):
             return _MXLayer.get().apply(x, combine, W13, W2, offs, rows, pos, mx13, mx2, not check, weight_format)

@@ -82,12 +82,24 @@ void check_capture(const Tensor& t) {
               "be captured (drop the results of the eager calls first, or detach)");
 }
 
+// At an address that the kernels' wide loads take (views of a longer tensor may lie anywhere).
+bool wide(const Tensor& t) { return (uintptr_t)t.data_ptr() % 16 == 0; }
+// A gradient as the kernels read it.
+Tensor dense(const Tensor& t) {
+  const Tensor c = t.contiguous();
+  return wide(c) ? c : c.clone();
+}
+
 bool fits(const Tensor& t, at::ScalarType type, const Tensor& with) {
   return t.is_cuda() && t.scalar_type() == type && t.is_contiguous() && t.device() == with.device();
 }
 bool fits(const Maybe& t, at::ScalarType type, const Tensor& with) { return !t || fits(*t, type, with); }
 bool fits_either(const Tensor& t) {
   return t.is_cuda() && t.is_contiguous() && (t.scalar_type() == torch::kFloat || t.scalar_type() == torch::kBFloat16);
+}
+// Logits as the router reads them: four at a time, or one by one.
+bool starts_a_row(const Tensor& t) {
+  return (uintptr_t)t.data_ptr() % ((t.size(1) % 4 == 0 ? 4 : 1) * t.element_size()) == 0;
 }
 bool shaped(const Tensor& t, std::initializer_list<int64_t> shape) { return t.sizes() == at::IntArrayRef(shape); }
 
@@ -173,7 +185,7 @@ struct Swiglu : torch::autograd::Function<Swiglu> {
 
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
     const variable_list saved = ctx->get_saved_variables();
-    const Tensor d = grads[0].contiguous();
+    const Tensor d = dense(grads[0]);
     const int64_t M = d.size(0), N = d.size(1);
     Tensor dgu = torch::empty({M, 2 * N}, d.options());
     check_backward("mx_swiglu_bwd", mx_swiglu_bwd(bf16(d), ptr<uint8_t>(saved[0]), ptr<uint8_t>(saved[1]), M, N,
@@ -191,7 +203,7 @@ struct Combine : torch::autograd::Function<Combine> {
 
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
     const variable_list saved = ctx->get_saved_variables();
-    const Tensor &y = saved[0], &combine = saved[1], &pos = saved[2], d = grads[0].contiguous();
+    const Tensor &y = saved[0], &combine = saved[1], &pos = saved[2], d = dense(grads[0]);
     Tensor dy, dcombine;
     if (ctx->needs_input_grad(0)) dy = torch::empty_like(y);
     if (ctx->needs_input_grad(1)) dcombine = torch::empty_like(combine);
@@ -289,7 +301,7 @@ std::optional<Five> swiglu_quantize_bwd(const Tensor& dh, const Tensor& kept, co
 std::optional<std::pair<Tensor, Tensor>> topk_router(const Tensor& logits, int64_t k, int64_t score, const Maybe& bias,
                                                      int64_t groups, int64_t topk_groups, int64_t group_score,
                                                      bool renormalize, double scale) {
-  if (!fits_either(logits) || logits.dim() != 2 || k < 0 || k > MX_MOE_MAX_TOPK || score < 0 || group_score < 0)
+  if (!fits_either(logits) || logits.dim() != 2 || !starts_a_row(logits) || k < 0 || k > MX_MOE_MAX_TOPK || score < 0 || group_score < 0)
     return std::nullopt;
   if (bias && (!fits(bias, torch::kFloat, logits) || !shaped(*bias, {logits.size(1)}) ||
                wants_grad(*bias)))
@@ -302,7 +314,7 @@ std::optional<std::pair<Tensor, Tensor>> topk_router(const Tensor& logits, int64
 }
 
 Maybe swiglu(const Tensor& gu) {
-  if (!fits_halves(gu)) return std::nullopt;
+  if (!fits_halves(gu) || !wide(gu)) return std::nullopt;
   const c10::DeviceGuard on(gu.device());
   if (!wants_grad(gu)) return run_swiglu(gu, Tensor(), Tensor());
   check_capture(gu);
@@ -310,7 +322,7 @@ Maybe swiglu(const Tensor& gu) {
 }
 
 Maybe topk_combine(const Tensor& y, const Tensor& combine, const Maybe& pos) {
-  if (!fits_either(y) || y.dim() != 3 || !fits(combine, torch::kFloat, y) || !shaped(combine, {y.size(0), y.size(1)}) ||
+  if (!fits_either(y) || y.dim() != 3 || !wide(y) || !fits(combine, torch::kFloat, y) || !shaped(combine, {y.size(0), y.size(1)}) ||
       !fits(pos, torch::kInt, y) || (pos && pos->numel() != combine.numel()))
     return std::nullopt;
   const c10::DeviceGuard on(y.device());

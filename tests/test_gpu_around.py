@@ -272,3 +272,48 @@ def test_weighted_sum_past_2_31_elements():
     dy, dw = mx.mx_topk_combine_bwd(dout, y, w)
     want = mx.mx_topk_combine_bwd(dout[-3:].clone(), *tail)
     assert torch.equal(dy[-3:], want[0]) and torch.equal(dw[-3:], want[1])
+
+
+def _shifted(torch, t):
+    """t at an address one element past an aligned one."""
+    room = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    return room[1:].view(t.shape).copy_(t)
+
+
+def test_operands_and_gradients_at_any_address():
+    """Contiguous, but not where the kernels' wide loads could read them: a copy is made, as for strides."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    for op, inputs, d in _ops(mx, torch):
+        want = _step(torch, op, _leaves(inputs), d)
+        leaves = [_shifted(torch, t).requires_grad_() for t in inputs]
+        for got in (_step(torch, op, leaves, d), _step(torch, op, _leaves(inputs), _shifted(torch, d)),
+                    _step(torch, op, leaves, _shifted(torch, d))):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        with torch.no_grad():
+            assert torch.equal(op(*[_shifted(torch, t) for t in inputs]), want[0])
+    # as autograd hands them over: the gradient of a part of a longer tensor
+    gu = torch.randn((8, 192), device="cuda:0").bfloat16().requires_grad_()
+    tail = torch.randn(1, device="cuda:0").bfloat16()
+    d = torch.randn(8 * 96 + 1, device="cuda:0").bfloat16()
+    got, = torch.autograd.grad(torch.cat((tail, mx.mx_swiglu(gu).reshape(-1))), gu, d)
+    want, = torch.autograd.grad(mx.mx_swiglu(gu), gu, d[1:].clone().view(8, 96))
+    assert torch.equal(got, want)
+
+
+def test_layer_at_any_address():
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    g = torch.Generator(device="cuda:0").manual_seed(6)
+    rand = lambda *shape: torch.randn(shape, device="cuda:0", generator=g).bfloat16()  # noqa: E731
+    ids = torch.randint(3, (40, 2), device="cuda:0", dtype=torch.int32, generator=g)
+    w = torch.rand((40, 2), device="cuda:0", generator=g)
+    inputs, d = [rand(40, 128), w, rand(3, 256, 128) * 0.05, rand(3, 128, 128) * 0.05], rand(40, 128)
+    layer = lambda x, w, a, b: mx.mx_moe_layer(x, ids, w, a, b)  # noqa: E731
+    want = _step(torch, layer, _leaves(inputs), d)
+    for leaves, dout in (([_shifted(torch, t).requires_grad_() for t in inputs], d),
+                         (_leaves(inputs), _shifted(torch, d))):
+        got = _step(torch, layer, leaves, dout)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with torch.no_grad():
+        assert torch.equal(layer(*[_shifted(torch, t) for t in inputs]), want[0])
