@@ -90,6 +90,7 @@ class WeightCache:
 
 
 def _quantize_weights(W, weight_format):
+    W = _dense(W)
     return mx_quantize_weights_fp4(W) if weight_format == "mxfp4" else mx_quantize_weights(W)
 
 
@@ -203,7 +204,7 @@ class _MXGroupedMM:
                 @staticmethod
                 def backward(ctx, dOut):
                     offs, qWt, sWt, qAt, sAt = ctx.saved_tensors
-                    dOut = dOut.contiguous()
+                    dOut = _dense(dOut)
                     dA = dW = None
                     if ctx.needs_input_grad[1]:
                         # dOut in both orientations from one read: 1x32 along N
@@ -236,7 +237,7 @@ def mx_grouped_mm(A, W, offs, check_offsets: bool = True, weights=None, cache: W
         _check(A, W, offs, check_offsets)
         W = W.contiguous()
         mx4 = _weights_for(W, weights, cache, weight_format)
-        return _MXGroupedMM.get().apply(A.contiguous(), W, offs, mx4, weight_format)
+        return _MXGroupedMM.get().apply(_dense(A), W, offs, mx4, weight_format)
 
 
 def mx_linear(x, weight, weight_format: str = "mxfp8"):
@@ -297,7 +298,7 @@ class _MXRouted:
                 @staticmethod
                 def backward(ctx, dOut):
                     offs, rows, qWt, sWt, qAt, sAt = ctx.saved_tensors
-                    dOut = dOut.contiguous()
+                    dOut = _dense(dOut)
                     topk = ctx.topk
                     dx = dW = None
                     alloc = torch.zeros if ctx.zero_fill else torch.empty
@@ -365,7 +366,7 @@ def mx_routed_experts(x, expert_idx, W, check: bool = True, weights=None, cache:
                 raise ValueError(f"mx_routed_experts: an expert id lies outside [0, {E})")
         W = W.contiguous()
         mx4 = _weights_for(W, weights, cache, weight_format)
-        out = _MXRouted.get().apply(x.contiguous(), W, offs, rows, mx4, not check, topk, weight_format)
+        out = _MXRouted.get().apply(_dense(x), W, offs, rows, mx4, not check, topk, weight_format)
         return out if expert_idx.dim() == 1 else out.view(T, topk, N)
 
 
@@ -525,7 +526,7 @@ def mx_moe_layer(x, expert_idx, combine, W13, W2, check: bool = True, weights=No
         offs, rows, pos, status = mx_route(expert_idx.contiguous().reshape(-1), E)
         if check and int(status.item()):
             raise ValueError(f"mx_moe_layer: an expert id lies outside [0, {E})")
-        x, W13, W2 = _dense(x), _dense(W13), _dense(W2)
+        x, W13, W2 = _dense(x), W13.contiguous(), W2.contiguous()
         mx13, mx2 = (_weights_for(W, w, cache, weight_format) for W, w in zip((W13, W2), weights or (None, None)))
         if _wants_grad(x, combine, W13, W2):
             return _MXLayer.get().apply(x, combine, W13, W2, offs, rows, pos, mx13, mx2, not check, weight_format)

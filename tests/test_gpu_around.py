@@ -317,3 +317,29 @@ def test_layer_at_any_address():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     with torch.no_grad():
         assert torch.equal(layer(*[_shifted(torch, t) for t in inputs]), want[0])
+
+
+def test_products_at_any_address():
+    """The differentiable products take operands and gradients that are contiguous anywhere."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    g = torch.Generator(device="cuda:0").manual_seed(7)
+    rand = lambda *shape: torch.randn(shape, device="cuda:0", generator=g).bfloat16()  # noqa: E731
+    offs = torch.tensor([32, 96], dtype=torch.int32, device="cuda:0")
+    ids = torch.randint(2, (96, 2), device="cuda:0", dtype=torch.int32, generator=g)
+    for fmt in ("mxfp8", "mxfp4"):
+        for op, W, d in ((lambda x, W: mx.mx_grouped_mm(x, W, offs, weight_format=fmt), rand(2, 256, 128), rand(96, 256)),
+                         (lambda x, W: mx.mx_linear(x, W, weight_format=fmt), rand(256, 128), rand(96, 256)),
+                         (lambda x, W: mx.mx_routed_experts(x, ids[:, 0].contiguous(), W, weight_format=fmt),
+                          rand(2, 256, 128), rand(96, 256)),
+                         (lambda x, W: mx.mx_routed_experts(x, ids, W, weight_format=fmt), rand(2, 256, 128),
+                          rand(96, 2, 256))):
+            x = rand(96, 128)
+            want = _step(torch, op, _leaves([x, W]), d)
+            for leaves, dout in (([_shifted(torch, t).requires_grad_() for t in (x, W)], d),
+                                 (_leaves([x, W]), _shifted(torch, d)),
+                                 ([x.clone().requires_grad_(), W], _shifted(torch, d))):
+                needed = [t for t in leaves if t.requires_grad]
+                out = op(*leaves)
+                got = [out, *torch.autograd.grad(out, needed, dout)]
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
