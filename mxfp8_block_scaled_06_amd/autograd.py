@@ -528,7 +528,7 @@ def mx_moe_layer(x, expert_idx, combine, W13, W2, check: bool = True, weights=No
             raise ValueError(f"mx_moe_layer: an expert id lies outside [0, {E})")
         x, W13, W2 = _dense(x), W13.contiguous(), W2.contiguous()
         mx13, mx2 = (_weights_for(W, w, cache, weight_format) for W, w in zip((W13, W2), weights or (None, None)))
-        if _wants_grad(x, combine, W13, W2):
+        if any(map(_native().traced, (x, combine, W13, W2))):
             return _MXLayer.get().apply(x, combine, W13, W2, offs, rows, pos, mx13, mx2, not check, weight_format)
         gathered = torch.div(rows, topk, rounding_mode="floor") if topk > 1 else rows
         qx, sx = mx_quantize_rowwise_gather(x, gathered)

@@ -64,6 +64,9 @@ variable_list first_order(variable_list grads) {
 }
 
 bool wants_grad(const Tensor& t) { return at::GradMode::is_enabled() && t.requires_grad(); }
+// Whether a call needs a node: for a gradient, or for an operand with a tangent (forward mode),
+// which the nodes refuse.
+bool traced(const Tensor& t) { return wants_grad(t) || t._fw_grad(0).defined(); }
 
 // A leaf's gradient is accumulated on the stream on which the leaf first entered a
 // living graph.  Where that is not the stream being captured, a captured backward
@@ -307,7 +310,8 @@ std::optional<std::pair<Tensor, Tensor>> topk_router(const Tensor& logits, int64
                wants_grad(*bias)))
     return std::nullopt;
   const c10::DeviceGuard on(logits.device());
-  if (!wants_grad(logits)) return run_router(logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale);
+  if (!traced(logits) && !(bias && traced(*bias)))
+    return run_router(logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale);
   check_capture(logits);
   const variable_list out = Router::apply(logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale);
   return std::make_pair(out[0], out[1]);
@@ -316,7 +320,7 @@ std::optional<std::pair<Tensor, Tensor>> topk_router(const Tensor& logits, int64
 Maybe swiglu(const Tensor& gu) {
   if (!fits_halves(gu) || !wide(gu)) return std::nullopt;
   const c10::DeviceGuard on(gu.device());
-  if (!wants_grad(gu)) return run_swiglu(gu, Tensor(), Tensor());
+  if (!traced(gu)) return run_swiglu(gu, Tensor(), Tensor());
   check_capture(gu);
   return Swiglu::apply(gu);
 }
@@ -326,7 +330,7 @@ Maybe topk_combine(const Tensor& y, const Tensor& combine, const Maybe& pos) {
       !fits(pos, torch::kInt, y) || (pos && pos->numel() != combine.numel()))
     return std::nullopt;
   const c10::DeviceGuard on(y.device());
-  if (!wants_grad(y) && !wants_grad(combine)) return run_combine(y, combine, pos);
+  if (!traced(y) && !traced(combine)) return run_combine(y, combine, pos);
   check_capture(y);
   check_capture(combine);
   return Combine::apply(y, combine, pos);
@@ -350,6 +354,7 @@ PYBIND11_MODULE(_nodes, m) {
   m.def("swiglu", &swiglu, no_gil());
   m.def("topk_combine", &topk_combine, no_gil());
   m.def("check_capture", &check_capture, no_gil());
+  m.def("traced", &traced, no_gil());
   m.def("dequantize", &dequantize, no_gil());
   m.def("swiglu_quantize", &swiglu_quantize, no_gil());
   m.def("swiglu_quantize_fwd", &swiglu_quantize_fwd, no_gil());

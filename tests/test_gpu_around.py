@@ -343,3 +343,30 @@ def test_products_at_any_address():
                 out = op(*leaves)
                 got = [out, *torch.autograd.grad(out, needed, dout)]
                 assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_forward_mode_is_refused():
+    """No operator has a forward-mode derivative: operands with a tangent are refused, not taken for constants,
+    with gradients enabled and without."""
+    torch = require_gpu()
+    import torch.autograd.forward_ad as fwd
+    import mxfp8_block_scaled_06_amd as mx
+    x = torch.randn((20, 128), device="cuda:0").bfloat16()
+    W13 = torch.randn((2, 256, 128), device="cuda:0").bfloat16()
+    W2 = torch.randn((2, 128, 128), device="cuda:0").bfloat16()
+    ids = torch.randint(2, (20, 1), device="cuda:0", dtype=torch.int32)
+    w = torch.ones((20, 1), device="cuda:0")
+    l, bias = torch.randn((7, 24), device="cuda:0"), torch.randn(24, device="cuda:0")
+    ops = [(op, inputs) for op, inputs, _ in _ops(mx, torch)]
+    ops.append((lambda x, w, a, b: mx.mx_moe_layer(x, ids, w, a, b), [x, w, W13, W2]))
+    ops.append((lambda b: mx.mx_topk_router(l, 3, "sigmoid", b), [bias]))
+    for op, inputs in ops:
+        for i in range(len(inputs)):
+            for strided in (False, True):
+                with fwd.dual_level():
+                    args = [t.mT.contiguous().mT if strided and t.dim() > 1 else t for t in inputs]
+                    args[i] = fwd.make_dual(args[i], torch.ones_like(args[i]))
+                    for grad in (True, False):
+                        with torch.set_grad_enabled(grad), pytest.raises((RuntimeError, ValueError)):
+                            op(*args)
+        op(*inputs)                       # without one they are taken as ever
