@@ -375,12 +375,21 @@ def _wants_grad(*tensors):
     return torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
 
 
+def _copied(t):
+    """_dense(t) of an operand of the nodes.  A copy is no leaf, so that a leaf has to be looked at before it:
+    one whose eager graph lives is refused in a capture."""
+    if t.is_cuda:
+        with _on(t.device):
+            _native().check_capture(t)
+    return _dense(t)
+
+
 def mx_topk_router(logits, k, score="softmax", bias=None, groups=1, topk_groups=1, group_score="max",
                    renormalize=True, scale=1.0):
     """(expert_idx int32 [T, k], combine fp32 [T, k]) of the router's logits [T, E], differentiable in the
     logits (the package's mx_topk_router).  The bias takes part in the choice alone: it gets no gradient,
     and one that requires it is refused."""
-    logits = _dense(logits)
+    logits = _copied(logits)
     if bias is not None and _wants_grad(bias):
         raise ValueError("mx_topk_router: the bias takes part in the choice of the experts alone and gets no "
                          "gradient: pass bias.detach()")
@@ -390,14 +399,14 @@ def mx_topk_router(logits, k, score="softmax", bias=None, groups=1, topk_groups=
 
 def mx_swiglu(gu):
     """silu(gate) * up with an MXFP8 checkpoint of gu for the backward (the package's mx_swiglu)."""
-    gu = _dense(gu)
+    gu = _copied(gu)
     _halves(gu)
     return _native().swiglu(gu)
 
 
 def mx_topk_combine(y, combine, pos=None):
     """Weighted sum over a token's experts, differentiable in y and combine (the package's mx_topk_combine)."""
-    y, combine = _dense(y), combine.contiguous()
+    y, combine = _copied(y), _copied(combine)
     _combine_sizes(y, combine, pos)
     return _native().topk_combine(y, combine, pos)
 

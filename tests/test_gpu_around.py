@@ -370,3 +370,24 @@ def test_forward_mode_is_refused():
                         with torch.set_grad_enabled(grad), pytest.raises((RuntimeError, ValueError)):
                             op(*args)
         op(*inputs)                       # without one they are taken as ever
+
+
+def test_capture_of_a_copied_leaf_beside_its_eager_graph_is_refused():
+    """Strided and unaligned leaves, which reach the kernels as copies, are looked at before the copy."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    for op, inputs, d in _ops(mx, torch):
+        for make in (lambda t: t.transpose(0, -1).contiguous().transpose(0, -1), lambda t: _shifted(torch, t)):
+            leaves = [make(t).detach().requires_grad_() for t in inputs]
+            eager = op(*leaves)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                with pytest.raises(RuntimeError, match="graph of the same leaf"):
+                    op(*leaves)
+                with torch.no_grad():
+                    static = op(*leaves)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(static, eager.detach())
+            del eager
