@@ -300,3 +300,53 @@ def test_dequantizer(layout):
     a, b = mx.mx_dequantize(q, s), mx.mx_dequantize(q, sg, "gemm")
     want = oracle.dequant_rowwise(*oracle.quantize_rowwise(x.reshape(-1, 256))).reshape(x.shape)
     assert torch.equal(a, b) and np.array_equal(_f64(a), want)
+
+
+def test_replays_of_the_routed_activation():
+    """Two graphs with workspaces of their own, replayed in turn on new values: each replay's outputs, kept before
+    the buffers are filled with other bytes, are those of eager steps."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    rng = np.random.default_rng(8)
+    T, k, E, N = 50, 2, 3, 256
+    cap = mx.route_capacity(T * k, E)
+    _, rows, pos, _ = oracle.route_groups(_routing(rng, T, k, E).reshape(-1), E, cap)
+    rows, pos = to_dev_i32(rows), to_dev_i32(pos)
+    steps = []
+    for _ in range(2):
+        w = torch.rand((T, k), device="cuda:0")
+        gu = torch.randn((cap, 2 * N), device="cuda:0").bfloat16()
+        dh = torch.randn((cap, N), device="cuda:0").bfloat16()
+        ws = torch.empty(mx.mx_swiglu_quantize_workspace_bytes(cap, N), dtype=torch.uint8, device="cuda:0")
+        outs = [*mx.mx_swiglu_quantize_fwd(gu, rows, w)]
+        outs += mx.mx_swiglu_quantize_bwd(dh, outs[4], outs[5], rows, pos, w, ws=ws)
+
+        def step(gu=gu, dh=dh, ws=ws, w=w, outs=outs):
+            mx.mx_swiglu_quantize_fwd(gu, rows, w, None, *outs[:6])
+            mx.mx_swiglu_quantize_bwd(dh, outs[4], outs[5], rows, pos, w, None, *outs[6:], ws=ws)
+
+        def spoil(ws=ws, outs=outs):
+            for t in (ws, *outs):
+                t.fill_(77)
+
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        steps.append(((gu, dh, w), outs, step, spoil, graph))
+    before = None
+    for _ in range(3):
+        for inputs, _, _, spoil, _ in steps:
+            for t in inputs:
+                t.copy_(torch.randn(t.shape, device="cuda:0"))
+            spoil()
+        for *_, graph in steps:
+            graph.replay()
+        torch.cuda.synchronize()
+        kept = [[t.clone() for t in outs] for _, outs, *_ in steps]
+        assert before is None or not any(torch.equal(a[0], b[0]) for a, b in zip(kept, before))
+        before = kept
+        for (_, outs, step, spoil, _), got in zip(steps, kept):
+            spoil()
+            step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, outs))
