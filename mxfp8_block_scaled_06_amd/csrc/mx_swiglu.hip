@@ -33,9 +33,16 @@ constexpr int kThreads = 256;
 constexpr uint32_t kFarGate = 0x4280;       // bf16 bits of 64: below, sigmoid_near serves
 constexpr uint32_t kFarByte = 124;          // a block of this scale byte holds at most 448 * 2^-3 = 56
 
-// Conversions to E4M3 saturate from here on, to +-448 (bit 23 of the MODE register).
-// Called before the loads of what they convert, which keeps them behind it.
-__device__ __forceinline__ void saturate_conversions() { __builtin_amdgcn_s_setreg(1 | (23 << 6), 1); }
+// Conversions to E4M3 saturate from here on, to +-448 (bit 23 of the MODE register).  To the
+// compiler a conversion has nothing to do with that register: what keeps it behind the change
+// is the 0 returned here, whose value the compiler cannot know and which goes into the address
+// of what is converted.
+__device__ __forceinline__ int saturate_conversions() {
+  __builtin_amdgcn_s_setreg(1 | (23 << 6), 1);
+  int zero = 0;
+  asm volatile("" : "+s"(zero));
+  return zero;
+}
 
 // Scale bytes need the exponents of the largest magnitudes alone: two at a time, the
 // high halves of their fp32 bits packed in a dword.  A half from 0x7F80 on is not finite.
@@ -163,10 +170,10 @@ __global__ __launch_bounds__(kThreads) void swiglu_fwd_kernel(const uint16_t* __
                                                               uint8_t* __restrict__ kept, uint8_t* __restrict__ kept_s) {
   const int64_t i = wide_block() * kThreads + threadIdx.x;
   if (i >= chunks) return;
-  saturate_conversions();
+  const int zero = saturate_conversions();
   int64_t row, c;
   row_of(i, N / 8, row, c);
-  const uint16_t* src = gu + row * 2 * N + 8 * c;
+  const uint16_t* src = gu + zero + row * 2 * N + 8 * c;
   const v4i gw = __builtin_nontemporal_load((const v4i*)src);
   const v4i uw = __builtin_nontemporal_load((const v4i*)(src + N));
   float g[8], u[8], o[8];
@@ -362,7 +369,7 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4)
   const int tid = threadIdx.x, blk = 2 * p.wc + (p.cp >> 2);
   const int64_t n0 = (int64_t)blockIdx.y * kTileRows, k0 = (int64_t)blockIdx.x * kTileCols;
   const int64_t r0 = n0 + p.row, c0 = k0 + p.col;
-  saturate_conversions();
+  const int zero = saturate_conversions();
   int item[kLaneRows];
 #pragma unroll
   for (int i = 0; i < kLaneRows; ++i) item[i] = item_of(a, r0 + i);
@@ -371,7 +378,7 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4)
   for (int i = 0; i < kLaneRows; ++i) {
     gw[i] = uw[i] = (v4i){0, 0, 0, 0};
     if (item[i] >= 0) {
-      const uint16_t* src = a.gu + (r0 + i) * 2 * a.N + c0;
+      const uint16_t* src = a.gu + zero + (r0 + i) * 2 * a.N + c0;
       gw[i] = __builtin_nontemporal_load((const v4i*)src);
       uw[i] = __builtin_nontemporal_load((const v4i*)(src + a.N));
     }
@@ -453,7 +460,7 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4)
   const Tile tile;
   const int64_t n0 = (int64_t)tile.y * kTileRows, k0 = (int64_t)tile.x * kTileCols;
   const int64_t r0 = n0 + p.row, c0 = k0 + p.col;
-  saturate_conversions();
+  const int zero = saturate_conversions();
   int item[kLaneRows];
 #pragma unroll
   for (int i = 0; i < kLaneRows; ++i) item[i] = item_of(a, r0 + i);
@@ -468,7 +475,7 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4)
     gs[i] = us[i] = 0;
     if (item[i] >= 0) {
       // (streaming loads: 262 us instead of 245)
-      dw[i] = *(const v4i*)(a.dh + r * a.N + c0);
+      dw[i] = *(const v4i*)(a.dh + zero + r * a.N + c0);
       const uint8_t* src = a.kept + r * 2 * a.N + c0;
       gq[i] = *(const v2i*)src;
       uq[i] = *(const v2i*)(src + a.N);
