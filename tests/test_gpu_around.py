@@ -391,3 +391,39 @@ def test_capture_of_a_copied_leaf_beside_its_eager_graph_is_refused():
             torch.cuda.synchronize()
             assert torch.equal(static, eager.detach())
             del eager
+
+
+def test_captured_training_step_of_router_and_layer():
+    """The router and the layer captured together, forward and backward, with weights given; replayed on new tokens
+    and logits against eager steps between the replays."""
+    torch = require_gpu()
+    import mxfp8_block_scaled_06_amd as mx
+    g = torch.Generator(device="cuda:0").manual_seed(8)
+    rand = lambda *shape: torch.randn(shape, device="cuda:0", generator=g)  # noqa: E731
+    W13, W2 = ((rand(4, *shape) * 0.05).bfloat16() for shape in ((512, 256), (256, 256)))
+    d = rand(96, 256).bfloat16()
+    weights = mx.mx_quantize_weights(W13), mx.mx_quantize_weights(W2)
+
+    def layer(x, logits, W13, W2):
+        ids, w = mx.mx_topk_router(logits, 2)
+        return mx.mx_moe_layer(x, ids, w, W13, W2, check=False, weights=weights)
+
+    leaves = _leaves([rand(96, 256).bfloat16(), rand(96, 4), W13, W2])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _step(torch, layer, leaves, d)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        static = [t.detach() for t in _step(torch, layer, leaves, d)]
+    for _ in range(3):
+        with torch.no_grad():
+            for leaf in leaves[:2]:
+                leaf.copy_(rand(*leaf.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in static]
+        want = _step(torch, layer, _leaves([t.detach() for t in leaves]), d)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
