@@ -523,7 +523,8 @@ mx_status mx_moe_few_tokens(const uint16_t* x, const int32_t* expert_idx, const 
  *   combine [T, k]     scale * s[expert_idx], with renormalize != 0 over their sum
  * Equal values go to the lowest index.  The choice is that of c in 64 bits;
  * without a bias and without sums of two it is by the logits themselves, which
- * order the experts as their scores do.  combine is computed in fp32.
+ * order the experts as their scores do (-0 and +0 are equal).  combine is computed in
+ * fp32; a score below its normal range may count as 0.
  * A masked expert (logit minus infinity, or the lowest finite value of its type)
  * has the score 0, adds nothing to its group's value and comes behind every other
  * expert of the chosen groups, a group with none but such behind every other group; so does an
@@ -546,8 +547,10 @@ mx_status mx_topk_router_fwd(const void* logits, int logits_type, const float* b
  *   sigmoid             dl[e] = combine[e] (1 - s[e]) g[e]
  *   ... renormalized    dl[e] = combine[e] (1 - s[e]) (g[e] - sum_j g[j] p[j])
  * (e not chosen: g[e] and combine[e] 0).  The choice passes no gradient, nor
- * does the bias get one.  Masked experts get 0.  An id outside [0, E) adds
- * nothing. */
+ * does the bias get one.  Masked experts get 0, and the g of a slot whose weight is 0
+ * counts as 0 whatever it holds.  An id outside [0, E) adds nothing.  1 - s[e] is taken
+ * from the logit; without renormalization, where combine[e] is not that logit's score,
+ * it is 1 - p[e]. */
 mx_status mx_topk_router_bwd(const void* logits, int logits_type, const int32_t* expert_idx, const float* combine,
                              const float* dcombine, int64_t T, int64_t E, int64_t k, int score, int renormalize,
                              float scale, void* dlogits, void* stream);

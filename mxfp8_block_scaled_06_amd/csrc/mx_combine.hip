@@ -10,9 +10,9 @@
 // wave's load or store is one run of 1 KiB (fp32 at 32 bytes a lane wrote half lines:
 // 79 us instead of 62 for the backward below); the token's own row, which was just
 // written or is read next, goes through them.  T x k x N, forward and backward:
-//   8192 x 8 x 7168 bf16   173 us (6.1 TB/s)   337 us (5.9 TB/s)
+//   8192 x 8 x 7168 bf16   173 us (6.1 TB/s)   360 us (5.5 TB/s; over the same tensors again 337)
 //   16384 x 2 x 7168 bf16  104 us (6.8 TB/s)   170 us (6.9 TB/s)
-//   2047 x 4 x 5120 fp32    33 us (5.8 TB/s)    62 us (5.7 TB/s)
+//   2047 x 4 x 5120 fp32    31 us (5.5 TB/s)    61 us (5.5 TB/s)
 #include <type_traits>
 
 #include "mx_device.h"
@@ -87,9 +87,12 @@ __global__ __launch_bounds__(kThreads) void combine_fwd_kernel(const Y* __restri
 
 // One workgroup of W threads per token and S slots: all slots together up to eight, so
 // that dout is read once (4 a workgroup: 425 us instead of 373 for 8192 x 8 x 7168).
-// From three slots on 512 threads (8192 x 8 x 7168: 337 us, 353 with 256; 2047 x 4 x
+// From three slots on 512 threads (8192 x 8 x 7168: 337 us, 351 with 256; 2047 x 4 x
 // 5120 fp32: 62 and 65); a token with fewer is too short for them (16384 x 1 x 5120:
-// 82 us, 74 with 256).
+// 82 us, 74 with 256).  Short rows leave part of the 512 without a column and would be
+// faster with 256: at eight slots of bf16 and N = 512, 1024, 2048, 4096 it is 110 us for 59,
+// 118 for 87, 178 for 182 and 183 for 180 (T 16384, at 4096 8192), at four slots and N =
+// 1024, 2048 64 for 49 and 99 for 88; of fp32 at N = 512 111 for 87, level from 1024 on.
 template <class Y, int S, int W>
 __global__ __launch_bounds__(W) void combine_bwd_kernel(const Y* __restrict__ y, const float* __restrict__ combine,
                                                         const int32_t* __restrict__ pos,

@@ -253,10 +253,11 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const uint16_t* __
 //
 // 4 rows a lane instead of 8 hold both of the backward's gradients in fp32 in 128
 // registers, so that two workgroups share a CU and one computes while the other
-// waits for memory.  16896 x 8192 (0.14 G of h): forward 197 - 212 us (5.3 - 5.6 TB/s;
-// 327 with 8 rows a lane and conversions in steps), inference 113 us, backward 236 -
-// 264 us (447), where plain vector instructions fill three issue slots in five and
-// reciprocals, powers and conversions take several each.
+// waits for memory.  16896 x 8192 (0.14 G of h): forward 197 us (5.6 TB/s; 327 with 8 rows a
+// lane and conversions in steps), inference 117 us (5.8), backward 264 us (4.3; 447), where
+// plain vector instructions fill three issue slots in five and reciprocals, powers and
+// conversions take several each; its waves wait for memory or LDS in 42% of their cycles, for
+// a slot in 33%.  Over two sets of tensors in turn: 226, 125 and 226 us.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -282,8 +283,11 @@ struct ColCodes {
 
 // Where 16-byte slot s (16 rows) of a column lies.  Neighbouring groups of eight
 // columns take the halves of a 256-byte line in opposite order, and every second one
-// another slot: the writes of a wave (eight groups x eight lanes of 4 bytes) and the
-// reads (eight slots of eight columns) meet no bank twice.
+// another slot: a wave's writes (eight groups x eight lanes of 4 bytes) and reads (eight slots
+// of eight columns) are spread evenly over 64 banks.  The writes are not free of conflicts for
+// that: half a wave goes at a time, over 32 banks, where the two halves of a line coincide, and
+// each write takes four cycles, two of them counted as conflicts (most of the kernels'
+// count).  They are hidden: without these writes the kernels take as long.
 __device__ __forceinline__ int code_at(int col, int s) {
   return (col ^ (col >> 3 & 1)) * kTileRows + 16 * (s ^ (2 * (col >> 4 & 3)));
 }
